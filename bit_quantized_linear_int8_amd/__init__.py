@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libqa.so")
 QA_F32, QA_F16, QA_BF16 = 0, 1, 2
 QA_SCALE_PER_ROW, QA_SCALE_PER_GROUP, QA_SCALE_PER_TENSOR = 0, 1, 2
 QA_SMOOTH_DIVIDE, QA_SMOOTH_MULTIPLY = 0, 1
+QA_SCORE_SOFTMAX, QA_SCORE_SIGMOID = 0, 1
 
 EXPORTS = (
     "qa_status_string", "qa_last_error",
@@ -37,6 +38,8 @@ EXPORTS = (
     "qa_hadamard_quant_int8", "qa_qlinear_w4a8_workspace", "qa_qlinear_w4a8",
     "qa_hadamard_quant_int4_asym", "qa_w4_column_terms", "qa_qlinear_w4a4_asym_workspace", "qa_qlinear_w4a4_asym",
     "qa_gemm_i8_i32", "qa_gemm_w4a4_group_acc", "qa_gemm_w4a8_group_acc",
+    "qa_rmsnorm_int8", "qa_route_experts_workspace", "qa_route_experts", "qa_experts_int8_workspace",
+    "qa_experts_int8", "qa_qlinear_int8_lora_workspace", "qa_qlinear_int8_lora",
     "qa_probe_stream_read",
 )
 
@@ -102,6 +105,14 @@ def lib() -> ctypes.CDLL:
             "qa_w4_column_terms": (S, [P, P, I64, I64, I32, P, P]),
             "qa_qlinear_w4a4_asym_workspace": (SZ, [I64, I64]),
             "qa_qlinear_w4a4_asym": (S, [P, I64, I64, P, P, P, I64, I32, P, S, P, SZ, P]),
+            "qa_rmsnorm_int8": (S, [P, I64, P, I64, P, S, I64, I64, F, P, P, P, I64, P, P]),
+            "qa_route_experts_workspace": (SZ, [I64, I64, I32]),
+            "qa_route_experts": (S, [P, S, I64, I64, I64, P, S, I32, I32, I32, I32, I32, F, P, P, P, P, P, SZ, P]),
+            "qa_experts_int8_workspace": (SZ, [I64, I64, I32, I64, I64]),
+            "qa_experts_int8": (S, [P, P, I64, I64, P, P, P, I64, I32, P, P, I64, P, P, P, S, P, SZ, P]),
+            "qa_qlinear_int8_lora_workspace": (SZ, [I64, I64, I32]),
+            "qa_qlinear_int8_lora": (S, [P, P, P, S, I64, I64, P, P, I64, P, P, P, I32, I64, P, P, I64, P, S, P, SZ,
+                                         P]),
             "qa_probe_stream_read": (S, [P, SZ, I32, I32, I32, P, P]),
         }
         for name, (res, args) in sig.items():
@@ -595,6 +606,174 @@ def qa_gemm_w4a8_group_acc(Xq, Wp, G: int, stream=None):
     _check("qa_gemm_w4a8_group_acc",
            lib().qa_gemm_w4a8_group_acc(_p(Xq), _p(Wp), M, K, N, int(G), _p(acc), _stream(stream)))
     return acc
+
+
+def _rows(t, name, dtype):
+    """A [rows x columns] tensor whose rows are contiguous -> its row stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be a matrix with contiguous rows" % name)
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+
+
+def qa_rmsnorm_int8(X, g, residual=None, eps=1e-6, want_y=False, total=None, stream=None):
+    """Residual addition + RMS norm + int8 codes per row.
+
+    X [rows x K] fp32 / fp16 / bf16 (rows may be strided), g [K] and residual
+    of the same type -> (Xq i8 [rows x K], s f32 [rows], total or None, y or
+    None): total = X + residual (with a residual; into the given `total`,
+    which may be X or residual itself), y the norm in X's type if wanted."""
+    if X.dtype not in _DTYPE_CODE:
+        raise TypeError("X must be fp32, fp16 or bf16, got %s" % X.dtype)
+    ldx = _rows(X, "X", X.dtype)
+    rows, K = X.shape
+    _dev(g, "g", X.dtype)
+    _shape(g, "g", (K,))
+    ldr = lds = K
+    if residual is not None:
+        ldr = _rows(residual, "residual", X.dtype)
+        _shape(residual, "residual", (rows, K))
+        if total is None:
+            total = _empty(stream, (rows, K), dtype=X.dtype, device=X.device)
+    if total is not None:
+        lds = _rows(total, "total", X.dtype)
+        _shape(total, "total", (rows, K))
+    Xq = _empty(stream, (rows, K), dtype=torch.int8, device=X.device)
+    s = _empty(stream, rows, dtype=torch.float32, device=X.device)
+    y = _empty(stream, (rows, K), dtype=X.dtype, device=X.device) if want_y else None
+    _check("qa_rmsnorm_int8",
+           lib().qa_rmsnorm_int8(_p(X), ldx, _p(residual), ldr, _p(g), _DTYPE_CODE[X.dtype], rows, K, float(eps),
+                                 _p(Xq), _p(s), _p(total), lds, _p(y), _stream(stream)))
+    return Xq, s, total, y
+
+
+def qa_route_experts_workspace(T: int, E: int, k: int) -> int:
+    return int(lib().qa_route_experts_workspace(T, E, k))
+
+
+def qa_route_experts(logits, k: int, bias=None, score=QA_SCORE_SOFTMAX, groups=1, top_groups=1, group_top=1,
+                     renorm=True, scale=1.0, workspace=None, stream=None):
+    """The k experts of each token -> (ids i32 [T x k], weights f32 [T x k], order i32 [T k], offsets i32 [E + 1]):
+    the chosen experts in descending order of score + bias, their weights, and the pairs t k + j by expert."""
+    if logits.dtype not in _DTYPE_CODE:
+        raise TypeError("logits must be fp32, fp16 or bf16, got %s" % logits.dtype)
+    ld = _rows(logits, "logits", logits.dtype)
+    T, E = logits.shape
+    k = int(k)
+    if bias is not None:
+        _dev(bias, "bias", torch.float32)
+        _shape(bias, "bias", (E,))
+    d = logits.device
+    n = max(k, 0)
+    ids = _empty(stream, (T, n), dtype=torch.int32, device=d)
+    w = _empty(stream, (T, n), dtype=torch.float32, device=d)
+    order = _empty(stream, T * n, dtype=torch.int32, device=d)
+    offsets = _empty(stream, E + 1, dtype=torch.int32, device=d)
+    workspace = _workspace(stream, qa_route_experts_workspace(T, E, k), d, workspace)
+    _check("qa_route_experts",
+           lib().qa_route_experts(_p(logits), _DTYPE_CODE[logits.dtype], T, E, ld, _p(bias), int(score), int(groups),
+                                  int(top_groups), int(group_top), k, int(bool(renorm)), float(scale), _p(ids), _p(w),
+                                  _p(order), _p(offsets), _p(workspace), workspace.numel(), _stream(stream)))
+    return ids, w, order, offsets
+
+
+def qa_experts_int8_workspace(T: int, K: int, k: int, E: int, F: int) -> int:
+    return int(lib().qa_experts_int8_workspace(T, K, k, E, F))
+
+
+def qa_experts_int8(Xq, s_x, weights, order, offsets, W13, s13, W2, s2, out_dtype=torch.float16, out=None,
+                    workspace=None, stream=None):
+    """Gated feed-forward of the routed experts on int8 codes -> out [T x K] of out_dtype.
+
+    Xq i8 [T x K], s_x f32 [T]; weights f32 [T x k], order, offsets from
+    qa_route_experts; W13 i8 [E x 2F x K] (gate rows, then up rows), s13 f32
+    [E x 2F]; W2 i8 [E x K x F], s2 f32 [E x K]."""
+    _dev(Xq, "Xq", torch.int8)
+    _dev(s_x, "s_x", torch.float32)
+    _dev(weights, "weights", torch.float32)
+    _dev(order, "order", torch.int32)
+    _dev(offsets, "offsets", torch.int32)
+    _dev(W13, "W13", torch.int8)
+    _dev(s13, "s13", torch.float32)
+    _dev(W2, "W2", torch.int8)
+    _dev(s2, "s2", torch.float32)
+    T, K = Xq.shape
+    E, F = W13.shape[0], W2.shape[2]
+    k = weights.shape[1]
+    _shape(s_x, "s_x", (T,))
+    _shape(weights, "weights", (T, k))
+    _shape(order, "order", (T * k,))
+    _shape(offsets, "offsets", (E + 1,))
+    _shape(W13, "W13", (E, 2 * F, K))
+    _shape(s13, "s13", (E, 2 * F))
+    _shape(W2, "W2", (E, K, F))
+    _shape(s2, "s2", (E, K))
+    if out is None:
+        out = _empty(stream, (T, K), dtype=out_dtype, device=Xq.device)
+    _dev(out, "out")
+    _shape(out, "out", (T, K))
+    workspace = _workspace(stream, qa_experts_int8_workspace(T, K, k, E, F), Xq.device, workspace)
+    _check("qa_experts_int8",
+           lib().qa_experts_int8(_p(Xq), _p(s_x), T, K, _p(weights), _p(order), _p(offsets), E, k, _p(W13), _p(s13), F,
+                                 _p(W2), _p(s2), _p(out), _DTYPE_CODE[out.dtype], _p(workspace), workspace.numel(),
+                                 _stream(stream)))
+    return out
+
+
+def qa_qlinear_int8_lora_workspace(M: int, K: int, r: int) -> int:
+    return int(lib().qa_qlinear_int8_lora_workspace(M, K, r))
+
+
+def qa_qlinear_int8_lora(Xq, s_x, X, Wq, s_w, A, B, alpha, seg, which, out_dtype=torch.float16, out=None,
+                         workspace=None, stream=None):
+    """int8 linear with each request's low-rank adapter -> out [M x N] of out_dtype.
+
+    Xq i8 [M x K], s_x f32 [M], X fp16 / bf16 [M x K]; Wq i8 [N x K], s_w f32
+    [N]; A [L x r x K], B [L x N x r] of X's type, alpha f32 [L]; seg i32
+    [R + 1] token starts of the requests, which i32 [R] their adapters (-1:
+    none)."""
+    _dev(Xq, "Xq", torch.int8)
+    _dev(s_x, "s_x", torch.float32)
+    if X.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("X must be fp16 or bf16, got %s" % X.dtype)
+    _dev(X, "X", X.dtype)
+    _dev(Wq, "Wq", torch.int8)
+    _dev(s_w, "s_w", torch.float32)
+    _dev(A, "A", X.dtype)
+    _dev(B, "B", X.dtype)
+    _dev(alpha, "alpha", torch.float32)
+    _dev(seg, "seg", torch.int32)
+    _dev(which, "which", torch.int32)
+    M, K = Xq.shape
+    N = Wq.shape[0]
+    L, r = A.shape[0], A.shape[1]
+    R = which.numel()
+    _shape(s_x, "s_x", (M,))
+    _shape(X, "X", (M, K))
+    _shape(Wq, "Wq", (N, K))
+    _shape(s_w, "s_w", (N,))
+    _shape(A, "A", (L, r, K))
+    _shape(B, "B", (L, N, r))
+    _shape(alpha, "alpha", (L,))
+    _shape(seg, "seg", (R + 1,))
+    if out is None:
+        out = _empty(stream, (M, N), dtype=out_dtype, device=Xq.device)
+    _dev(out, "out")
+    _shape(out, "out", (M, N))
+    workspace = _workspace(stream, qa_qlinear_int8_lora_workspace(M, K, r), Xq.device, workspace)
+    _check("qa_qlinear_int8_lora",
+           lib().qa_qlinear_int8_lora(_p(Xq), _p(s_x), _p(X), _DTYPE_CODE[X.dtype], M, K, _p(Wq), _p(s_w), N, _p(A),
+                                      _p(B), _p(alpha), r, L, _p(seg), _p(which), R, _p(out), _DTYPE_CODE[out.dtype],
+                                      _p(workspace), workspace.numel(), _stream(stream)))
+    return out
 
 
 def qa_probe_stream_read(src, nbytes: int, wgs: int, lane_bytes: int = 16, unroll: int = 4, sink=None, stream=None):

@@ -1,0 +1,409 @@
+// k_experts.hip -- the gated feed-forward of the experts a token was routed to,
+// on int8 MFMA (gfx950).
+//
+//   g, u   = s_x[t] s13[e][.] (Xq[t] W13[e]^T)          gate rows 0..F-1, up rows F..2F-1
+//   h      = g / (1 + exp(-g)) * u                      (fp32)
+//   s_h    = max|h| / 127 (1 where that is 0), hq = rint(h / s_h)
+//   y      = s_h s2[e][.] (hq W2[e]^T)                  (fp32)
+//   out[t] = sum_j w[t][j] y[pair t k + j]              (j ascending, fp32)
+//
+// Rows are the dispatched pairs in expert order ("slots"): offsets[e] ..
+// offsets[e + 1] are expert e's, order[slot] names the pair t k + j.
+//
+// Four launches: the gate and up product (its tile takes 16 gate and 16 up
+// columns in turn, so one lane holds both factors of an h), the codes of h, the
+// down product, and the sum per token.  h and y pass through memory in fp32: the
+// scale of an h row needs the whole row, and fp16 there would move about 1% of
+// the codes.
+//
+// Few rows per expert: the weights are the traffic, so k_experts_stream reads
+// each weight byte once per 16 MT rows, straight into MFMA operands, K split
+// over the block's waves.  Many rows: k_experts_tile on LDS tiles.
+#include "qa_tile.hpp"
+#include "qa_launch.hpp"
+
+namespace qa {
+
+namespace {
+
+struct ExpertArgs {
+    const int8_t* A;          // codes: Xq [T x K] (gated) or hq [slots x F]
+    const float* sa;          // scale per token or per slot
+    const int8_t* W;          // [E x rows x Kc]
+    const float* sw;          // [E x rows]
+    const int32_t* order;     // [P]
+    const int32_t* offsets;   // [E + 1]
+    const int32_t* tiles;     // (expert, first row) per row tile, and the number of tiles before them
+    int32_t* inv;             // [P] slot of a pair
+    float* out;               // h [slots x F] or y [slots x K]
+    int64_t T, P;
+    int32_t E, k;
+    int64_t Kc;               // bytes of the contraction
+    int64_t N;                // output columns (gated: F)
+};
+
+// Expert e's slots, held within [0, P] whatever the offsets say.
+__device__ __forceinline__ void slots_of(const ExpertArgs& a, int e, int64_t& s0, int64_t& n) {
+    int64_t b = a.offsets[e], c = a.offsets[e + 1];
+    b = b < 0 ? 0 : (b > a.P ? a.P : b);
+    c = c < b ? b : (c > a.P ? a.P : c);
+    s0 = b;
+    n = c - b;
+}
+
+// Row of A that a slot reads (gated: its token), or -1.
+template <bool GATED>
+__device__ __forceinline__ int64_t row_of(const ExpertArgs& a, int64_t slot) {
+    if constexpr (!GATED) return slot;
+    const int p = a.order[slot];
+    return p < 0 || p >= a.P ? -1 : p / a.k;
+}
+
+__device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Few rows: block (n, e) computes 32 weight rows of expert e (16 gate and the
+// same 16 up columns, or 32 columns) for all its slots, 16 MT at a time.
+// ---------------------------------------------------------------------------
+template <int MT, bool GATED>
+__global__ __launch_bounds__(256) void k_experts_stream(ExpertArgs a) {
+    __shared__ v4i part[4][MT][2][64];
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    if (GATED) {
+        const int64_t stride = (int64_t)gridDim.x * gridDim.y * 256;
+        for (int64_t p = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x; p < a.P; p += stride)
+            a.inv[p] = -1;
+    }
+    const int e = blockIdx.y;
+    int64_t s0, n;
+    slots_of(a, e, s0, n);
+    if (n == 0) return;
+    const int64_t n0 = (int64_t)blockIdx.x * (GATED ? 16 : 32);
+    const int64_t wrows = GATED ? 2 * a.N : a.N;
+    const rsrc_t rw = make_rsrc(a.W + (int64_t)e * wrows * a.Kc, wrows * a.Kc);
+    const int r16 = lane & 15, c16 = (lane >> 4) * 16;
+    const int64_t c0 = n0 + r16, c1 = GATED ? c0 : c0 + 16;  // output columns of this lane's weight rows
+    const uint32_t o0 = c0 < a.N ? (uint32_t)(c0 * a.Kc) : kOOB;
+    const uint32_t o1 = c1 < a.N ? (uint32_t)((GATED ? a.N + c1 : c1) * a.Kc) : kOOB;
+    const uint32_t Kc = (uint32_t)a.Kc;
+    const int nk = (int)((Kc + 63) / 64);
+    for (int64_t m0 = 0; m0 < n; m0 += 16 * MT) {
+        const int8_t* A = GATED ? a.A : a.A + (s0 + m0) * a.Kc;
+        const rsrc_t ra = make_rsrc(A, GATED ? a.T * a.Kc : (n - m0) * a.Kc);
+        uint32_t oa[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int64_t s = m0 + m * 16 + r16;
+            const int64_t row = s < n ? (GATED ? row_of<true>(a, s0 + s) : s - m0) : -1;
+            oa[m] = row < 0 ? kOOB : (uint32_t)(row * a.Kc);
+        }
+        v4i acc[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = v4i{0, 0, 0, 0};
+        constexpr int U = 4;
+        for (int s = wave; s < nk; s += 4 * U) {
+            u32x4 w0[U], w1[U], x[U][MT];
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                const uint32_t kb = (uint32_t)(s + 4 * q) * 64 + c16;
+                const bool in = kb < Kc;
+                w0[q] = bload16(rw, in ? o0 + kb : kOOB);
+                w1[q] = bload16(rw, in ? o1 + kb : kOOB);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) x[q][m] = bload16(ra, in ? oa[m] + kb : kOOB);
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const v4i xv = __builtin_bit_cast(v4i, x[q][m]);
+                    acc[m][0] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, w0[q]), xv, acc[m][0], 0, 0, 0);
+                    acc[m][1] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, w1[q]), xv, acc[m][1], 0, 0, 0);
+                }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            part[wave][m][0][lane] = acc[m][0];
+            part[wave][m][1][lane] = acc[m][1];
+        }
+        __syncthreads();
+        for (int it = threadIdx.x; it < MT * (GATED ? 64 : 128); it += 256) {
+            const int m = GATED ? it >> 6 : it >> 7, f = GATED ? 0 : (it >> 6) & 1, ln = it & 63;
+            const int64_t s = m0 + m * 16 + (ln & 15);
+            const int64_t col = n0 + f * 16 + 4 * (ln >> 4);
+            if (s < n && col < a.N) {                        // N % 16 == 0: four columns exist together
+                const int64_t row = row_of<GATED>(a, s0 + s);
+                const float sx = row < 0 ? 0.0f : a.sa[row];
+                v4i g = part[0][m][f][ln];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) g += part[w][m][f][ln];
+                v4f o;
+                if constexpr (GATED) {
+                    v4i u = part[0][m][1][ln];
+#pragma unroll
+                    for (int w = 1; w < 4; ++w) u += part[w][m][1][ln];
+                    const float* sg = a.sw + (int64_t)e * wrows + col;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        o[q] = gated((float)g[q] * sx * sg[q], (float)u[q] * sx * sg[a.N + q]);
+                } else {
+                    const float* sg = a.sw + (int64_t)e * wrows + col;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) o[q] = (float)g[q] * sx * sg[q];
+                }
+                *reinterpret_cast<v4f*>(a.out + (s0 + s) * a.N + col) = o;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows.  tiles[0] = number of row tiles, then (expert, first row) each.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(1024) void k_experts_plan(ExpertArgs a, int32_t* __restrict__ tiles, int32_t bm,
+                                                       int32_t most) {
+    __shared__ int32_t pre[1024];
+    const int e = threadIdx.x;
+    for (int64_t p = (int64_t)blockIdx.x * 1024 + e; p < a.P; p += (int64_t)gridDim.x * 1024) a.inv[p] = -1;
+    if (blockIdx.x != 0) return;
+    int64_t s0 = 0, n = 0;
+    if (e < a.E) slots_of(a, e, s0, n);
+    const int mine = (int)((n + bm - 1) / bm);
+    pre[e] = mine;
+    __syncthreads();
+    for (int o = 1; o < 1024; o <<= 1) {
+        const int v = e >= o ? pre[e - o] : 0;
+        __syncthreads();
+        pre[e] += v;
+        __syncthreads();
+    }
+    // `most` tiles cover every set of disjoint ranges; overlapping ones (which
+    // the caller must not pass) are cut off there
+    if (e == 1023) tiles[0] = min(pre[1023], most);
+    const int at = pre[e] - mine;
+    for (int i = 0; i < mine && at + i < most; ++i) {
+        tiles[2 + 2 * (at + i)] = e;
+        tiles[3 + 2 * (at + i)] = i * bm;
+    }
+}
+
+template <class C, bool GATED>
+__global__ __launch_bounds__(C::THREADS) void k_experts_tile(ExpertArgs a, int32_t tiles_n) {
+    extern __shared__ uint8_t smem[];
+    const int ntiles = a.tiles[0] * tiles_n;
+    // Blocks go round-robin over the 8 XCDs: XCD x walks a contiguous range of
+    // tiles, a row tile's columns in turn, so that its rows stay in that L2.
+    const int per = (ntiles + 7) >> 3;
+    const int slot8 = (int)(blockIdx.x >> 3);
+    const int id = (int)(blockIdx.x & 7) * per + slot8;
+    if (slot8 >= per || id >= ntiles) return;
+    const int tm = id / tiles_n, tn = id % tiles_n;
+    const int e = a.tiles[2 + 2 * tm];
+    const int64_t m0 = a.tiles[3 + 2 * tm];
+    int64_t s0, n;
+    slots_of(a, e, s0, n);
+    constexpr int NC = GATED ? C::BN / 2 : C::BN;            // output columns of the tile
+    const int64_t n0 = (int64_t)tn * NC;
+    const int64_t wrows = GATED ? 2 * a.N : a.N;
+    const int8_t* A = GATED ? a.A : a.A + (s0 + m0) * a.Kc;
+    const rsrc_t ra = make_rsrc(A, GATED ? a.T * a.Kc : (n - m0) * a.Kc);
+    const rsrc_t rw = make_rsrc(a.W + (int64_t)e * wrows * a.Kc, wrows * a.Kc);
+    v4i acc[C::FM][C::FN];
+    tile::product<C>(
+        ra, rw, (uint32_t)a.Kc, smem,
+        [&](int r) -> uint32_t {
+            if (m0 + r >= n) return kOOB;
+            const int64_t row = GATED ? row_of<true>(a, s0 + m0 + r) : r;
+            return row < 0 ? kOOB : (uint32_t)(row * a.Kc);
+        },
+        [&](int r) -> uint32_t {
+            // gated: fragments of 16 gate rows and of the same 16 up rows in turn
+            const int64_t col = GATED ? n0 + (r >> 5) * 16 + (r & 15) : n0 + r;
+            if (col >= a.N) return kOOB;
+            return (uint32_t)(((GATED && (r & 16) ? a.N : 0) + col) * a.Kc);
+        },
+        acc);
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const float* sw = a.sw + (int64_t)e * wrows;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+        const int64_t s = m0 + wm * C::TM + i * 16 + (lane & 15);
+        if (s >= n) continue;
+        const int64_t row = row_of<GATED>(a, s0 + s);
+        const float sx = row < 0 ? 0.0f : a.sa[row];
+        float* o = a.out + (s0 + s) * a.N;
+#pragma unroll
+        for (int j = 0; j < C::FN; j += GATED ? 2 : 1) {
+            const int64_t col = n0 + (GATED ? (wn * C::TN + j * 16) / 2 : wn * C::TN + j * 16) + 4 * (lane >> 4);
+            if (col >= a.N) continue;
+            const v4f sg = *reinterpret_cast<const v4f*>(sw + col);
+            v4f v;
+            if constexpr (GATED) {
+                const v4f su = *reinterpret_cast<const v4f*>(sw + a.N + col);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    v[q] = gated((float)acc[i][j][q] * sx * sg[q], (float)acc[i][j + 1][q] * sx * su[q]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = (float)acc[i][j][q] * sx * sg[q];
+            }
+            *reinterpret_cast<v4f*>(o + col) = v;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Codes of h: one block per slot, the row read twice (the second time from the
+// caches).  Also the slot of each pair, for the sum.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void k_experts_codes(const float* __restrict__ h, const int32_t* __restrict__ order,
+                                                       const int32_t* __restrict__ offsets, int32_t E, int64_t P,
+                                                       int64_t F, int8_t* __restrict__ q, float* __restrict__ s_h,
+                                                       int32_t* __restrict__ inv) {
+    __shared__ float red[4];
+    const int64_t slot = blockIdx.x;
+    if (slot >= offsets[E]) return;
+    const float* x = h + slot * F;
+    float amax = 0.0f;
+    bool nan = false;
+    for (int64_t c = threadIdx.x * 4; c < F; c += 1024) {
+        const v4f v = *reinterpret_cast<const v4f*>(x + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            amax = fmaxf(amax, __builtin_fabsf(v[j]));
+            nan |= v[j] != v[j];
+        }
+    }
+    if (nan) amax = __builtin_inff();
+    amax = wave_max(amax);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
+    __syncthreads();
+    amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const bool fine = amax < __builtin_inff();
+    float s = amax / 127.0f;
+    if (s == 0.0f) s = 1.0f;
+    if (!fine) s = __builtin_nanf("");
+    if (threadIdx.x == 0) {
+        s_h[slot] = s;
+        const int p = order[slot];
+        if (p >= 0 && p < P) inv[p] = (int32_t)slot;
+    }
+    for (int64_t c = threadIdx.x * 4; c < F; c += 1024) {
+        const v4f v = *reinterpret_cast<const v4f*>(x + c);
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w |= (fine ? (uint32_t)(int)__builtin_rintf(v[j] / s) & 0xffu : 0u) << (8 * j);
+        *reinterpret_cast<uint32_t*>(q + slot * F + c) = w;
+    }
+}
+
+// out[t] = sum_j w[t][j] y[slot of pair t k + j]; pairs without a slot add nothing.
+template <int DT>
+__global__ __launch_bounds__(256) void k_experts_sum(const float* __restrict__ y, const float* __restrict__ w,
+                                                     const int32_t* __restrict__ inv, int32_t k, int64_t K,
+                                                     void* __restrict__ out) {
+    const int64_t t = blockIdx.x;
+    const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
+    if (c >= K) return;
+    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < k; ++j) {
+        const int s = inv[t * k + j];
+        if (s < 0) continue;
+        const float wt = w[t * k + j];
+        const v4f v = *reinterpret_cast<const v4f*>(y + (int64_t)s * K + c);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = __builtin_fmaf(wt, v[q], o[q]);
+    }
+    store4(out, t * K + c, DT, o, 4, true);
+}
+
+namespace {
+constexpr size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+struct ExpertLayout { size_t mid, hq, s_h, inv, tiles, total; };
+ExpertLayout expert_layout(int64_t P, int64_t K, int64_t E, int64_t F) {
+    ExpertLayout L;
+    size_t off = 0;
+    L.mid = off; off += up256((size_t)P * (size_t)(K > F ? K : F) * 4);      // h, then y
+    L.hq = off; off += up256((size_t)P * (size_t)F);
+    L.s_h = off; off += up256((size_t)P * 4);
+    L.inv = off; off += up256((size_t)P * 4);
+    L.tiles = off; off += up256((size_t)(2 + 2 * (P / 16 + E + 1)) * 4);
+    L.total = off;
+    return L;
+}
+}  // namespace
+
+size_t experts_scratch_bytes(int64_t P, int64_t K, int64_t E, int64_t F) { return expert_layout(P, K, E, F).total; }
+
+// Upper bound of the row tiles: the whole ones and one ragged one per expert.
+template <class C>
+static int64_t most_tiles(const ExpertArgs& a) { return a.P / C::BM + (a.E < a.P ? a.E : a.P); }
+
+template <class C, bool GATED>
+static hipError_t run_tile(const ExpertArgs& a, hipStream_t st) {
+    static const hipError_t once = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_experts_tile<C, GATED>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+    if (once != hipSuccess) return once;
+    const int64_t nc = GATED ? C::BN / 2 : C::BN;
+    const int64_t tn = (a.N + nc - 1) / nc;
+    const int64_t tm = most_tiles<C>(a);
+    const int64_t blocks = ((tm * tn + 7) / 8) * 8;
+    hipLaunchKernelGGL((k_experts_tile<C, GATED>), dim3((unsigned)blocks), dim3(C::THREADS), C::LDS, st, a, (int32_t)tn);
+    return hipGetLastError();
+}
+
+template <bool GATED>
+static hipError_t run_stream(const ExpertArgs& a, int mt, hipStream_t st) {
+    const dim3 grid((unsigned)((a.N + (GATED ? 15 : 31)) / (GATED ? 16 : 32)), (unsigned)a.E);
+    if (mt == 1) hipLaunchKernelGGL((k_experts_stream<1, GATED>), grid, dim3(256), 0, st, a);
+    else if (mt == 2) hipLaunchKernelGGL((k_experts_stream<2, GATED>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_experts_stream<4, GATED>), grid, dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_experts_i8(const int8_t* Xq, const float* s_x, int64_t T, int64_t K, const float* w,
+                             const int32_t* order, const int32_t* offsets, int64_t E, int k, const int8_t* W13,
+                             const float* s13, int64_t F, const int8_t* W2, const float* s2, void* out, int out_dtype,
+                             void* scratch, hipStream_t st) {
+    const int64_t P = T * k;
+    const ExpertLayout L = expert_layout(P, K, E, F);
+    uint8_t* ws = static_cast<uint8_t*>(scratch);
+    float* mid = reinterpret_cast<float*>(ws + L.mid);
+    int8_t* hq = reinterpret_cast<int8_t*>(ws + L.hq);
+    float* s_h = reinterpret_cast<float*>(ws + L.s_h);
+    int32_t* inv = reinterpret_cast<int32_t*>(ws + L.inv);
+    int32_t* tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
+    ExpertArgs a1{Xq, s_x, W13, s13, order, offsets, tiles, inv, mid, T, P, (int32_t)E, k, K, F};
+    ExpertArgs a2{hq, s_h, W2, s2, order, offsets, tiles, inv, mid, T, P, (int32_t)E, k, F, K};
+    const int64_t avg = P / E;
+    const bool stream = avg <= 48;
+    const int mt = avg <= 8 ? 1 : (avg <= 24 ? 2 : 4);
+    hipError_t e;
+    typedef tile::Cfg<128, 256, 2, 4> Tile;
+    if (stream) {
+        e = run_stream<true>(a1, mt, st);
+    } else {
+        hipLaunchKernelGGL(k_experts_plan, dim3((unsigned)((P + 8191) / 8192)), dim3(1024), 0, st, a1, tiles, Tile::BM,
+                           (int32_t)most_tiles<Tile>(a1));
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        e = run_tile<Tile, true>(a1, st);
+    }
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_experts_codes, dim3((unsigned)P), dim3(256), 0, st, mid, order, offsets, (int32_t)E, P, F, hq,
+                       s_h, inv);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    e = stream ? run_stream<false>(a2, mt, st) : run_tile<Tile, false>(a2, st);
+    if (e != hipSuccess) return e;
+    const dim3 grid((unsigned)T, (unsigned)((K + 1023) / 1024));
+    if (out_dtype == 0) hipLaunchKernelGGL(k_experts_sum<0>, grid, dim3(256), 0, st, mid, w, inv, k, K, out);
+    else if (out_dtype == 1) hipLaunchKernelGGL(k_experts_sum<1>, grid, dim3(256), 0, st, mid, w, inv, k, K, out);
+    else hipLaunchKernelGGL(k_experts_sum<2>, grid, dim3(256), 0, st, mid, w, inv, k, K, out);
+    return hipGetLastError();
+}
+
+}  // namespace qa

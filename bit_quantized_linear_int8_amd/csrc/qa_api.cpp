@@ -135,6 +135,17 @@ W4zLayout w4z_layout(int64_t M, int64_t K) {
     return L;
 }
 
+constexpr int64_t kMaxI32 = 2147483647;
+constexpr int64_t kMaxExperts = 1024;       // a block's threads in the routing and tile plans
+constexpr int64_t kMaxSlots = 32;           // experts per token
+constexpr int64_t kMaxRank = 256;
+
+bool experts_shape_ok(int64_t T, int64_t K, int32_t k, int64_t E, int64_t F) {
+    return T >= 0 && T <= kMaxI32 && E >= 1 && E <= kMaxExperts && k >= 1 && k <= kMaxSlots && K > 0 && K % 16 == 0 &&
+           K <= kMaxK_i8 && F > 0 && F % 16 == 0 && F <= kMaxK_i8 && T * K <= kMaxI32 && 2 * F * K <= kMaxI32 &&
+           T * k <= ((int64_t)1 << 26);
+}
+
 bool valid_dtype(qa_dtype d) { return d == QA_F32 || d == QA_F16 || d == QA_BF16; }
 
 }  // namespace
@@ -829,6 +840,126 @@ qa_status qa_gemm_w4a8_group_acc(const int8_t* Xq, const uint32_t* Wp, int64_t M
         return fail(QA_ERR_ALIGN, "qa_gemm_w4a8_group_acc: Xq, Wp 16-byte, acc 4-byte aligned");
     return device_status(qa::launch_gemm_w4a8_group_acc(Xq, Wp, M, K, N, G, acc, as_stream(stream)),
                          "qa_gemm_w4a8_group_acc");
+}
+
+// ----------------------------------------------------------------- norm
+qa_status qa_rmsnorm_int8(const void* X, int64_t ldx, const void* residual_or_null, int64_t ldr, const void* g,
+                          qa_dtype dtype, int64_t rows, int64_t K, float eps, int8_t* Xq, float* s,
+                          void* sum_or_null, int64_t lds, void* y_or_null, void* stream) {
+    if (rows < 0 || rows > kMaxI32 || K <= 0 || K > kMaxK_quant || ldx < K || (residual_or_null && ldr < K) ||
+        (sum_or_null && lds < K))
+        return fail(QA_ERR_SHAPE, "qa_rmsnorm_int8: need 0 <= rows < 2^31, 0 < K <= 2^26, row strides >= K");
+    if (!valid_dtype(dtype)) return fail(QA_ERR_VALUE, "qa_rmsnorm_int8: bad dtype %d", (int)dtype);
+    if (!(eps > 0.0f) || std::isinf(eps)) return fail(QA_ERR_VALUE, "qa_rmsnorm_int8: eps must be positive and finite");
+    if (rows == 0) return ok();
+    if (!X || !g || !Xq || !s) return fail(QA_ERR_NULL, "qa_rmsnorm_int8: NULL X, g, Xq or s");
+    const size_t el = dtype == QA_F32 ? 4 : 2;
+    if (!aligned(X, el) || !aligned(residual_or_null, el) || !aligned(g, el) || !aligned(sum_or_null, el) ||
+        !aligned(y_or_null, el) || !aligned(s, 4))
+        return fail(QA_ERR_ALIGN, "qa_rmsnorm_int8: arrays must be aligned to their elements");
+    return device_status(qa::launch_rmsnorm_i8(X, ldx, residual_or_null, ldr, g, (int)dtype, rows, K, eps, Xq, s,
+                                               sum_or_null, lds, y_or_null, as_stream(stream)),
+                         "qa_rmsnorm_int8");
+}
+
+// ----------------------------------------------------------------- experts
+size_t qa_route_experts_workspace(int64_t T, int64_t E, int32_t k) {
+    if (T < 0 || T > kMaxI32 || E < 1 || E > kMaxExperts || k < 1 || k > kMaxSlots) return 0;
+    return up(qa::route_scratch_bytes(T, E));
+}
+
+qa_status qa_route_experts(const void* logits, qa_dtype dtype, int64_t T, int64_t E, int64_t ld,
+                           const float* bias_or_null, qa_score score, int32_t n_groups, int32_t top_groups,
+                           int32_t group_top, int32_t k, int32_t renorm, float scale, int32_t* ids, float* weights,
+                           int32_t* order, int32_t* offsets, void* workspace, size_t workspace_bytes, void* stream) {
+    if (T < 0 || T > kMaxI32 || E < 1 || E > kMaxExperts || ld < E || k < 1 || k > kMaxSlots || k > E ||
+        T * k > kMaxI32)
+        return fail(QA_ERR_SHAPE, "qa_route_experts: need T >= 0, 1 <= E <= 1024, ld >= E, 1 <= k <= min(32, E), T k < 2^31");
+    if (n_groups < 1 || n_groups > 32 || E % n_groups != 0 || top_groups < 1 || top_groups > n_groups ||
+        k > top_groups * (E / n_groups))
+        return fail(QA_ERR_SHAPE, "qa_route_experts: need 1 <= n_groups <= 32 dividing E, 1 <= top_groups <= n_groups, "
+                                  "k <= top_groups E / n_groups");
+    if (!valid_dtype(dtype) || (score != QA_SCORE_SOFTMAX && score != QA_SCORE_SIGMOID) ||
+        (group_top != 1 && group_top != 2) || !std::isfinite(scale))
+        return fail(QA_ERR_VALUE, "qa_route_experts: bad dtype, score, group_top (1 or 2) or scale");
+    if (!offsets || (T > 0 && (!logits || !ids || !weights || !order || !workspace)))
+        return fail(QA_ERR_NULL, "qa_route_experts: NULL pointer");
+    if (!aligned(logits, dtype == QA_F32 ? 4 : 2) || !aligned(bias_or_null, 4) || !aligned(ids, 4) ||
+        !aligned(weights, 4) || !aligned(order, 4) || !aligned(offsets, 4) || !aligned(workspace, 4))
+        return fail(QA_ERR_ALIGN, "qa_route_experts: arrays must be aligned to their elements");
+    if (T > 0 && workspace_bytes < qa_route_experts_workspace(T, E, k))
+        return fail(QA_ERR_WORKSPACE, "qa_route_experts: workspace %zu < %zu bytes", workspace_bytes,
+                    qa_route_experts_workspace(T, E, k));
+    return device_status(qa::launch_route(logits, (int)dtype, T, E, ld, bias_or_null, score == QA_SCORE_SIGMOID,
+                                          n_groups, top_groups, group_top == 2, k, renorm != 0, scale, ids, weights,
+                                          order, offsets, workspace, as_stream(stream)),
+                         "qa_route_experts");
+}
+
+size_t qa_experts_int8_workspace(int64_t T, int64_t K, int32_t k, int64_t E, int64_t F) {
+    if (!experts_shape_ok(T, K, k, E, F)) return 0;
+    return up(qa::experts_scratch_bytes(T * k, K, E, F));
+}
+
+qa_status qa_experts_int8(const int8_t* Xq, const float* s_x, int64_t T, int64_t K, const float* weights,
+                          const int32_t* order, const int32_t* offsets, int64_t E, int32_t k, const int8_t* W13,
+                          const float* s13, int64_t F, const int8_t* W2, const float* s2, void* out,
+                          qa_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!experts_shape_ok(T, K, k, E, F))
+        return fail(QA_ERR_SHAPE, "qa_experts_int8: need T >= 0, 1 <= E <= 1024, 1 <= k <= 32, K and F multiples of 16 "
+                                  "in 16..131072, T K and 2 F K below 2^31, T k <= 2^26");
+    if (!valid_dtype(out_dtype)) return fail(QA_ERR_VALUE, "qa_experts_int8: bad out_dtype %d", (int)out_dtype);
+    if (T == 0) return ok();
+    if (!Xq || !s_x || !weights || !order || !offsets || !W13 || !s13 || !W2 || !s2 || !out || !workspace)
+        return fail(QA_ERR_NULL, "qa_experts_int8: NULL pointer");
+    if (!aligned(Xq, 16) || !aligned(W13, 16) || !aligned(W2, 16) || !aligned(s13, 16) || !aligned(s2, 16) ||
+        !aligned(out, 16) || !aligned(s_x, 4) || !aligned(weights, 4) || !aligned(order, 4) || !aligned(offsets, 4) ||
+        !aligned(workspace, kAlign))
+        return fail(QA_ERR_ALIGN, "qa_experts_int8: codes, weights' codes and scales, out 16-byte, workspace 256-byte, "
+                                  "others 4-byte aligned");
+    if (workspace_bytes < qa_experts_int8_workspace(T, K, k, E, F))
+        return fail(QA_ERR_WORKSPACE, "qa_experts_int8: workspace %zu < %zu bytes", workspace_bytes,
+                    qa_experts_int8_workspace(T, K, k, E, F));
+    return device_status(qa::launch_experts_i8(Xq, s_x, T, K, weights, order, offsets, E, k, W13, s13, F, W2, s2, out,
+                                               (int)out_dtype, workspace, as_stream(stream)),
+                         "qa_experts_int8");
+}
+
+// ----------------------------------------------------------------- adapters
+size_t qa_qlinear_int8_lora_workspace(int64_t M, int64_t K, int32_t r) {
+    if (M < 0 || M > kMaxI32 || K <= 0 || r < 8 || r > kMaxRank || r % 8 != 0) return 0;
+    return up(qa::lora_scratch_bytes(M, r));
+}
+
+qa_status qa_qlinear_int8_lora(const int8_t* Xq, const float* s_x, const void* X, qa_dtype dtype, int64_t M,
+                               int64_t K, const int8_t* Wq, const float* s_w, int64_t N, const void* A, const void* B,
+                               const float* alpha, int32_t r, int64_t L, const int32_t* seg, const int32_t* which,
+                               int64_t R, void* out, qa_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    if (M < 0 || M > kMaxI32 || N < 0 || N > kMaxI32 || L < 0 || L > kMaxI32 || R < 0 || R > kMaxI32 - 1 || K <= 0 ||
+        K % 16 != 0 || K > kMaxK_i8 || r < 8 || r > kMaxRank || r % 8 != 0 ||
+        ((M + 63) / 64) * ((N + 127) / 128) > kMaxI32)
+        return fail(QA_ERR_SHAPE, "qa_qlinear_int8_lora: need M, N, L, R >= 0, K %% 16 == 0, 0 < K <= %lld, r %% 8 == 0, "
+                                  "8 <= r <= %d",
+                    (long long)kMaxK_i8, (int)kMaxRank);
+    if ((dtype != QA_F16 && dtype != QA_BF16) || !valid_dtype(out_dtype))
+        return fail(QA_ERR_VALUE, "qa_qlinear_int8_lora: dtype must be fp16 or bf16, out_dtype fp32, fp16 or bf16");
+    if (M == 0 || N == 0) return ok();
+    const bool adapters = R > 0 && L > 0;
+    if (!Xq || !s_x || !Wq || !s_w || !out || !workspace ||
+        (adapters && (!X || !A || !B || !alpha || !seg || !which)))
+        return fail(QA_ERR_NULL, "qa_qlinear_int8_lora: NULL pointer");
+    if (!aligned(Xq, 16) || !aligned(X, 16) || !aligned(Wq, 16) || !aligned(A, 16) || !aligned(B, 16) ||
+        !aligned(s_x, 4) || !aligned(s_w, 4) || !aligned(alpha, 4) || !aligned(seg, 4) || !aligned(which, 4) ||
+        !aligned(out, 4) || !aligned(workspace, kAlign))
+        return fail(QA_ERR_ALIGN, "qa_qlinear_int8_lora: Xq, X, Wq, A, B 16-byte, workspace 256-byte, others 4-byte aligned");
+    if (workspace_bytes < qa_qlinear_int8_lora_workspace(M, K, r))
+        return fail(QA_ERR_WORKSPACE, "qa_qlinear_int8_lora: workspace %zu < %zu bytes", workspace_bytes,
+                    qa_qlinear_int8_lora_workspace(M, K, r));
+    return device_status(qa::launch_lora_i8(Xq, s_x, X, dtype == QA_BF16, M, K, Wq, s_w, N, A, B, alpha, r, (int)L, seg,
+                                            which, adapters ? (int)R : 0, out, (int)out_dtype, workspace,
+                                            as_stream(stream)),
+                         "qa_qlinear_int8_lora");
 }
 
 qa_status qa_probe_stream_read(const void* src, size_t bytes, int32_t wgs, int32_t lane_bytes, int32_t unroll,

@@ -202,4 +202,31 @@ hipError_t launch_gemm_w4a4_asym(const uint32_t* Xp, const float* s_x, const int
 hipError_t launch_gemm_w4a8_group_acc(const int8_t* Xq, const uint32_t* Wp, int64_t M, int64_t K, int64_t N, int G,
                                       int32_t* acc, hipStream_t st);
 
+// Residual addition + RMS norm + [-127, 127] absmax codes per row; dtype 0 f32,
+// 1 f16, 2 bf16 for X, R (or null), g, sum (or null) and y (or null, contiguous).
+hipError_t launch_rmsnorm_i8(const void* X, int64_t ldx, const void* R, int64_t ldr, const void* g, int dtype,
+                             int64_t rows, int64_t K, float eps, int8_t* q, float* s, void* sum, int64_t lds, void* y,
+                             hipStream_t st);
+
+// Routing: the choice of k experts per token, their weights, the pairs in
+// expert order and the experts' starts.
+size_t route_scratch_bytes(int64_t T, int64_t E);
+hipError_t launch_route(const void* x, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, bool sigmoid,
+                        int groups, int top_groups, bool top2, int k, bool renorm, float scale, int32_t* ids, float* w,
+                        int32_t* order, int32_t* offsets, void* scratch, hipStream_t st);
+
+// The gated feed-forward of the experts on int8 codes; P = T k pairs.
+size_t experts_scratch_bytes(int64_t P, int64_t K, int64_t E, int64_t F);
+hipError_t launch_experts_i8(const int8_t* Xq, const float* s_x, int64_t T, int64_t K, const float* w,
+                             const int32_t* order, const int32_t* offsets, int64_t E, int k, const int8_t* W13,
+                             const float* s13, int64_t F, const int8_t* W2, const float* s2, void* out, int out_dtype,
+                             void* scratch, hipStream_t st);
+
+// The int8 linear with the low-rank adapters of R requests.
+size_t lora_scratch_bytes(int64_t M, int64_t r);
+hipError_t launch_lora_i8(const int8_t* Xq, const float* s_x, const void* X, bool bf16, int64_t M, int64_t K,
+                          const int8_t* Wq, const float* s_w, int64_t N, const void* A, const void* B,
+                          const float* alpha, int r, int L, const int32_t* seg, const int32_t* which, int R, void* out,
+                          int out_dtype, void* scratch, hipStream_t st);
+
 }  // namespace qa

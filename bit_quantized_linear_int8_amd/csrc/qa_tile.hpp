@@ -1,0 +1,153 @@
+// qa_tile.hpp -- the int8 tile product shared by the grouped and the adapter
+// linears: acc[FM][FN] = A rows x B rows^T with rows picked by the caller.
+//
+// Both operands are K-contiguous int8 rows.  A stage holds BK = 64 bytes of K
+// of the tile's BM rows of A followed by its BN rows of B; it is filled by
+// direct global -> LDS loads (one instruction: 64 lanes x 16 bytes = 16 rows),
+// and since every lane names its own address, the rows may come from anywhere:
+// gathered tokens, or gate and up rows in turn.  Four stages, three in flight.
+// The 16-byte chunk c of row r is stored at chunk c ^ ((r >> 1) & 3), which
+// makes the fragment reads of 8 consecutive rows hit 8 different bank groups;
+// the permutation is produced by the chunk that each lane fetches.
+//
+// The MFMA takes B first, so it makes the transposed 16 x 16 tile: lane l,
+// element e of acc[i][j] is row 16 i + l % 16, column 16 j + 4 (l / 16) + e of
+// the wave's tile.
+#pragma once
+
+#include "qa_device.hpp"
+
+namespace qa {
+namespace tile {
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <int BM_, int BN_, int WM_, int WN_>
+struct Cfg {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN;
+    static constexpr int BK = 64, STAGES = 4, THREADS = 64 * NW;
+    static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+    static constexpr int INS = (BM + BN) / 16 / NW;          // load instructions of a wave per stage
+    static constexpr int STAGE = (BM + BN) * BK, LDS = STAGES * STAGE;
+    static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "wave tiles are whole fragments");
+    static_assert((BM + BN) % (16 * NW) == 0, "a stage's rows split evenly over the waves");
+};
+
+__device__ __forceinline__ int swz(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
+
+// s_waitcnt immediate waiting for vmcnt <= n only (gfx9 encoding)
+constexpr int vmcnt(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
+
+__device__ __forceinline__ void block_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Block -> output tile: block b runs on XCD b % 8; every XCD takes a contiguous
+// range of tiles, walked eight tile rows at a time, so that neighbours in time
+// share rows of A and of B in that XCD's L2.
+__device__ __forceinline__ void of_block(int bid, int tiles_m, int tiles_n, int& tm, int& tn) {
+    const int ntiles = tiles_m * tiles_n, per = ntiles >> 3, rem = ntiles & 7;
+    const int xcd = bid & 7, slot = bid >> 3;
+    const int t = xcd < rem ? xcd * (per + 1) + slot : rem * (per + 1) + (xcd - rem) * per + slot;
+    const int g = t / (8 * tiles_n), first = g * 8;
+    const int gm = tiles_m - first < 8 ? tiles_m - first : 8;
+    const int r = t - g * 8 * tiles_n;
+    tm = first + r % gm;
+    tn = r / gm;
+}
+
+// row_a(r), row_b(r): byte offset of tile row r in its descriptor, or kOOB for
+// a row of zeros.  K is a multiple of 16.  On return no load is in flight and
+// every wave has passed its last fragment read, so smem is free.
+template <class C, class RA, class RB>
+__device__ __forceinline__ void product(rsrc_t rsa, rsrc_t rsb, uint32_t K, uint8_t* smem, RA&& row_a, RB&& row_b,
+                                        v4i (&acc)[C::FM][C::FN]) {
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    uint32_t off[C::INS], ck[C::INS];
+#pragma unroll
+    for (int q = 0; q < C::INS; ++q) {
+        const int P = (q * C::NW + wave) * 64 + lane;        // 16-byte chunk of the stage
+        const int r = P >> 2, c = (P & 3) ^ ((r >> 1) & 3);
+        const uint32_t base = r < C::BM ? row_a(r) : row_b(r - C::BM);
+        off[q] = base == kOOB ? kOOB : base + c * 16;
+        ck[q] = c * 16;
+    }
+    const int nk = (int)((K + C::BK - 1) / C::BK);
+    auto issue = [&](int kt) __attribute__((always_inline)) {
+        uint8_t* st = smem + (kt % C::STAGES) * C::STAGE;
+        const uint32_t k0 = (uint32_t)kt * C::BK;
+#pragma unroll
+        for (int q = 0; q < C::INS; ++q) {
+            const bool a = (q * C::NW + wave) * 16 < C::BM;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(a ? rsa : rsb, (lds_void*)(st + (q * C::NW + wave) * 1024), 16,
+                                                     k0 + ck[q] < K ? off[q] + k0 : kOOB, 0, 0, 0);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+    issue(0);
+    if (nk > 1) issue(1);
+    if (nk > 2) issue(2);
+    const int c = lane >> 4;
+    for (int kt = 0; kt < nk; ++kt) {
+        const int ahead = (kt + 2 < nk - 1 ? kt + 2 : nk - 1) - kt;          // younger stages in flight
+        if (ahead >= 2) __builtin_amdgcn_s_waitcnt(vmcnt(2 * C::INS));
+        else if (ahead == 1) __builtin_amdgcn_s_waitcnt(vmcnt(C::INS));
+        else __builtin_amdgcn_s_waitcnt(vmcnt(0));
+        block_barrier();
+        // stage kt + 3 takes the buffer of stage kt - 1, whose reads every wave
+        // finished before its MFMAs of iteration kt - 1, before this barrier
+        if (kt + 3 < nk) issue(kt + 3);
+        const uint8_t* sa = smem + (kt % C::STAGES) * C::STAGE;
+        const uint8_t* sb = sa + C::BM * C::BK;
+        v4i fa[C::FM], fb[C::FN];
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+            fa[i] = *reinterpret_cast<const v4i*>(sa + swz(wm * C::TM + i * 16 + (lane & 15), c));
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+            fb[j] = *reinterpret_cast<const v4i*>(sb + swz(wn * C::TN + j * 16 + (lane & 15), c));
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+    __syncthreads();
+}
+
+}  // namespace tile
+
+// Four outputs at p (element type dt: 0 fp32, 1 fp16, 2 bf16), of which the
+// first n exist; whole vectors where `vec` says that rows allow them.
+__device__ __forceinline__ void store4(void* p, int64_t at, int dt, const float* v, int n, bool vec) {
+    if (dt == 0) {
+        float* o = static_cast<float*>(p) + at;
+        if (vec && n >= 4) {
+            *reinterpret_cast<v4f*>(o) = v4f{v[0], v[1], v[2], v[3]};
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n) o[e] = v[e];
+        return;
+    }
+    uint16_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = dt == 1 ? f2h(v[e]) : f2bf(v[e]);
+    uint16_t* o = static_cast<uint16_t*>(p) + at;
+    if (vec && n >= 4) {
+        *reinterpret_cast<u32x2*>(o) = u32x2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < n) o[e] = h[e];
+}
+
+}  // namespace qa

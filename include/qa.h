@@ -18,6 +18,9 @@
  *     migration factors and the weight's input channels multiplied by them,
  *     so both quantize to int8 with plain absmax scales (per token or per
  *     tensor for X, per output channel for W) and no fp16 branch.
+ *   - Around them: the norm that makes a linear's codes, routing to experts,
+ *     the experts' gated feed-forward on int8 codes, and an int8 projection
+ *     with the low-rank adapters of many requests.
  *
  * Sources, cited by page title and section:
  *   [AIInfra-Q01]  Infrasys-AI "AIInfra" notes, page 05Quantization01 (模型量化):
@@ -585,6 +588,131 @@ qa_status qa_gemm_w4a4_group_acc(const uint32_t* Xp, const uint32_t* Wp, int64_t
                                  int64_t N, int32_t G, int32_t* acc, void* stream);
 qa_status qa_gemm_w4a8_group_acc(const int8_t* Xq, const uint32_t* Wp, int64_t M, int64_t K,
                                  int64_t N, int32_t G, int32_t* acc, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Residual addition, root-mean-square norm and int8 codes in one pass: the
+ * operator in front of an int8 linear that takes codes
+ *
+ *   h = X + residual                    (fp32; residual NULL: h = X)
+ *   y = h g / sqrt(mean_j h_j^2 + eps)  (fp32)
+ *   s[m] = max_j |y_j| / 127 (1.0 where that is 0), Xq = rint(y / s)
+ *   X, residual, g, sum, y   arrays of `dtype` (fp32, fp16 or bf16)
+ *   ldx, ldr, lds   row strides of X, residual and sum, in elements
+ *   sum     [rows x K] or NULL: h rounded to dtype; may be X or residual itself
+ *           (same pointer and stride), no other overlap of outputs is allowed
+ *   y       [rows x K] contiguous or NULL: the norm rounded to dtype
+ *   Xq, s   i8 [rows x K] contiguous, f32 [rows]
+ * Any K >= 1; rows whose arrays all start at 16-byte boundaries (K, strides)
+ * are read and written in whole 16-byte pieces.
+ * A row that holds an infinity or NaN, or whose sum of squares passes fp32,
+ * gets s = NaN and codes 0 (so a linear's output row is NaN); other rows are
+ * unaffected.  g must be finite.
+ * Errors: rows < 0, rows > 2^31 - 1, K <= 0, K > 2^26, a stride below K, bad
+ * dtype, eps not positive and finite, NULL X / g / Xq / s, X / g / residual /
+ * sum / y not aligned to their elements, s not 4-byte aligned.
+ * ------------------------------------------------------------------------- */
+qa_status qa_rmsnorm_int8(const void* X, int64_t ldx, const void* residual_or_null, int64_t ldr, const void* g,
+                          qa_dtype dtype, int64_t rows, int64_t K, float eps, int8_t* Xq, float* s,
+                          void* sum_or_null, int64_t lds, void* y_or_null, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Routing of tokens to experts
+ *
+ *   score_e  = softmax(logits)_e or 1 / (1 + exp(-logit_e))
+ *   choice_e = score_e + bias_e
+ *   With n_groups > 1 the E experts form n_groups equal ranges; a group's value
+ *   is its largest choice (group_top 1) or the sum of its two largest
+ *   (group_top 2), and only the top_groups groups of largest value keep their
+ *   experts.  The k experts of largest choice are taken in descending order.
+ *   Ties, of groups and of experts, go to the lower index.
+ *   weight_j = score (without the bias) of the j-th expert; with renorm divided
+ *   by the sum of the token's k (where that is not 0); times scale.
+ *   logits  [T x E] of dtype, row stride ld elements; bias f32 [E] or NULL
+ *   ids     i32 [T x k]; weights f32 [T x k]
+ *   order   i32 [T k]: the pairs t k + j grouped by expert, ascending within
+ *           an expert; places past the last pair hold -1
+ *   offsets i32 [E + 1]: expert e's pairs are order[offsets[e] .. offsets[e+1])
+ * Softmax without a bias (and with groups valued by their largest expert)
+ * chooses by the logits themselves, which have the same order.
+ * A logit of -infinity or NaN masks its expert; +infinity counts as the
+ * largest finite value.  Where fewer than k experts are left, the last slots
+ * are expert -1 with weight 0 and are in no expert's range.
+ *   workspace  qa_route_experts_workspace(T, E, k) bytes (any content)
+ * The result does not depend on the order in which blocks run.  T == 0 writes
+ * offsets alone (zeros).
+ * Errors (QA_ERR_SHAPE): T < 0, E outside 1..1024, ld < E, k outside
+ * 1..min(32, E), T k > 2^31 - 1, n_groups outside 1..32 or not dividing E,
+ * top_groups outside 1..n_groups, k > top_groups E / n_groups; (QA_ERR_VALUE)
+ * bad dtype, score or group_top, scale not finite; NULL pointers, alignment to
+ * the elements, small workspace.
+ * ------------------------------------------------------------------------- */
+typedef enum { QA_SCORE_SOFTMAX = 0, QA_SCORE_SIGMOID = 1 } qa_score;
+size_t qa_route_experts_workspace(int64_t T, int64_t E, int32_t k);
+qa_status qa_route_experts(const void* logits, qa_dtype dtype, int64_t T, int64_t E, int64_t ld,
+                           const float* bias_or_null, qa_score score, int32_t n_groups, int32_t top_groups,
+                           int32_t group_top, int32_t k, int32_t renorm, float scale, int32_t* ids, float* weights,
+                           int32_t* order, int32_t* offsets, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Gated feed-forward of the experts on int8 codes
+ *
+ * For every pair p = t k + j in expert e's range of `order`:
+ *   g = s_x[t] s13[e][f] sum_c Xq[t][c] W13[e][f][c]          f = 0 .. F-1
+ *   u = the same with row F + f
+ *   h = g / (1 + exp(-g)) u           (fp32)
+ *   s_h = max_f |h| / 127 (1.0 where that is 0), hq = rint(h / s_h)
+ *   y = s_h s2[e][c] sum_f hq[f] W2[e][c][f]                  c = 0 .. K-1
+ * and out[t] = sum_j weights[t][j] y (j ascending, fp32), rounded once.  Pairs
+ * that are in no range add nothing; a token with none gets a row of zeros.
+ *   Xq, s_x  i8 [T x K], f32 [T] (qa_rmsnorm_int8 or qa_quantize_rowwise_int8)
+ *   weights, order, offsets   of qa_route_experts: f32 [T x k], i32 [T k],
+ *            i32 [E + 1], ranges ascending and disjoint, each pair at most once
+ *            (others give unspecified values; no access leaves the arrays)
+ *   W13, s13 i8 [E x 2F x K] (gate rows, then up rows), f32 [E x 2F]
+ *   W2, s2   i8 [E x K x F], f32 [E x K]; scales per output channel
+ *   out      [T x K] of out_dtype
+ *   workspace  qa_experts_int8_workspace(T, K, k, E, F) bytes (any content)
+ * Errors (QA_ERR_SHAPE): T < 0, E outside 1..1024, k outside 1..32, K or F not
+ * a positive multiple of 16 up to 131072, T K or 2 F K >= 2^31, T k > 2^26;
+ * bad out_dtype; NULL pointers; Xq, W13, W2, s13, s2, out not 16-byte, others
+ * not 4-byte, workspace not 256-byte aligned; small workspace.
+ * ------------------------------------------------------------------------- */
+size_t qa_experts_int8_workspace(int64_t T, int64_t K, int32_t k, int64_t E, int64_t F);
+qa_status qa_experts_int8(const int8_t* Xq, const float* s_x, int64_t T, int64_t K, const float* weights,
+                          const int32_t* order, const int32_t* offsets, int64_t E, int32_t k, const int8_t* W13,
+                          const float* s13, int64_t F, const int8_t* W2, const float* s2, void* out,
+                          qa_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * A shared int8 projection with the low-rank adapters of many requests
+ *
+ *   out[m][n] = s_x[m] s_w[n] sum_k Xq[m][k] Wq[n][k]
+ *             + alpha[a] sum_j (sum_k X[m][k] A[a][j][k]) B[a][n][j]
+ * with a the adapter of the request that holds token m; tokens of requests
+ * with adapter -1, and tokens of no request, take the first line alone.  The
+ * sum is formed in fp32 and rounded once.
+ *   Xq, s_x  i8 [M x K], f32 [M]: the tokens' codes (qa_rmsnorm_int8)
+ *   X        [M x K] of dtype (fp16 or bf16): the values the adapters see (its y)
+ *   Wq, s_w  i8 [N x K], f32 [N]
+ *   A, B     [L x r x K], [L x N x r] of dtype; alpha f32 [L]
+ *   seg      i32 [R + 1]: request i holds the tokens seg[i] .. seg[i + 1]
+ *            (not descending; empty requests are allowed)
+ *   which    i32 [R]: adapter of a request; outside 0 .. L-1: none
+ *   out      [M x N] of out_dtype
+ *   workspace  qa_qlinear_int8_lora_workspace(M, K, r) bytes (any content)
+ * With R == 0 or L == 0 the adapter arrays may be NULL.
+ * Errors (QA_ERR_SHAPE): M, N, L or R negative or past 2^31 - 1, K not a
+ * positive multiple of 16 up to 131072, r not a multiple of 8 in 8..256;
+ * (QA_ERR_VALUE) dtype not fp16 / bf16, bad out_dtype; NULL pointers; Xq, X,
+ * Wq, A, B not 16-byte, others not 4-byte, workspace not 256-byte aligned;
+ * small workspace.
+ * ------------------------------------------------------------------------- */
+size_t qa_qlinear_int8_lora_workspace(int64_t M, int64_t K, int32_t r);
+qa_status qa_qlinear_int8_lora(const int8_t* Xq, const float* s_x, const void* X, qa_dtype dtype, int64_t M,
+                               int64_t K, const int8_t* Wq, const float* s_w, int64_t N, const void* A, const void* B,
+                               const float* alpha, int32_t r, int64_t L, const int32_t* seg, const int32_t* which,
+                               int64_t R, void* out, qa_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 /* ---------------------------------------------------------------------------
  * Measurement helper, not part of the method: the single-launch HBM read
