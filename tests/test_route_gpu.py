@@ -1,0 +1,196 @@
+"""qa_route_experts against the definition in 64 bits: choices, weights and the grouping of the pairs."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_linear_int8_amd as qa
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+SCORE = {"softmax": qa.QA_SCORE_SOFTMAX, "sigmoid": qa.QA_SCORE_SIGMOID}
+
+
+def reference(x, k, bias, score, groups, top_groups, group_top, renorm, scale):
+    """One row at a time, in 64 bits -> ids, weights, and whether the row's choice hangs on less than 4e-6."""
+    T, E = x.shape
+    ids = np.full((T, k), -1, np.int64)
+    w = np.zeros((T, k))
+    close = np.zeros(T, bool)
+    for t in range(T):
+        v = x[t].astype(np.float64)
+        v = np.where(np.isnan(v), -np.inf, np.minimum(v, np.finfo(np.float32).max))
+        live = v > -np.inf
+        if not live.any():
+            continue
+        with np.errstate(over="ignore"):
+            if score == "sigmoid":
+                s = 1 / (1 + np.exp(-v))
+            else:
+                s = np.exp(v - v.max())
+                s = s / s.sum()
+        by_logit = score == "softmax" and bias is None and (groups == 1 or group_top == 1)
+        c = v.copy() if by_logit else s + (0 if bias is None else bias.astype(np.float64))
+        c[~live] = -np.inf
+
+        def near(a, first, last):
+            """Whether unequal neighbours, from rank `first` to rank `last` from the top, are as near as that."""
+            a = -np.sort(-a[np.isfinite(a)])[first:last + 1]
+            d = -np.diff(a)
+            return not by_logit and bool(((d > 0) & (d < 4e-6 * np.maximum(np.abs(a[1:]), 1e-2))).any())
+        if groups > 1:
+            g = c.reshape(groups, -1)
+            top = -np.sort(-g, 1)[:, :group_top]
+            val = np.where(np.isinf(top[:, 0]), -np.inf, np.where(np.isinf(top), 0, top).sum(1))
+            close[t] |= near(val, top_groups - 1, top_groups)
+            keep = np.argsort(-val, kind="stable")[:top_groups]
+            mask = np.ones(groups, bool)
+            mask[keep] = False
+            c = np.where(np.repeat(mask, E // groups), -np.inf, c)
+        close[t] |= near(c, 0, k)
+        o = np.argsort(-c, kind="stable")[:k]
+        o = o[c[o] > -np.inf]
+        ids[t, :len(o)] = o
+        w[t, :len(o)] = s[o]
+        if renorm and w[t].sum() > 0:
+            w[t] /= w[t].sum()
+    return ids, w * scale, close
+
+
+def check(logits, k, bias=None, score="softmax", groups=1, top_groups=1, group_top=1, renorm=True, scale=1.0):
+    ids, w, order, offsets = qa.qa_route_experts(logits, k, bias=bias, score=SCORE[score], groups=groups,
+                                                 top_groups=top_groups, group_top=group_top, renorm=renorm, scale=scale)
+    T, E = logits.shape
+    rid, rw, close = reference(logits.float().cpu().numpy(), k, None if bias is None else bias.cpu().numpy(), score,
+                               groups, top_groups, group_top, renorm, scale)
+    ids, w, order, offsets = (t.cpu().numpy() for t in (ids, w, order, offsets))
+    assert close.mean() < 0.2
+    assert np.array_equal(ids[~close], rid[~close])
+    # exp within 2 units of fp32, a sum of at most 16 + 6 terms a lane and the quotients; an exponent x - max rounds
+    # once, by at most |x - max| 2^-24 relative to the result
+    tol = (40 + 2 * np.nan_to_num(np.abs(logits.float().cpu().numpy()), posinf=0, neginf=0).clip(0, 100).max()) * 2.0 ** -24
+    assert (np.abs(w[~close] - rw[~close]) <= tol * np.abs(rw[~close]) + 1e-37 * scale).all()
+    # the grouping, of the ids that came
+    flat = ids.reshape(-1)
+    want = np.concatenate([np.nonzero(flat == e)[0] for e in range(E)] + [np.full((flat < 0).sum(), -1)])
+    assert np.array_equal(order, want)
+    assert np.array_equal(offsets, np.concatenate([[0], np.cumsum([(flat == e).sum() for e in range(E)])]))
+
+
+def logits_of(T, E, dt, seed=0, std=1.5):
+    g = torch.Generator(device=DEV).manual_seed(seed * 7 + T * 1031 + E)
+    return (torch.randn(T, E, device=DEV, generator=g) * std).to(DT[dt])
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (5, 2, 2), (63, 16, 4), (64, 33, 8), (65, 64, 6), (129, 100, 16),
+                                   (70, 128, 32), (200, 256, 8), (66, 257, 5), (33, 512, 17), (65, 1000, 32),
+                                   (3, 1024, 8)])
+def test_against_64_bits(dt, score, T, E, k):
+    check(logits_of(T, E, dt), k, score=score)
+
+
+@pytest.mark.parametrize("renorm,scale", [(False, 1.0), (True, 2.5), (False, 0.5)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(100, 64, 6), (40, 255, 8), (30, 700, 8)])
+def test_bias(score, T, E, k, renorm, scale):
+    g = torch.Generator(device=DEV).manual_seed(E)
+    bias = torch.randn(E, device=DEV, generator=g) * 0.2
+    check(logits_of(T, E, "f32"), k, bias=bias, score=score, renorm=renorm, scale=scale)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("T,E,k,groups,top_groups", [(70, 256, 8, 8, 4), (65, 64, 4, 4, 1), (33, 96, 6, 32, 7),
+                                                     (20, 640, 8, 10, 3), (9, 12, 3, 12, 5), (17, 60, 15, 4, 1),
+                                                     (40, 128, 8, 8, 8)])
+def test_groups(score, bias, group_top, T, E, k, groups, top_groups):
+    g = torch.Generator(device=DEV).manual_seed(E + groups)
+    b = torch.randn(E, device=DEV, generator=g) * 0.2 if bias else None
+    check(logits_of(T, E, "f32", seed=3), k, bias=b, score=score, groups=groups, top_groups=top_groups,
+          group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_ties_go_to_the_lower_index(score, groups):
+    x = torch.randint(-2, 3, (130, 64), device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)).float()
+    check(x, 8, score=score, groups=groups, top_groups=max(1, groups // 2))
+    check(torch.zeros(65, 40, device=DEV), 8, score=score, groups=groups, top_groups=max(1, groups // 2))
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("groups,top_groups,group_top", [(1, 1, 1), (8, 3, 2), (8, 3, 1)])
+def test_masked_and_extreme_logits(dt, score, bias, groups, top_groups, group_top):
+    x = logits_of(140, 64, dt, seed=5)
+    low = torch.finfo(DT[dt]).min
+    x[0] = -math.inf                                          # nothing left
+    x[1] = float("nan")
+    x[2, 3:] = -math.inf                                      # fewer than k left
+    x[3, ::2] = float("nan")
+    x[4] = low                                                # the type's lowest value everywhere
+    x[5, 10:] = low
+    x[6, 20] = math.inf
+    x[7, 8:24] = -math.inf                                    # two groups of masked experts
+    x[8, 1:] = -math.inf
+    x[139] = -math.inf                                        # the last token
+    b = torch.linspace(-0.3, 0.3, 64, device=DEV) if bias else None
+    check(x, 8, bias=b, score=score, groups=groups, top_groups=top_groups, group_top=group_top)
+
+
+def test_two_infinite_logits_share_the_weight():
+    x = torch.zeros(1, 8, device=DEV)
+    x[0, 2] = x[0, 5] = math.inf
+    ids, w, _, _ = qa.qa_route_experts(x, 3, renorm=False)
+    assert ids[0].tolist() == [2, 5, 0] and w[0].tolist() == [0.5, 0.5, 0.0]
+
+
+def test_strided_logits():
+    x = logits_of(100, 200, "f16")
+    check(x[:, 3:67], 4)
+    check(x[::2, :128], 4)
+
+
+@pytest.mark.parametrize("T", [4096, 9000])
+def test_many_blocks(T):
+    check(logits_of(T, 24, "bf16", std=1.0), 3, renorm=False)
+
+
+def test_one_expert_takes_all():
+    x = logits_of(3000, 16, "f32") * 0.1
+    x[:, 7] = 50.0
+    check(x, 1)
+
+
+def test_no_tokens():
+    ids, w, order, offsets = qa.qa_route_experts(torch.empty(0, 16, device=DEV), 4)
+    assert ids.shape == (0, 4) and order.shape == (0,) and (offsets.cpu() == 0).all()
+
+
+def test_the_same_twice():
+    x = logits_of(5000, 128, "f32")
+    a, b = qa.qa_route_experts(x, 8), qa.qa_route_experts(x, 8)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_refusals():
+    x = torch.zeros(4, 16, device=DEV)
+    for kw in (dict(k=0), dict(k=17), dict(k=4, groups=3), dict(k=8, groups=4, top_groups=1), dict(k=4, groups=4, top_groups=5),
+               dict(k=4, score=2), dict(k=4, group_top=3), dict(k=4, scale=math.inf)):
+        with pytest.raises(qa.QAError):
+            qa.qa_route_experts(x, **kw)
+    with pytest.raises(TypeError):
+        qa.qa_route_experts(x.double(), 2)
+    with pytest.raises(ValueError):
+        qa.qa_route_experts(x, 2, bias=torch.zeros(15, device=DEV))
+    with pytest.raises(ValueError):
+        qa.qa_route_experts(x.t(), 2)
+    with pytest.raises(qa.QAError):
+        qa.qa_route_experts(torch.zeros(2, 1025, device=DEV), 2)
