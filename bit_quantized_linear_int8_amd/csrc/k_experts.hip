@@ -114,6 +114,7 @@ __global__ __launch_bounds__(256) void k_experts_stream(ExpertArgs a) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m) x[q][m] = bload16(ra, in ? oa[m] + kb : kOOB);
             }
+            __builtin_amdgcn_sched_barrier(0);               // every load in flight before the first use
 #pragma unroll
             for (int q = 0; q < U; ++q)
 #pragma unroll
@@ -384,7 +385,7 @@ hipError_t launch_experts_i8(const int8_t* Xq, const float* s_x, int64_t T, int6
     const bool stream = avg <= 48;
     const int mt = avg <= 8 ? 1 : (avg <= 24 ? 2 : 4);
     hipError_t e;
-    typedef tile::Cfg<128, 256, 2, 4> Tile;
+    typedef tile::Cfg<128, 256, 2, 4, 3> Tile;
     if (stream) {
         e = run_stream<true>(a1, mt, st);
     } else {

@@ -144,6 +144,7 @@ __global__ __launch_bounds__(512) void k_lora_stream(LoraArgs a) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) x[q][m] = bload16(rx, in ? ox[m] + kb : kOOB);
         }
+        __builtin_amdgcn_sched_barrier(0);                   // every load in flight before the first use
 #pragma unroll
         for (int q = 0; q < U; ++q)
 #pragma unroll
@@ -185,12 +186,13 @@ __global__ __launch_bounds__(512) void k_lora_stream(LoraArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: 16 tokens x 32 ranks per block on MFMA, K split over 8 waves.
-// The tile's requests are taken in turn, each with its adapter's rows.
+// Many tokens: 16 tokens x 32 ranks per block on MFMA, K split over 16 waves.
+// Block z takes every gridDim.z-th request of the tile that has an adapter;
+// rows without one are not written (and not read).
 // ---------------------------------------------------------------------------
 template <bool BF>
-__global__ __launch_bounds__(512) void k_lora_down_tile(LoraArgs a) {
-    __shared__ v4f part[8][2][64];
+__global__ __launch_bounds__(1024) void k_lora_down_tile(LoraArgs a) {
+    __shared__ v4f part[16][2][64];
     __shared__ float hrow[16][33];
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int64_t m0 = (int64_t)blockIdx.x * 16, m1 = m0 + 16 < a.M ? m0 + 16 : a.M;
@@ -201,32 +203,41 @@ __global__ __launch_bounds__(512) void k_lora_down_tile(LoraArgs a) {
     const rsrc_t rx = make_rsrc(a.X + m0 * a.K, (a.M - m0) * a.K * 2);
     const uint32_t ox = m0 + r16 < a.M ? (uint32_t)r16 * KB : kOOB;
     const int steps = (int)((KB + 63) / 64);
-    hrow[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;
-    int s = request_of(a, m0);
+    const bool wide32 = g * 32 + 16 < a.r;                   // the group's second 16 ranks exist
+    int s = request_of(a, m0), nth = 0;
     for (s = s < 0 ? 0 : s; s < a.R; ++s) {
-        const int64_t b = a.seg[s] > m0 ? a.seg[s] : m0, e = a.seg[s + 1] < m1 ? a.seg[s + 1] : m1;
         if (a.seg[s] >= m1) break;
+        const int64_t b = a.seg[s] > m0 ? a.seg[s] : m0, e = a.seg[s + 1] < m1 ? a.seg[s + 1] : m1;
         const int ad = adapter(a, s);
         if (e <= b || ad < 0) continue;
+        if (nth++ % (int)gridDim.z != (int)blockIdx.z) continue;
         const rsrc_t ra = make_rsrc(a.A + (int64_t)ad * a.r * a.K, (int64_t)a.r * KB);
         const int j0 = g * 32 + r16, j1 = j0 + 16;
         const uint32_t o0 = j0 < a.r ? (uint32_t)j0 * KB : kOOB, o1 = j1 < a.r ? (uint32_t)j1 * KB : kOOB;
         v4f acc[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
-        constexpr int U = 4;
-        for (int st = wave; st < steps; st += 8 * U) {
+        constexpr int U = 8;
+        for (int st = wave; st < steps; st += 16 * U) {
             u32x4 x[U], p0[U], p1[U];
 #pragma unroll
             for (int q = 0; q < U; ++q) {
-                const uint32_t kb = (uint32_t)(st + 8 * q) * 64 + c16;
+                const uint32_t kb = (uint32_t)(st + 16 * q) * 64 + c16;
                 const bool in = kb < KB;
                 x[q] = bload16(rx, in ? ox + kb : kOOB);
                 p0[q] = bload16(ra, in ? o0 + kb : kOOB);
-                p1[q] = bload16(ra, in ? o1 + kb : kOOB);
             }
+            if (wide32) {
 #pragma unroll
-            for (int q = 0; q < U; ++q) {
-                acc[0] = mfma16<BF>(p0[q], x[q], acc[0]);
-                acc[1] = mfma16<BF>(p1[q], x[q], acc[1]);
+                for (int q = 0; q < U; ++q) {
+                    const uint32_t kb = (uint32_t)(st + 16 * q) * 64 + c16;
+                    p1[q] = bload16(ra, kb < KB ? o1 + kb : kOOB);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);               // every load in flight before the first use
+#pragma unroll
+            for (int q = 0; q < U; ++q) acc[0] = mfma16<BF>(p0[q], x[q], acc[0]);
+            if (wide32) {
+#pragma unroll
+                for (int q = 0; q < U; ++q) acc[1] = mfma16<BF>(p1[q], x[q], acc[1]);
             }
         }
         part[wave][0][lane] = acc[0];
@@ -234,49 +245,43 @@ __global__ __launch_bounds__(512) void k_lora_down_tile(LoraArgs a) {
         __syncthreads();
         if (threadIdx.x < 128) {
             const int f = threadIdx.x >> 6, ln = threadIdx.x & 63, row = ln & 15;
-            if (m0 + row >= b && m0 + row < e) {
-                v4f c = part[0][f][ln];
+            v4f c = part[0][f][ln];
 #pragma unroll
-                for (int w = 1; w < 8; ++w) c += part[w][f][ln];
-                const float al = a.alpha[ad];
+            for (int w = 1; w < 16; ++w) c += part[w][f][ln];
+            const float al = a.alpha[ad];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) hrow[row][f * 16 + 4 * (ln >> 4) + q] = c[q] * al;
+            for (int q = 0; q < 4; ++q) hrow[row][f * 16 + 4 * (ln >> 4) + q] = c[q] * al;
+        }
+        __syncthreads();
+        // hi + lo = h 2^-e with the row's largest |h| in [2^7, 2^8)
+        if (threadIdx.x < 512) {
+            const int row = threadIdx.x >> 5, j = threadIdx.x & 31;
+            const int64_t m = m0 + row;
+            const float v = hrow[row][j];
+            float mx = __builtin_fabsf(v);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 32));
+            // 2^e from the exponent bits, kept within normal numbers; an
+            // infinite or NaN row keeps its values
+            const uint32_t ex = (__builtin_bit_cast(uint32_t, mx) >> 23) & 0xff;
+            const int sh = ex == 0xff || mx == 0.0f ? 0 : clampi((int)ex - 127 - 7, -120, 120);
+            const float up = __builtin_bit_cast(float, (uint32_t)(127 + sh) << 23);
+            const float t = v * __builtin_bit_cast(float, (uint32_t)(127 - sh) << 23);
+            if (m >= b && m < e) {
+                const uint16_t hi = BF ? f2bf(t) : f2h(t);
+                const uint16_t lo = BF ? f2bf(t - wide(hi, true)) : f2h(t - h2f(hi));
+                uint16_t* o = a.h16 + ((int64_t)g * a.M + m) * 64 + j;
+                o[0] = hi;
+                o[32] = lo;
+                if (j == 0) a.hs[(int64_t)g * a.M + m] = up;
             }
         }
         __syncthreads();
     }
-    __syncthreads();
-    // hi + lo = h 2^-e with the row's largest |h| in [2^7, 2^8)
-    const int row = threadIdx.x >> 5, j = threadIdx.x & 31;
-    const int64_t m = m0 + row;
-    const float v = hrow[row][j];
-    float mx = __builtin_fabsf(v);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 32));
-    // 2^e from the exponent bits, kept within normal numbers; an infinite or NaN
-    // row keeps its values
-    const uint32_t ex = (__builtin_bit_cast(uint32_t, mx) >> 23) & 0xff;
-    const int sh = ex == 0xff || mx == 0.0f ? 0 : clampi((int)ex - 127 - 7, -120, 120);
-    const float up = __builtin_bit_cast(float, (uint32_t)(127 + sh) << 23);
-    const float t = v * __builtin_bit_cast(float, (uint32_t)(127 - sh) << 23);
-    if (m < a.M) {
-        uint16_t hi, lo;
-        if (BF) {
-            hi = f2bf(t);
-            lo = f2bf(t - wide(hi, true));
-        } else {
-            hi = f2h(t);
-            lo = f2h(t - h2f(hi));
-        }
-        uint16_t* o = a.h16 + ((int64_t)g * a.M + m) * 64 + j;
-        o[0] = hi;
-        o[32] = lo;
-        if (j == 0) a.hs[(int64_t)g * a.M + m] = up;
-    }
 }
 
 template <class C, bool BF>
-__global__ __launch_bounds__(C::THREADS) void k_lora_tile(LoraArgs a, int32_t tiles_m, int32_t tiles_n) {
+__global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t tiles_m, int32_t tiles_n) {
     extern __shared__ uint8_t smem[];
     int tm, tn;
     tile::of_block(blockIdx.x, tiles_m, tiles_n, tm, tn);
@@ -402,12 +407,13 @@ static hipError_t run_lora(const LoraArgs& a, hipStream_t st) {
         else hipLaunchKernelGGL((k_lora_stream<4, BF>), dim3(nb, 1), dim3(512), 0, st, a);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL(k_lora_down_tile<BF>, dim3((unsigned)((a.M + 15) / 16), (unsigned)((a.r + 31) / 32)), dim3(512),
-                       0, st, a);
+    const unsigned z = a.R > 4 ? 4 : (a.R > 0 ? a.R : 1);
+    hipLaunchKernelGGL(k_lora_down_tile<BF>, dim3((unsigned)((a.M + 15) / 16), (unsigned)((a.r + 31) / 32), z),
+                       dim3(1024), 0, st, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t big = ((a.M + 127) / 128) * ((a.N + 255) / 256);
-    if (big >= 192) return run_lora_tile<tile::Cfg<128, 256, 2, 4>, BF>(a, st);
-    return run_lora_tile<tile::Cfg<64, 128, 2, 2>, BF>(a, st);
+    if (big >= 192) return run_lora_tile<tile::Cfg<128, 256, 2, 4, 3>, BF>(a, st);
+    return run_lora_tile<tile::Cfg<64, 128, 2, 2, 3>, BF>(a, st);
 }
 
 hipError_t launch_lora_i8(const int8_t* Xq, const float* s_x, const void* X, bool bf16, int64_t M, int64_t K,

@@ -19,9 +19,16 @@
 // four tokens and every reduction is four DPP steps in a row of 16 lanes; 64
 // above that), lane l holding the EPL experts l EPL .. in registers.
 //
+// The choice: k rounds of "largest left" cost each lane its EPL registers in
+// every round.  Instead the k-th largest of the lanes' own maxima is a bound
+// that the k chosen reach (k lanes hold a value as large), and few others do:
+// the values that reach it go to LDS, one to a lane, and a value's rank among
+// them is its slot.  Only where more than 16 reach it (k > 8, many ties) the
+// rounds are run.  Measured at 50001 x 128, k = 8: see launch_route.
+//
 // The grouping is stable (ascending pair index within an expert) and uses no
 // order-dependent atomics: a token chooses an expert at most once, so a block of
-// 64 tokens keeps one 64-bit token mask per expert in LDS (atomic or, any
+// up to 64 tokens keeps one 64-bit token mask per expert in LDS (atomic or, any
 // order), the expert's count is its popcount and a pair's rank the popcount
 // below its token.
 #include "qa_device.hpp"
@@ -31,9 +38,9 @@ namespace qa {
 
 namespace {
 
-constexpr int TB = 64;                       // tokens per block
-constexpr int RT = 512;                      // threads per block
 constexpr float NEG = -__builtin_inff();
+constexpr int CAP = 16;                      // values that may reach the bound
+constexpr int MAXK = 32;
 
 // LDS accesses of a wave's lanes before this are seen by its lanes after it.
 __device__ __forceinline__ void wave_sync() {
@@ -64,11 +71,86 @@ template <int LPT> __device__ __forceinline__ float rmax(float v) { return reduc
 template <int LPT> __device__ __forceinline__ float rsum(float v) { return reduce<LPT>(v, [](float a, float b) { return a + b; }); }
 template <int LPT> __device__ __forceinline__ int rmin(int v) { return reduce<LPT>(v, [](int a, int b) { return min(a, b); }); }
 
+// exp(x) for x <= 88: the exponent of 2 in two parts, so that the result is off
+// by about the exponential's own rounding whatever the size of x.  (The library
+// function's range handling costs three times as much, once per expert.)
+__device__ __forceinline__ float fexp(float x) {
+    constexpr float L2E = 1.44269502162933349609375f, L2E_LO = 1.925963033500011079e-8f, LN2 = 0.693147182464599609375f;
+    x = fmaxf(x, -104.0f);                                   // exp(-104) is 0 in fp32
+    const float t = x * L2E;
+    const float lo = __builtin_fmaf(x, L2E, -t) + x * L2E_LO;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(e, lo * LN2, e);
+}
+// 1 / (1 + exp(-x)), with one correction of the reciprocal; below -88 about 2^-127.
+__device__ __forceinline__ float sigmoid(float x) {
+    const float d = 1.0f + fexp(fminf(-x, 88.0f));
+    const float r = __builtin_amdgcn_rcpf(d);
+    return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+
+// The order of floats as unsigned numbers (no NaN; -0 counts as 0).
+__device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
 template <int DT>
 __device__ __forceinline__ float ldx(const void* p, int64_t j) {
     if constexpr (DT == 0) return static_cast<const float*>(p)[j];
     const uint16_t b = static_cast<const uint16_t*>(p)[j];
     return DT == 1 ? h2f(b) : __builtin_bit_cast(float, (uint32_t)b << 16);
+}
+
+// N consecutive elements at p, aligned to their whole size (16 bytes at most).
+template <int DT, int N>
+__device__ __forceinline__ void ldv(const uint8_t* p, float* x) {
+    constexpr int B = N * (DT == 0 ? 4 : 2);
+    uint32_t w[(B + 3) / 4];
+    if constexpr (B >= 16) {
+#pragma unroll
+        for (int i = 0; i < B / 16; ++i) {
+            const u32x4 v = reinterpret_cast<const u32x4*>(p)[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
+        }
+    } else if constexpr (B == 8) {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+        w[0] = v[0];
+        w[1] = v[1];
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if constexpr (DT == 0) {
+            x[i] = __builtin_bit_cast(float, w[i]);
+        } else {
+            const uint16_t b = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+            x[i] = DT == 1 ? h2f(b) : __builtin_bit_cast(float, (uint32_t)b << 16);
+        }
+    }
+}
+
+// Rotation within a row of 16 lanes, and an inclusive prefix sum over it.
+template <int N> __device__ __forceinline__ int ror16(int v) { return dpp<0x120 + N>(v); }
+__device__ __forceinline__ int prefix16(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    return v;
+}
+
+// For each lane of a row of 16: how many of the other 15 f(theirs, mine, other lane) counts.
+template <int N, class F>
+__device__ __forceinline__ int count15(float v, int l, F f) {
+    if constexpr (N == 16) return 0;
+    else {
+        // row_ror:N hands lane l the value of lane (l - N) mod 16
+        const float o = __builtin_bit_cast(float, ror16<N>(__builtin_bit_cast(int, v)));
+        return (f(o, v, (l + 16 - N) & 15) ? 1 : 0) + count15<N + 1>(v, l, f);
+    }
 }
 
 }  // namespace
@@ -78,124 +160,220 @@ struct RouteArgs {
     const float* bias;       // or nullptr
     int32_t* ids;
     float* w;
-    int32_t* hist;           // [E][nb] counts per block of TB tokens
+    int32_t* hist;           // [E][nb] counts per block of tokens
+    int32_t* order;          // written here when one block holds every token
+    int32_t* offsets;
     int64_t T, ld;
     int32_t E, k, groups, gsize, top_groups, nb;
     float scale;
     bool sigmoid, top2, renorm;
+    bool vec;                // rows allow whole-vector loads of EPL elements
 };
 
-// LDS words a token needs: the choice values when groups are valued, the scores
-// when the bias hides them.
-template <int DT, int LPT, int EPL>
-__global__ __launch_bounds__(RT) void k_route(RouteArgs a) {
-    constexpr int TPW = 64 / LPT;                            // tokens per wave
-    constexpr int TPP = RT / LPT;                            // tokens per pass of the block
-    constexpr int NS = 32 / LPT > 0 ? (32 + LPT - 1) / LPT : 1;   // slots per lane (k <= 32)
-    extern __shared__ uint8_t smem[];
-    uint64_t* mask = reinterpret_cast<uint64_t*>(smem);      // [E]
-    float* lc = reinterpret_cast<float*>(smem + (size_t)a.E * 8);     // [TPP][E + 1] scores or choice values
+// Exclusive prefix over the block's threads of two values each; *all gets the total.
+template <int THREADS>
+__device__ __forceinline__ int block_prefix(int v, int32_t* wsum, int* all) {
     const int lane = threadIdx.x & 63, wave = wave_id();
-    const int l = lane % LPT;
-    const int slot = wave * TPW + lane / LPT;                // token of the pass
-    float* row = lc + (size_t)slot * (a.E + 1);
-    for (int e = threadIdx.x; e < a.E; e += RT) mask[e] = 0;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(s, o, QA_WAVE);
+        if (lane >= o) s += u;
+    }
+    if (lane == 63) wsum[wave] = s;
     __syncthreads();
-    // the choice goes by the logits themselves
-    const bool by_logit = !a.sigmoid && !a.bias && (a.groups == 1 || !a.top2);
-#pragma unroll 1
-    for (int t0 = 0; t0 < TB; t0 += TPP) {
-        const int tb = t0 + slot;
-        const int64_t t = (int64_t)blockIdx.x * TB + tb;
-        const bool live = t < a.T && tb < TB;
-        const uint8_t* xp = static_cast<const uint8_t*>(a.x) + (live ? t : 0) * a.ld * (DT == 0 ? 4 : 2);
-        float c[EPL];                                        // what is chosen by; -inf: not to be chosen
+    int before = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) {
+        before += w < wave ? wsum[w] : 0;
+        sum += wsum[w];
+    }
+    *all = sum;
+    return before + s - v;
+}
+
+// Values of the groups and the experts of the kept ones, out of c in registers
+// when a group is m whole lanes (m a power of two), else over `row` in LDS.
+template <int LPT, int EPL>
+__device__ __forceinline__ void keep_groups(const RouteArgs& a, float (&c)[EPL], float* row, int l) {
+    const int m = a.gsize / EPL;
+    if (LPT == 16 && a.gsize % EPL == 0 && (m & (m - 1)) == 0) {
+        float m1 = NEG, m2 = NEG;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const int e = l * EPL + i;
-            float v = NEG;
-            if (live && e < a.E) v = ldx<DT>(xp, e);
-            // NaN masks; +inf counts as the largest finite value
-            c[i] = v != v ? NEG : fminf(v, 3.4028234663852886e38f);
+            m2 = fmaxf(m2, fminf(m1, c[i]));
+            m1 = fmaxf(m1, c[i]);
         }
-        float mx = c[0];
+        auto join = [&](float o1, float o2) {
+            m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+            m1 = fmaxf(m1, o1);
+        };
+        auto f = [](int v) { return __builtin_bit_cast(float, v); };
+        auto i = [](float v) { return __builtin_bit_cast(int, v); };
+        if (m >= 2) join(f(dpp<0xB1>(i(m1))), f(dpp<0xB1>(i(m2))));
+        if (m >= 4) join(f(dpp<0x4E>(i(m1))), f(dpp<0x4E>(i(m2))));
+        if (m >= 8) join(f(dpp<0x141>(i(m1))), f(dpp<0x141>(i(m2))));
+        if (m >= 16) join(f(dpp<0x140>(i(m1))), f(dpp<0x140>(i(m2))));
+        const float val = a.top2 && m2 != NEG ? m1 + m2 : m1;
+        const int sh = 31 - __builtin_clz(m);
+        // every group is seen through each of its m lanes
+        const int before = count15<1>(val, l, [&](float o, float v, int ol) {
+            return o > v || (o == v && (ol >> sh) < (l >> sh));
+        });
+        if (before >= a.top_groups << sh)
 #pragma unroll
-        for (int i = 1; i < EPL; ++i) mx = fmaxf(mx, c[i]);
-        mx = rmax<LPT>(mx);
-        float den = 1.0f;
-        if (!a.sigmoid) {
-            float s = 0.0f;
+            for (int q = 0; q < EPL; ++q) c[q] = NEG;
+        return;
+    }
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) s += c[i] == NEG ? 0.0f : expf(c[i] - mx);
-            den = rsum<LPT>(s);
+    for (int i = 0; i < EPL; ++i)
+        if (l * EPL + i < a.E) row[l * EPL + i] = c[i];
+    wave_sync();
+    constexpr int NS = (32 + LPT - 1) / LPT;
+    float val[NS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        const int g = n * LPT + l;
+        float m1 = NEG, m2 = NEG;
+        if (g < a.groups)
+            for (int j = 0; j < a.gsize; ++j) {
+                const float v = row[g * a.gsize + j];
+                m2 = fmaxf(m2, fminf(m1, v));
+                m1 = fmaxf(m1, v);
+            }
+        val[n] = a.top2 && m2 != NEG ? m1 + m2 : m1;
+    }
+    wave_sync();
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+        if (n * LPT + l < a.groups) row[n * LPT + l] = val[n];               // groups <= E
+    wave_sync();
+    uint32_t kept = 0;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        const int g = n * LPT + l;
+        int before = 0;
+        for (int o = 0; o < a.groups; ++o) {
+            const float v = row[o];
+            before += v > val[n] || (v == val[n] && o < g) ? 1 : 0;
         }
+        if (g < a.groups && before < a.top_groups) kept |= 1u << g;
+    }
+    kept = reduce<LPT>((int)kept, [](int p, int q) { return p | q; });
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        if (!((kept >> (min(l * EPL + i, a.E - 1) / a.gsize)) & 1)) c[i] = NEG;
+}
+
+// One token per LPT lanes, TB tokens per block (TB LPT threads).
+template <int DT, int LPT, int EPL, int TB>
+__global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
+    constexpr int THREADS = TB * LPT;
+    constexpr int NS = (MAXK + LPT - 1) / LPT;               // slots per lane
+    extern __shared__ uint8_t smem[];
+    uint64_t* mask = reinterpret_cast<uint64_t*>(smem);      // [E] tokens of the block that chose the expert
+    float* rows = reinterpret_cast<float*>(smem + (size_t)a.E * 8);           // [TB][E + 1], for keep_groups
+    __shared__ uint64_t ckey[TB][CAP];
+    __shared__ float cscore[TB][CAP];
+    __shared__ int sid[TB][MAXK];
+    __shared__ float swt[TB][MAXK];
+    const int l = threadIdx.x % LPT, tb = threadIdx.x / LPT;
+    for (int e = threadIdx.x; e < a.E; e += THREADS) mask[e] = 0;
+    __syncthreads();
+    const int64_t t = (int64_t)blockIdx.x * TB + tb;
+    const bool live = t < a.T;
+    const uint8_t* xp = static_cast<const uint8_t*>(a.x) + (live ? t : 0) * a.ld * (DT == 0 ? 4 : 2);
+    // the choice goes by the logits themselves
+    const bool by_logit = !a.sigmoid && !a.bias && (a.groups == 1 || !a.top2);
+    float c[EPL], s[EPL];                                    // chosen by (-inf: not to be chosen), score
+    if (a.vec) {
+        if (l * EPL < a.E) ldv<DT, EPL>(xp + (size_t)l * EPL * (DT == 0 ? 4 : 2), c);
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (l * EPL + i < a.E) c[i] = ldx<DT>(xp, l * EPL + i);
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        // NaN masks; +inf counts as the largest finite value
+        const bool in = live && l * EPL + i < a.E && c[i] == c[i];
+        c[i] = in ? fminf(c[i], 3.4028234663852886e38f) : NEG;
+    }
+    float mx = c[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) mx = fmaxf(mx, c[i]);
+    const float lane_top = mx;
+    mx = rmax<LPT>(mx);
+    float den = 1.0f;
+    if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) s[i] = sigmoid(c[i]);
+    } else {
+        den = 0.0f;
+        const float m0 = mx == NEG ? 0.0f : mx;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            s[i] = fexp(c[i] - m0);
+            den += s[i];
+        }
+        den = rsum<LPT>(den);
         if (!by_logit) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = l * EPL + i;
-                const bool in = c[i] != NEG;
-                const float s = a.sigmoid ? 1.0f / (1.0f + expf(-c[i])) : expf(c[i] - mx) / den;
-                if (a.bias && e < a.E) row[e] = s;
-                c[i] = in ? s + (a.bias ? a.bias[min(e, a.E - 1)] : 0.0f) : NEG;
-            }
+            for (int i = 0; i < EPL; ++i) s[i] = s[i] / den;
         }
-        if (a.groups > 1) {
-            // the groups' values, over the choice values in LDS (the scores are
-            // put back there afterwards when the bias needs them)
-            float keep_s[EPL];
+    }
+    float top = lane_top;
+    if (!by_logit) {
+        top = NEG;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = l * EPL + i;
-                keep_s[i] = a.bias && e < a.E ? row[e] : 0.0f;
-            }
+        for (int i = 0; i < EPL; ++i) {
+            const bool in = c[i] != NEG;
+            c[i] = in ? s[i] + (a.bias ? a.bias[min(l * EPL + i, a.E - 1)] : 0.0f) : NEG;
+            top = fmaxf(top, c[i]);
+        }
+    }
+    if (a.groups > 1) {
+        keep_groups<LPT, EPL>(a, c, rows + (size_t)tb * (a.E + 1), l);
+        top = c[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) top = fmaxf(top, c[i]);
+    }
+    // the bound: the k-th largest of the lanes' maxima
+    bool few = false;
+    if (LPT == 16 && a.k <= 8) {
+        const int before = count15<1>(top, l, [&](float o, float v, int ol) { return o > v || (o == v && ol < l); });
+        const float bound = reduce<16>(before < a.k ? top : __builtin_inff(), [](float p, float q) { return fminf(p, q); });
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) n += c[i] >= bound && c[i] != NEG ? 1 : 0;
+        const int upto = prefix16(n);
+        const int total = reduce<16>(upto, [](int p, int q) { return max(p, q); });
+        few = !__any(total > CAP);
+        if (few) {
+            int at = upto - n;
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (l * EPL + i < a.E) row[l * EPL + i] = c[i];
-            wave_sync();
-            float val[NS];
-            uint32_t kept = 0;
-#pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                const int g = n * LPT + l;
-                float m1 = NEG, m2 = NEG;
-                if (g < a.groups)
-                    for (int j = 0; j < a.gsize; ++j) {
-                        const float v = row[g * a.gsize + j];
-                        m2 = fmaxf(m2, fminf(m1, v));
-                        m1 = fmaxf(m1, v);
-                    }
-                val[n] = a.top2 && m2 != NEG ? m1 + m2 : m1;
-            }
-            wave_sync();
-#pragma unroll
-            for (int n = 0; n < NS; ++n)
-                if (n * LPT + l < a.groups) row[n * LPT + l] = val[n];       // groups <= E
-            wave_sync();
-#pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                const int g = n * LPT + l;
-                int before = 0;
-                for (int o = 0; o < a.groups; ++o) {
-                    const float v = row[o];
-                    before += v > val[n] || (v == val[n] && o < g) ? 1 : 0;
+                if (c[i] >= bound && c[i] != NEG) {
+                    ckey[tb][at] = ((uint64_t)ordered(c[i]) << 32) | (uint32_t)(0xffff - (l * EPL + i));
+                    cscore[tb][at] = by_logit ? c[i] : s[i];
+                    ++at;
                 }
-                if (g < a.groups && before < a.top_groups) kept |= 1u << g;
-            }
-            kept = reduce<LPT>((int)kept, [](int p, int q) { return p | q; });
+            sid[tb][l] = -1;
             wave_sync();
+            const bool mine = l < total;
+            const uint64_t key = mine ? ckey[tb][l] : 0;
+            int rank = 0;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = l * EPL + i;
-                if (!((kept >> (min(e, a.E - 1) / a.gsize)) & 1)) c[i] = NEG;
-                if (a.bias && e < a.E) row[e] = keep_s[i];
+            for (int o = 0; o < CAP; ++o) rank += o < total && ckey[tb][o] > key ? 1 : 0;
+            if (mine && rank < a.k) {
+                sid[tb][rank] = 0xffff - (int)(key & 0xffff);
+                swt[tb][rank] = cscore[tb][l];
             }
         }
-        wave_sync();
+    }
+    if (!few) {
         // k rounds: the largest value left, the lowest index among equals
-        int id[NS];
-        float wt[NS];
-#pragma unroll
-        for (int n = 0; n < NS; ++n) { id[n] = -1; wt[n] = 0.0f; }
         for (int j = 0; j < a.k; ++j) {
             float b = c[0];
             int bi = 0;
@@ -205,112 +383,143 @@ __global__ __launch_bounds__(RT) void k_route(RouteArgs a) {
             const float m = rmax<LPT>(b);
             int e = rmin<LPT>(b == m ? l * EPL + bi : 0x7fffffff);
             if (m == NEG) e = -1;
+            float sc = m;
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (l * EPL + i == e) c[i] = NEG;
-#pragma unroll
-            for (int n = 0; n < NS; ++n)
-                if (j == n * LPT + l) { id[n] = e; wt[n] = m; }
-        }
-        float sum = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            if (id[n] < 0) wt[n] = 0.0f;
-            else if (by_logit) wt[n] = expf(wt[n] - mx) / den;
-            else if (a.bias) wt[n] = row[id[n]];
-            sum += wt[n];
-        }
-        sum = rsum<LPT>(sum);
-#pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            const int j = n * LPT + l;
-            if (live && j < a.k) {
-                const float w = a.renorm && sum > 0.0f ? wt[n] / sum : wt[n];
-                a.ids[t * a.k + j] = id[n];
-                a.w[t * a.k + j] = w * a.scale;
-                if (id[n] >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&mask[id[n]]), 1ull << tb);
+                if (l * EPL + i == e) {
+                    c[i] = NEG;
+                    sc = s[i];
+                }
+            if (e < 0 ? l == 0 : e / EPL == l) {             // the expert's lane, or lane 0 for none
+                sid[tb][j] = e;
+                swt[tb][j] = by_logit ? m : sc;
             }
         }
-        wave_sync();
+    }
+    wave_sync();
+    int id[NS];
+    float wt[NS], sum = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        const int j = n * LPT + l;
+        id[n] = j < a.k ? sid[tb][j] : -1;
+        wt[n] = 0.0f;
+        if (id[n] >= 0) wt[n] = by_logit ? expf(swt[tb][j] - mx) / den : swt[tb][j];
+        sum += wt[n];
+    }
+    sum = rsum<LPT>(sum);
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        const int j = n * LPT + l;
+        if (live && j < a.k) {
+            const float w = a.renorm && sum > 0.0f ? wt[n] / sum : wt[n];
+            a.ids[t * a.k + j] = id[n];
+            a.w[t * a.k + j] = w * a.scale;
+            if (id[n] >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&mask[id[n]]), 1ull << tb);
+        }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += RT) a.hist[(int64_t)e * a.nb + blockIdx.x] = __popcll(mask[e]);
+    if (a.nb > 1) {
+        for (int e = threadIdx.x; e < a.E; e += THREADS) a.hist[(int64_t)e * a.nb + blockIdx.x] = __popcll(mask[e]);
+        return;
+    }
+    // one block holds every token: the experts' starts and the pairs' places here
+    __shared__ int32_t wsum[THREADS / 64];
+    int32_t* base = reinterpret_cast<int32_t*>(rows);        // [E]: the token rows are no longer read
+    constexpr int PER = (1024 + THREADS - 1) / THREADS;
+    int v[PER], mysum = 0, all;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = threadIdx.x * PER + i;
+        v[i] = e < a.E ? __popcll(mask[e]) : 0;
+        mysum += v[i];
+    }
+    int st = block_prefix<THREADS>(mysum, wsum, &all);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = threadIdx.x * PER + i;
+        if (e < a.E) {
+            base[e] = st;
+            a.offsets[e] = st;
+        }
+        st += v[i];
+    }
+    if (threadIdx.x == 0) a.offsets[a.E] = all;
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        const int j = n * LPT + l;
+        if (live && j < a.k && id[n] >= 0)
+            a.order[base[id[n]] + __popcll(mask[id[n]] & ((1ull << tb) - 1))] = (int32_t)(t * a.k + j);
+    }
+    for (int p = all + threadIdx.x; p < a.T * a.k; p += THREADS) a.order[p] = -1;
 }
 
 // Exclusive prefix of an expert's counts over the blocks, in place, and its
-// total: one wave per expert.
-__global__ __launch_bounds__(256) void k_route_scan(int32_t* __restrict__ hist, int32_t* __restrict__ total, int32_t E,
-                                                    int32_t nb) {
-    const int lane = threadIdx.x & 63;
-    const int e = blockIdx.x * 4 + wave_id();
-    if (e >= E) return;
-    int32_t* h = hist + (int64_t)e * nb;
-    int base = 0;
-    for (int b0 = 0; b0 < nb; b0 += 64) {
-        const int b = b0 + lane;
-        const int v = b < nb ? h[b] : 0;
-        int s = v;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int u = __shfl_up(s, o, QA_WAVE);
-            if (lane >= o) s += u;
-        }
-        if (b < nb) h[b] = base + s - v;
-        base += __shfl(s, 63, QA_WAVE);
+// total: one block per expert, thread t on the `per` blocks from t per.
+__global__ __launch_bounds__(256) void k_route_scan(int32_t* __restrict__ hist, int32_t* __restrict__ total, int32_t nb,
+                                                    int32_t per) {
+    __shared__ int32_t wsum[4];
+    int32_t* h = hist + (int64_t)blockIdx.x * nb;
+    const int64_t b0 = (int64_t)threadIdx.x * per, b1 = min(b0 + per, (int64_t)nb);
+    int s = 0, all;
+    for (int64_t b = b0; b < b1; ++b) s += h[b];
+    int at = block_prefix<256>(s, wsum, &all);
+    for (int64_t b = b0; b < b1; ++b) {
+        const int v = h[b];
+        h[b] = at;
+        at += v;
     }
-    if (lane == 0) total[e] = base;
+    if (threadIdx.x == 0) total[blockIdx.x] = all;
 }
 
 // Every pair of the block's tokens to its place: expert start + the expert's
 // pairs in earlier blocks + its tokens before this one in the block.
-__global__ __launch_bounds__(RT) void k_route_scatter(const int32_t* __restrict__ ids, const int32_t* __restrict__ pre,
-                                                      const int32_t* __restrict__ total, int64_t T, int32_t E,
-                                                      int32_t k, int32_t nb, int32_t* __restrict__ order,
-                                                      int32_t* __restrict__ offsets) {
+template <int TB>
+__global__ __launch_bounds__(512) void k_route_scatter(const int32_t* __restrict__ ids, const int32_t* __restrict__ pre,
+                                                       const int32_t* __restrict__ total, int64_t T, int32_t E,
+                                                       int32_t k, int32_t nb, int32_t* __restrict__ order,
+                                                       int32_t* __restrict__ offsets) {
+    constexpr int RT = 512, PP = (TB * MAXK + RT - 1) / RT;  // pairs per thread
     extern __shared__ uint8_t smem[];
     uint64_t* mask = reinterpret_cast<uint64_t*>(smem);      // [E]
     int32_t* base = reinterpret_cast<int32_t*>(smem + (size_t)E * 8);   // [E]
     __shared__ int32_t wsum[RT / 64];
-    const int lane = threadIdx.x & 63, wave = wave_id();
-    // exclusive prefix of the totals: thread t takes experts 2t, 2t + 1
+    const int64_t p0 = (int64_t)blockIdx.x * TB * k;
+    const int np = (int)min((int64_t)TB * k, T * k - p0);
+    int id[PP];
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+        const int p = threadIdx.x + i * RT;
+        id[i] = p < np ? ids[p0 + p] : -1;
+    }
+    // thread t takes experts 2t, 2t + 1
     const int e0 = threadIdx.x * 2;
     const int v0 = e0 < E ? total[e0] : 0, v1 = e0 + 1 < E ? total[e0 + 1] : 0;
-    int s = v0 + v1;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(s, o, QA_WAVE);
-        if (lane >= o) s += u;
-    }
-    if (lane == 63) wsum[wave] = s;
+    const int q0 = e0 < E ? pre[(int64_t)e0 * nb + blockIdx.x] : 0;
+    const int q1 = e0 + 1 < E ? pre[(int64_t)(e0 + 1) * nb + blockIdx.x] : 0;
     for (int e = threadIdx.x; e < E; e += RT) mask[e] = 0;
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < RT / 64; ++w) {
-        before += w < wave ? wsum[w] : 0;
-        all += wsum[w];
-    }
-    const int st = before + s - v0 - v1;
-    if (e0 < E) base[e0] = st + pre[(int64_t)e0 * nb + blockIdx.x];
-    if (e0 + 1 < E) base[e0 + 1] = st + v0 + pre[(int64_t)(e0 + 1) * nb + blockIdx.x];
+    int all;
+    const int st = block_prefix<RT>(v0 + v1, wsum, &all);    // its barrier also ends the clearing
+    if (e0 < E) base[e0] = st + q0;
+    if (e0 + 1 < E) base[e0 + 1] = st + v0 + q1;
     if (blockIdx.x == 0) {
         if (e0 < E) offsets[e0] = st;
         if (e0 + 1 < E) offsets[e0 + 1] = st + v0;
         if (threadIdx.x == 0) offsets[E] = all;
     }
-    const int64_t p0 = (int64_t)blockIdx.x * TB * k, p1 = min(p0 + (int64_t)TB * k, T * k);
-    for (int64_t p = p0 + threadIdx.x; p < p1; p += RT) {
-        const int e = ids[p];
-        if (e >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&mask[e]), 1ull << ((int)(p - p0) / k));
-        if (p >= all) order[p] = -1;                         // places after the last pair
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+        const int p = threadIdx.x + i * RT;
+        if (id[i] >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&mask[id[i]]), 1ull << (p / k));
+        if (p < np && p0 + p >= all) order[p0 + p] = -1;     // places after the last pair
     }
     __syncthreads();
-    for (int64_t p = p0 + threadIdx.x; p < p1; p += RT) {
-        const int e = ids[p];
-        if (e >= 0) {
-            const int tb = (int)(p - p0) / k;
-            order[base[e] + __popcll(mask[e] & ((1ull << tb) - 1))] = (int32_t)p;
-        }
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+        const int p = threadIdx.x + i * RT;
+        if (id[i] >= 0)
+            order[base[id[i]] + __popcll(mask[id[i]] & ((1ull << (p / k)) - 1))] = (int32_t)(p0 + p);
     }
 }
 
@@ -318,9 +527,44 @@ __global__ void k_route_none(int32_t* offsets, int32_t E) {
     for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = 0;
 }
 
+// Tokens per block.  A block is one pass over its tokens, so few tokens want
+// small blocks (4096 x 256: 16 tokens fill 256 blocks, 64 tokens only 64); many
+// want few counts to scan.  Up to 64 tokens one block of 64 does the grouping
+// as well, without the other two launches.
+static int route_tb(int64_t T) { return T <= 64 || T > 16384 ? 64 : 16; }
+
 size_t route_scratch_bytes(int64_t T, int64_t E) {
-    const int64_t nb = (T + TB - 1) / TB;
+    const int64_t tb = E > 256 ? 16 : route_tb(T);
+    const int64_t nb = (T + tb - 1) / tb;
     return (size_t)(E * nb + E) * 4;
+}
+
+template <int DT, int LPT, int EPL, int TB>
+static hipError_t run_route(RouteArgs a, hipStream_t st) {
+    constexpr int SZ = DT == 0 ? 4 : 2;
+    const int bytes = EPL * SZ < 16 ? EPL * SZ : 16;
+    a.vec = a.E % EPL == 0 && a.ld * SZ % bytes == 0 && reinterpret_cast<uintptr_t>(a.x) % bytes == 0;
+    const int m = a.gsize / EPL;
+    const bool in_lanes = LPT == 16 && a.gsize % EPL == 0 && (m & (m - 1)) == 0;
+    const size_t rows = a.groups > 1 && !in_lanes ? (size_t)TB * (a.E + 1) * 4 : (size_t)a.E * 4;
+    static const hipError_t once =                           // 64 rows of 257 floats beside 28 KB of static LDS
+        hipFuncSetAttribute(reinterpret_cast<const void*>(&k_route<DT, LPT, EPL, TB>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, 96 << 10);
+    if (once != hipSuccess) return once;
+    hipLaunchKernelGGL((k_route<DT, LPT, EPL, TB>), dim3(a.nb), dim3(TB * LPT), (size_t)a.E * 8 + rows, st, a);
+    return hipGetLastError();
+}
+
+template <int DT>
+static hipError_t route_by_experts(const RouteArgs& a, int tb, hipStream_t st) {
+#define QA_ROUTE(EPL) (tb == 64 ? run_route<DT, 16, EPL, 64>(a, st) : run_route<DT, 16, EPL, 16>(a, st))
+    if (a.E <= 32) return QA_ROUTE(2);
+    if (a.E <= 64) return QA_ROUTE(4);
+    if (a.E <= 128) return QA_ROUTE(8);
+    if (a.E <= 256) return QA_ROUTE(16);
+#undef QA_ROUTE
+    if (a.E <= 512) return run_route<DT, 64, 8, 16>(a, st);
+    return run_route<DT, 64, 16, 16>(a, st);
 }
 
 hipError_t launch_route(const void* x, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, bool sigmoid,
@@ -330,35 +574,23 @@ hipError_t launch_route(const void* x, int dtype, int64_t T, int64_t E, int64_t 
         hipLaunchKernelGGL(k_route_none, dim3(1), dim3(256), 0, st, offsets, (int32_t)E);
         return hipGetLastError();
     }
-    const int nb = (int)((T + TB - 1) / TB);
+    const int tb = E > 256 ? 16 : route_tb(T);
+    const int nb = (int)((T + tb - 1) / tb);
     int32_t* hist = static_cast<int32_t*>(scratch);
     int32_t* total = hist + E * nb;
-    const RouteArgs a{x, bias, ids, w, hist, T, ld, (int32_t)E, k, groups, (int32_t)(E / groups), top_groups, nb, scale,
-                      sigmoid, top2, renorm};
-    const int lpt = E <= 256 ? 16 : 64;
-    const bool rows_in_lds = bias || groups > 1;
-    const size_t lds = (size_t)E * 8 + (rows_in_lds ? (size_t)(RT / lpt) * (E + 1) * 4 : 0);
-#define QA_ROUTE(DT, LPT, EPL) hipLaunchKernelGGL((k_route<DT, LPT, EPL>), dim3(nb), dim3(RT), lds, st, a)
-#define QA_ROUTE_E(DT)                                                                          \
-    do {                                                                                        \
-        if (E <= 32) QA_ROUTE(DT, 16, 2);                                                       \
-        else if (E <= 64) QA_ROUTE(DT, 16, 4);                                                  \
-        else if (E <= 128) QA_ROUTE(DT, 16, 8);                                                 \
-        else if (E <= 256) QA_ROUTE(DT, 16, 16);                                                \
-        else if (E <= 512) QA_ROUTE(DT, 64, 8);                                                 \
-        else QA_ROUTE(DT, 64, 16);                                                              \
-    } while (0)
-    if (dtype == 0) QA_ROUTE_E(0);
-    else if (dtype == 1) QA_ROUTE_E(1);
-    else QA_ROUTE_E(2);
-#undef QA_ROUTE_E
-#undef QA_ROUTE
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_route_scan, dim3((unsigned)((E + 3) / 4)), dim3(256), 0, st, hist, total, (int32_t)E, nb);
+    const RouteArgs a{x, bias, ids, w, hist, order, offsets, T, ld, (int32_t)E, k, groups, (int32_t)(E / groups),
+                      top_groups, nb, scale, sigmoid, top2, renorm, false};
+    hipError_t e = dtype == 0 ? route_by_experts<0>(a, tb, st)
+                              : (dtype == 1 ? route_by_experts<1>(a, tb, st) : route_by_experts<2>(a, tb, st));
+    if (e != hipSuccess || nb == 1) return e;
+    hipLaunchKernelGGL(k_route_scan, dim3((unsigned)E), dim3(256), 0, st, hist, total, nb, (nb + 255) / 256);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(k_route_scatter, dim3(nb), dim3(RT), (size_t)E * 12, st, ids, hist, total, T, (int32_t)E, k, nb,
-                       order, offsets);
+    if (tb == 64)
+        hipLaunchKernelGGL(k_route_scatter<64>, dim3(nb), dim3(512), (size_t)E * 12, st, ids, hist, total, T, (int32_t)E,
+                           k, nb, order, offsets);
+    else
+        hipLaunchKernelGGL(k_route_scatter<16>, dim3(nb), dim3(512), (size_t)E * 12, st, ids, hist, total, T, (int32_t)E,
+                           k, nb, order, offsets);
     return hipGetLastError();
 }
 

@@ -5,7 +5,7 @@
 // of the tile's BM rows of A followed by its BN rows of B; it is filled by
 // direct global -> LDS loads (one instruction: 64 lanes x 16 bytes = 16 rows),
 // and since every lane names its own address, the rows may come from anywhere:
-// gathered tokens, or gate and up rows in turn.  Four stages, three in flight.
+// gathered tokens, or gate and up rows in turn.  STAGES stages, all but one in flight.
 // The 16-byte chunk c of row r is stored at chunk c ^ ((r >> 1) & 3), which
 // makes the fragment reads of 8 consecutive rows hit 8 different bank groups;
 // the permutation is produced by the chunk that each lane fetches.
@@ -22,15 +22,16 @@ namespace tile {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-template <int BM_, int BN_, int WM_, int WN_>
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_ = 4>
 struct Cfg {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN;
-    static constexpr int BK = 64, STAGES = 4, THREADS = 64 * NW;
+    static constexpr int BK = 64, STAGES = STAGES_, THREADS = 64 * NW;
     static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
     static constexpr int INS = (BM + BN) / 16 / NW;          // load instructions of a wave per stage
     static constexpr int STAGE = (BM + BN) * BK, LDS = STAGES * STAGE;
     static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "wave tiles are whole fragments");
     static_assert((BM + BN) % (16 * NW) == 0, "a stage's rows split evenly over the waves");
+    static_assert(STAGES >= 2 && STAGES <= 4, "the waits know one to three stages ahead");
 };
 
 __device__ __forceinline__ int swz(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
@@ -90,19 +91,20 @@ __device__ __forceinline__ void product(rsrc_t rsa, rsrc_t rsb, uint32_t K, uint
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-    issue(0);
-    if (nk > 1) issue(1);
-    if (nk > 2) issue(2);
+    constexpr int AHEAD = C::STAGES - 1;
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q)
+        if (q < nk) issue(q);
     const int c = lane >> 4;
     for (int kt = 0; kt < nk; ++kt) {
-        const int ahead = (kt + 2 < nk - 1 ? kt + 2 : nk - 1) - kt;          // younger stages in flight
-        if (ahead >= 2) __builtin_amdgcn_s_waitcnt(vmcnt(2 * C::INS));
-        else if (ahead == 1) __builtin_amdgcn_s_waitcnt(vmcnt(C::INS));
+        const int left = nk - 1 - kt;                        // younger stages in flight: at most AHEAD - 1
+        if (AHEAD >= 3 && left >= 2) __builtin_amdgcn_s_waitcnt(vmcnt(2 * C::INS));
+        else if (AHEAD >= 2 && left >= 1) __builtin_amdgcn_s_waitcnt(vmcnt(C::INS));
         else __builtin_amdgcn_s_waitcnt(vmcnt(0));
         block_barrier();
-        // stage kt + 3 takes the buffer of stage kt - 1, whose reads every wave
-        // finished before its MFMAs of iteration kt - 1, before this barrier
-        if (kt + 3 < nk) issue(kt + 3);
+        // stage kt + AHEAD takes the buffer of stage kt - 1, whose reads every
+        // wave finished before its MFMAs of iteration kt - 1, before this barrier
+        if (kt + AHEAD < nk) issue(kt + AHEAD);
         const uint8_t* sa = smem + (kt % C::STAGES) * C::STAGE;
         const uint8_t* sb = sa + C::BM * C::BK;
         v4i fa[C::FM], fb[C::FN];
