@@ -620,8 +620,19 @@ def _rows(t, name, dtype):
 
 
 def _shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+
+
+def _a(t):
+    """Device address of a tensor (None: NULL), as a plain number: a call with twenty of them is host time."""
+    return None if t is None else t.data_ptr()
+
+
+def _s(stream):
+    """The given stream's handle, or that of the current device's current stream (without the stream object that
+    torch.cuda.current_stream() builds, 3 us of the host's time)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
 def qa_rmsnorm_int8(X, g, residual=None, eps=1e-6, want_y=False, total=None, stream=None):
@@ -650,8 +661,8 @@ def qa_rmsnorm_int8(X, g, residual=None, eps=1e-6, want_y=False, total=None, str
     s = _empty(stream, rows, dtype=torch.float32, device=X.device)
     y = _empty(stream, (rows, K), dtype=X.dtype, device=X.device) if want_y else None
     _check("qa_rmsnorm_int8",
-           lib().qa_rmsnorm_int8(_p(X), ldx, _p(residual), ldr, _p(g), _DTYPE_CODE[X.dtype], rows, K, float(eps),
-                                 _p(Xq), _p(s), _p(total), lds, _p(y), _stream(stream)))
+           lib().qa_rmsnorm_int8(_a(X), ldx, _a(residual), ldr, _a(g), _DTYPE_CODE[X.dtype], rows, K, float(eps),
+                                 _a(Xq), _a(s), _a(total), lds, _a(y), _s(stream)))
     return Xq, s, total, y
 
 
@@ -679,9 +690,9 @@ def qa_route_experts(logits, k: int, bias=None, score=QA_SCORE_SOFTMAX, groups=1
     offsets = _empty(stream, E + 1, dtype=torch.int32, device=d)
     workspace = _workspace(stream, qa_route_experts_workspace(T, E, k), d, workspace)
     _check("qa_route_experts",
-           lib().qa_route_experts(_p(logits), _DTYPE_CODE[logits.dtype], T, E, ld, _p(bias), int(score), int(groups),
-                                  int(top_groups), int(group_top), k, int(bool(renorm)), float(scale), _p(ids), _p(w),
-                                  _p(order), _p(offsets), _p(workspace), workspace.numel(), _stream(stream)))
+           lib().qa_route_experts(_a(logits), _DTYPE_CODE[logits.dtype], T, E, ld, _a(bias), int(score), int(groups),
+                                  int(top_groups), int(group_top), k, int(bool(renorm)), float(scale), _a(ids), _a(w),
+                                  _a(order), _a(offsets), _a(workspace), workspace.numel(), _s(stream)))
     return ids, w, order, offsets
 
 
@@ -722,9 +733,9 @@ def qa_experts_int8(Xq, s_x, weights, order, offsets, W13, s13, W2, s2, out_dtyp
     _shape(out, "out", (T, K))
     workspace = _workspace(stream, qa_experts_int8_workspace(T, K, k, E, F), Xq.device, workspace)
     _check("qa_experts_int8",
-           lib().qa_experts_int8(_p(Xq), _p(s_x), T, K, _p(weights), _p(order), _p(offsets), E, k, _p(W13), _p(s13), F,
-                                 _p(W2), _p(s2), _p(out), _DTYPE_CODE[out.dtype], _p(workspace), workspace.numel(),
-                                 _stream(stream)))
+           lib().qa_experts_int8(_a(Xq), _a(s_x), T, K, _a(weights), _a(order), _a(offsets), E, k, _a(W13), _a(s13), F,
+                                 _a(W2), _a(s2), _a(out), _DTYPE_CODE[out.dtype], _a(workspace), workspace.numel(),
+                                 _s(stream)))
     return out
 
 
@@ -770,9 +781,9 @@ def qa_qlinear_int8_lora(Xq, s_x, X, Wq, s_w, A, B, alpha, seg, which, out_dtype
     _shape(out, "out", (M, N))
     workspace = _workspace(stream, qa_qlinear_int8_lora_workspace(M, K, r), Xq.device, workspace)
     _check("qa_qlinear_int8_lora",
-           lib().qa_qlinear_int8_lora(_p(Xq), _p(s_x), _p(X), _DTYPE_CODE[X.dtype], M, K, _p(Wq), _p(s_w), N, _p(A),
-                                      _p(B), _p(alpha), r, L, _p(seg), _p(which), R, _p(out), _DTYPE_CODE[out.dtype],
-                                      _p(workspace), workspace.numel(), _stream(stream)))
+           lib().qa_qlinear_int8_lora(_a(Xq), _a(s_x), _a(X), _DTYPE_CODE[X.dtype], M, K, _a(Wq), _a(s_w), N, _a(A),
+                                      _a(B), _a(alpha), r, L, _a(seg), _a(which), R, _a(out), _DTYPE_CODE[out.dtype],
+                                      _a(workspace), workspace.numel(), _s(stream)))
     return out
 
 

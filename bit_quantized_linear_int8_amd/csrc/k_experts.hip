@@ -2,7 +2,7 @@
 // on int8 MFMA (gfx950).
 //
 //   g, u   = s_x[t] s13[e][.] (Xq[t] W13[e]^T)          gate rows 0..F-1, up rows F..2F-1
-//   h      = g / (1 + exp(-g)) * u                      (fp32)
+//   h      = g u / (1 + exp(-g))                        (fp32)
 //   s_h    = max|h| / 127 (1 where that is 0), hq = rint(h / s_h)
 //   y      = s_h s2[e][.] (hq W2[e]^T)                  (fp32)
 //   out[t] = sum_j w[t][j] y[pair t k + j]              (j ascending, fp32)
@@ -10,8 +10,8 @@
 // Rows are the dispatched pairs in expert order ("slots"): offsets[e] ..
 // offsets[e + 1] are expert e's, order[slot] names the pair t k + j.
 //
-// Four launches: the gate and up product (its tile takes 16 gate and 16 up
-// columns in turn, so one lane holds both factors of an h), the codes of h, the
+// Four launches: the gate and up product (the weight rows alternate between a
+// gate row and its up row, so one lane holds both factors of an h), the codes of h, the
 // down product, and the sum per token.  h and y pass through memory in fp32: the
 // scale of an h row needs the whole row, and fp16 there would move about 1% of
 // the codes.
@@ -26,6 +26,8 @@ namespace qa {
 
 namespace {
 
+typedef float v2f __attribute__((ext_vector_type(2)));
+
 struct ExpertArgs {
     const int8_t* A;          // codes: Xq [T x K] (gated) or hq [slots x F]
     const float* sa;          // scale per token or per slot
@@ -33,7 +35,7 @@ struct ExpertArgs {
     const float* sw;          // [E x rows]
     const int32_t* order;     // [P]
     const int32_t* offsets;   // [E + 1]
-    const int32_t* tiles;     // (expert, first row) per row tile, and the number of tiles before them
+    const int32_t* tiles;     // of k_experts_plan
     int32_t* inv;             // [P] slot of a pair
     float* out;               // h [slots x F] or y [slots x K]
     int64_t T, P;
@@ -59,7 +61,7 @@ __device__ __forceinline__ int64_t row_of(const ExpertArgs& a, int64_t slot) {
     return p < 0 || p >= a.P ? -1 : p / a.k;
 }
 
-__device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+__device__ __forceinline__ float gated(float g, float u) { return g * sigmoid(g) * u; }
 
 }  // namespace
 
@@ -162,7 +164,9 @@ __global__ __launch_bounds__(256) void k_experts_stream(ExpertArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows.  tiles[0] = number of row tiles, then (expert, first row) each.
+// Many rows.  tiles[0] = number of row tiles; tiles[8 + 8 i ..] of row tile i: its
+// expert, the expert's first row tile and its number of them, its first slot and
+// its number of slots.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(1024) void k_experts_plan(ExpertArgs a, int32_t* __restrict__ tiles, int32_t bm,
                                                        int32_t most) {
@@ -186,32 +190,59 @@ __global__ __launch_bounds__(1024) void k_experts_plan(ExpertArgs a, int32_t* __
     if (e == 1023) tiles[0] = min(pre[1023], most);
     const int at = pre[e] - mine;
     for (int i = 0; i < mine && at + i < most; ++i) {
-        tiles[2 + 2 * (at + i)] = e;
-        tiles[3 + 2 * (at + i)] = i * bm;
+        int32_t* t = tiles + 8 + 8 * (at + i);
+        t[0] = e;
+        t[1] = at;
+        t[2] = min(mine, most - at);
+        t[3] = (int32_t)s0;
+        t[4] = (int32_t)n;
     }
 }
 
 template <class C, bool GATED>
-__global__ __launch_bounds__(C::THREADS) void k_experts_tile(ExpertArgs a, int32_t tiles_n) {
+__global__ __launch_bounds__(C::THREADS, 4) void k_experts_tile(ExpertArgs a, int32_t tiles_n) {
     extern __shared__ uint8_t smem[];
     const int ntiles = a.tiles[0] * tiles_n;
     // Blocks go round-robin over the 8 XCDs: XCD x walks a contiguous range of
-    // tiles, a row tile's columns in turn, so that its rows stay in that L2.
+    // tiles, an expert's row tiles in turn for one column tile and then the next,
+    // so that weight rows (the larger operand) are fetched once into that L2.
+    // Columns fastest instead fetched them once per row tile: 412 against the
+    // figure at launch_experts_i8 for the gate and up product.
     const int per = (ntiles + 7) >> 3;
     const int slot8 = (int)(blockIdx.x >> 3);
     const int id = (int)(blockIdx.x & 7) * per + slot8;
     if (slot8 >= per || id >= ntiles) return;
-    const int tm = id / tiles_n, tn = id % tiles_n;
-    const int e = a.tiles[2 + 2 * tm];
-    const int64_t m0 = a.tiles[3 + 2 * tm];
-    int64_t s0, n;
-    slots_of(a, e, s0, n);
+    const int32_t* row_tile = a.tiles + 8 + 8 * (id / tiles_n);
+    const int e = row_tile[0], local = id - row_tile[1] * tiles_n;
+    const int tn = local / row_tile[2];
+    const int64_t m0 = (int64_t)(local % row_tile[2]) * C::BM;
+    const int64_t s0 = row_tile[3], n = row_tile[4];
     constexpr int NC = GATED ? C::BN / 2 : C::BN;            // output columns of the tile
     const int64_t n0 = (int64_t)tn * NC;
     const int64_t wrows = GATED ? 2 * a.N : a.N;
     const int8_t* A = GATED ? a.A : a.A + (s0 + m0) * a.Kc;
     const rsrc_t ra = make_rsrc(A, GATED ? a.T * a.Kc : (n - m0) * a.Kc);
     const rsrc_t rw = make_rsrc(a.W + (int64_t)e * wrows * a.Kc, wrows * a.Kc);
+    // the lane's rows and columns, their scales requested before the product
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int64_t mw = m0 + (wave / C::WN) * C::TM + (lane & 15);
+    const int wn = wave % C::WN;
+    const float* sw = a.sw + (int64_t)e * wrows;
+    float sx[C::FM], sg[C::FN][4];
+    int64_t col[C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+        const int64_t s = mw + i * 16, row = s < n ? row_of<GATED>(a, s0 + s) : -1;
+        sx[i] = row < 0 ? 0.0f : a.sa[row];
+    }
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+        col[j] = GATED ? n0 + wn * (C::TN / 2) + (lane >> 4) * (2 * C::FN) + j * 2
+                       : n0 + wn * C::TN + j * 16 + 4 * (lane >> 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            sg[j][q] = col[j] < a.N ? (GATED ? sw[(q & 1 ? a.N : 0) + col[j] + (q >> 1)] : sw[col[j] + q]) : 0.0f;
+    }
     v4i acc[C::FM][C::FN];
     tile::product<C>(
         ra, rw, (uint32_t)a.Kc, smem,
@@ -221,38 +252,27 @@ __global__ __launch_bounds__(C::THREADS) void k_experts_tile(ExpertArgs a, int32
             return row < 0 ? kOOB : (uint32_t)(row * a.Kc);
         },
         [&](int r) -> uint32_t {
-            // gated: fragments of 16 gate rows and of the same 16 up rows in turn
-            const int64_t col = GATED ? n0 + (r >> 5) * 16 + (r & 15) : n0 + r;
+            // gated: row 4 q + e of a wave's fragment j is the gate (e even) or up (e odd) row of its output column
+            // 2 FN q + 2 j + e / 2, so that lane q's outputs of all fragments lie side by side
+            const int64_t col = !GATED ? n0 + r
+                                       : n0 + r / C::TN * (C::TN / 2) + ((r >> 2) & 3) * (2 * C::FN) +
+                                             (r % C::TN) / 16 * 2 + ((r >> 1) & 1);
             if (col >= a.N) return kOOB;
-            return (uint32_t)(((GATED && (r & 16) ? a.N : 0) + col) * a.Kc);
+            return (uint32_t)(((GATED && (r & 1) ? a.N : 0) + col) * a.Kc);
         },
         acc);
-    const int lane = threadIdx.x & 63, wave = wave_id();
-    const int wm = wave / C::WN, wn = wave % C::WN;
-    const float* sw = a.sw + (int64_t)e * wrows;
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i) {
-        const int64_t s = m0 + wm * C::TM + i * 16 + (lane & 15);
-        if (s >= n) continue;
-        const int64_t row = row_of<GATED>(a, s0 + s);
-        const float sx = row < 0 ? 0.0f : a.sa[row];
-        float* o = a.out + (s0 + s) * a.N;
+    for (int j = 0; j < C::FN; ++j) {
+        if (col[j] >= a.N) continue;                         // N % 16 == 0: a lane's columns exist together
 #pragma unroll
-        for (int j = 0; j < C::FN; j += GATED ? 2 : 1) {
-            const int64_t col = n0 + (GATED ? (wn * C::TN + j * 16) / 2 : wn * C::TN + j * 16) + 4 * (lane >> 4);
-            if (col >= a.N) continue;
-            const v4f sg = *reinterpret_cast<const v4f*>(sw + col);
-            v4f v;
-            if constexpr (GATED) {
-                const v4f su = *reinterpret_cast<const v4f*>(sw + a.N + col);
+        for (int i = 0; i < C::FM; ++i) {
+            if (mw + i * 16 >= n) continue;
+            float* o = a.out + (s0 + mw + i * 16) * a.N + col[j];
+            float v[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    v[q] = gated((float)acc[i][j][q] * sx * sg[q], (float)acc[i][j + 1][q] * sx * su[q]);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = (float)acc[i][j][q] * sx * sg[q];
-            }
-            *reinterpret_cast<v4f*>(o + col) = v;
+            for (int q = 0; q < 4; ++q) v[q] = (float)acc[i][j][q] * sx[i] * sg[j][q];
+            if constexpr (GATED) *reinterpret_cast<v2f*>(o) = v2f{gated(v[0], v[1]), gated(v[2], v[3])};
+            else *reinterpret_cast<v4f*>(o) = v4f{v[0], v[1], v[2], v[3]};
         }
     }
 }
@@ -333,7 +353,7 @@ ExpertLayout expert_layout(int64_t P, int64_t K, int64_t E, int64_t F) {
     L.hq = off; off += up256((size_t)P * (size_t)F);
     L.s_h = off; off += up256((size_t)P * 4);
     L.inv = off; off += up256((size_t)P * 4);
-    L.tiles = off; off += up256((size_t)(2 + 2 * (P / 16 + E + 1)) * 4);
+    L.tiles = off; off += up256((size_t)(8 + 8 * (P / 64 + E + 1)) * 4);      // tiles of 64 rows or more
     L.total = off;
     return L;
 }
@@ -362,9 +382,17 @@ template <bool GATED>
 static hipError_t run_stream(const ExpertArgs& a, int mt, hipStream_t st) {
     const dim3 grid((unsigned)((a.N + (GATED ? 15 : 31)) / (GATED ? 16 : 32)), (unsigned)a.E);
     if (mt == 1) hipLaunchKernelGGL((k_experts_stream<1, GATED>), grid, dim3(256), 0, st, a);
-    else if (mt == 2) hipLaunchKernelGGL((k_experts_stream<2, GATED>), grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_experts_stream<4, GATED>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_experts_stream<2, GATED>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
+}
+
+template <class C, class F>
+static hipError_t run_tiles(const ExpertArgs& a1, const ExpertArgs& a2, int32_t* tiles, F&& codes, hipStream_t st) {
+    hipLaunchKernelGGL(k_experts_plan, dim3((unsigned)((a1.P + 8191) / 8192)), dim3(1024), 0, st, a1, tiles, C::BM,
+                       (int32_t)most_tiles<C>(a1));
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || (e = run_tile<C, true>(a1, st)) != hipSuccess || (e = codes()) != hipSuccess) return e;
+    return run_tile<C, false>(a2, st);
 }
 
 hipError_t launch_experts_i8(const int8_t* Xq, const float* s_x, int64_t T, int64_t K, const float* w,
@@ -381,25 +409,33 @@ hipError_t launch_experts_i8(const int8_t* Xq, const float* s_x, int64_t T, int6
     int32_t* tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
     ExpertArgs a1{Xq, s_x, W13, s13, order, offsets, tiles, inv, mid, T, P, (int32_t)E, k, K, F};
     ExpertArgs a2{hq, s_h, W2, s2, order, offsets, tiles, inv, mid, T, P, (int32_t)E, k, F, K};
-    const int64_t avg = P / E;
-    const bool stream = avg <= 48;
-    const int mt = avg <= 8 ? 1 : (avg <= 24 ? 2 : 4);
     hipError_t e;
-    typedef tile::Cfg<128, 256, 2, 4, 3> Tile;
-    if (stream) {
-        e = run_stream<true>(a1, mt, st);
+    auto codes = [&]() {
+        hipLaunchKernelGGL(k_experts_codes, dim3((unsigned)P), dim3(256), 0, st, mid, order, offsets, (int32_t)E, P, F, hq,
+                           s_h, inv);
+        return hipGetLastError();
+    };
+    // By rows per expert (64 experts of 8 per token, K = 4096, F = 1024; us of the
+    // call).  Streaming 16 or 32 rows at a time, tiles of 64 x 128 (three stages,
+    // for weights that come from HBM), tiles of 128 x 192:
+    //   rows     1     4     8    16    32    64   125   250
+    //   16      99   158   199   285   449   816
+    //   32     102   152   180   229   332   555
+    //   64     113   166   179   195   219   248   318   569
+    //   128    116   197   204   219   239   270   313   486
+    const int64_t avg = P / E;
+    if (avg < 8) {
+        const int mt = avg <= 2 ? 1 : 2;
+        if ((e = run_stream<true>(a1, mt, st)) != hipSuccess) return e;
+        if ((e = codes()) != hipSuccess) return e;
+        if ((e = run_stream<false>(a2, mt, st)) != hipSuccess) return e;
     } else {
-        hipLaunchKernelGGL(k_experts_plan, dim3((unsigned)((P + 8191) / 8192)), dim3(1024), 0, st, a1, tiles, Tile::BM,
-                           (int32_t)most_tiles<Tile>(a1));
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        e = run_tile<Tile, true>(a1, st);
+        // the large tile needs enough of them for two on every CU
+        const int64_t large = (P / 128) * ((2 * F + 191) / 192);
+        if (avg < 120 || large < 512) e = run_tiles<tile::Cfg<64, 128, 2, 4, 3>>(a1, a2, tiles, codes, st);
+        else e = run_tiles<tile::Cfg<128, 192, 2, 4, 2>>(a1, a2, tiles, codes, st);
+        if (e != hipSuccess) return e;
     }
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_experts_codes, dim3((unsigned)P), dim3(256), 0, st, mid, order, offsets, (int32_t)E, P, F, hq,
-                       s_h, inv);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    e = stream ? run_stream<false>(a2, mt, st) : run_tile<Tile, false>(a2, st);
-    if (e != hipSuccess) return e;
     const dim3 grid((unsigned)T, (unsigned)((K + 1023) / 1024));
     if (out_dtype == 0) hipLaunchKernelGGL(k_experts_sum<0>, grid, dim3(256), 0, st, mid, w, inv, k, K, out);
     else if (out_dtype == 1) hipLaunchKernelGGL(k_experts_sum<1>, grid, dim3(256), 0, st, mid, w, inv, k, K, out);

@@ -11,9 +11,9 @@
 // to the dequantized tile in fp32, so the output is rounded once and written
 // once.
 //
-// The inner products h stay in fp32, or where the second product runs on MFMA
-// as two 16-bit numbers hi + lo = h 2^-e (e from the row's largest |h| of 32
-// ranks), so that neither the type's range nor its digits limit them.
+// The inner products h stay in fp32.  Where the second product runs on MFMA they
+// enter it as two 16-bit numbers hi + lo = h 2^-e (e from the row's largest |h| of
+// 32 ranks), so that neither the type's range nor its digits limit them.
 #include "qa_tile.hpp"
 #include "qa_launch.hpp"
 
@@ -36,9 +36,10 @@ struct LoraArgs {
     const int32_t* seg;        // [R + 1] first token of each request
     const int32_t* which;      // [R] adapter or -1
     int32_t r, L, R;
+    int32_t* ad;               // [M] adapter of a token or -1, written by the first launch
     float* h;                  // [M][r] (few tokens)
-    uint16_t* h16;             // [groups of 32 ranks][M][hi 32, lo 32]
-    float* hs;                 // [groups][M] scale 2^e
+    float* hp;                 // [splits][groups of 32 ranks][M][32] parts of h (many tokens)
+    int32_t splits;
     void* out;
     int32_t dt;                // of out
     bool vec;                  // out rows allow 4-element vector stores
@@ -54,10 +55,21 @@ __device__ __forceinline__ int adapter(const LoraArgs& a, int s) {
     return w >= 0 && w < a.L ? w : -1;
 }
 
-// The last request that starts at or before token m (-1: none).  Starts do not
-// decrease, so an empty request is followed by another with the same start.
+// Adapter of token m (wave-uniform m): its request is the last one that starts
+// at or before it (starts do not decrease, so an empty request is followed by
+// another with the same start).  Up to 256 starts are counted with four loads in
+// flight at once; more are searched, a load after the other.
 __device__ __forceinline__ int request_of(const LoraArgs& a, int64_t m) {
-    int lo = 0, hi = a.R;                                    // seg[lo - 1] <= m < seg[hi]
+    const int lane = threadIdx.x & 63;
+    if (a.R < 256) {
+        int v[4], n = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = q * 64 <= a.R ? a.seg[min(q * 64 + lane, a.R)] : 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) n += __popcll(__ballot(q * 64 + lane <= a.R && v[q] <= m));
+        return n - 1;
+    }
+    int lo = 0, hi = a.R + 1;                                // seg[lo - 1] <= m < seg[hi]
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (a.seg[mid] <= m) lo = mid + 1;
@@ -67,8 +79,36 @@ __device__ __forceinline__ int request_of(const LoraArgs& a, int64_t m) {
 }
 
 __device__ __forceinline__ int adapter_of(const LoraArgs& a, int64_t m) {
-    const int s = request_of(a, m);
-    return s < 0 || m >= a.seg[s + 1] ? -1 : adapter(a, s);
+    if (a.R == 0) return -1;
+    const int s = __builtin_amdgcn_readfirstlane(request_of(a, m));
+    return s < 0 || s >= a.R ? -1 : adapter(a, s);
+}
+
+// The same for the 16 tokens from m0: lane l gets that of token m0 + l % 16.
+__device__ __forceinline__ int adapters16(const LoraArgs& a, int64_t m0) {
+    const int lane = threadIdx.x & 63, r = lane & 15;
+    if (a.R == 0) return -1;
+    int s = -1;
+    if (a.R < 256) {
+        int v[4], n = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = q * 64 <= a.R ? a.seg[min(q * 64 + lane, a.R)] : 0;
+        for (int q = 0; q * 64 <= a.R; ++q) {
+            const int w = v[q];
+            const bool in = q * 64 + lane <= a.R;
+            const uint64_t first = __ballot(in && w <= m0), last = __ballot(in && w <= m0 + 15);
+            n += __popcll(first);
+            for (uint64_t b = last & ~first; b; b &= b - 1)  // starts inside the tile
+                n += __builtin_amdgcn_readlane(w, (int)__builtin_ctzll(b)) <= m0 + r ? 1 : 0;
+        }
+        s = n - 1;
+    } else {
+        s = __builtin_amdgcn_readfirstlane(request_of(a, m0));
+        int n = s;
+        for (int i = s + 1; i <= a.R && a.seg[i] <= m0 + 15; ++i) n = a.seg[i] <= m0 + r ? i : n;
+        s = n;
+    }
+    return s < 0 || s >= a.R ? -1 : adapter(a, s);
 }
 
 template <bool BF>
@@ -82,27 +122,35 @@ __device__ __forceinline__ v4f mfma16(u32x4 x, u32x4 y, v4f c) {
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Few tokens: one block per token, its 16 waves on a rank each.
+// Few tokens: one block per token, its 16 waves on a rank each.  The token's
+// row is requested before its adapter is looked up.
 // ---------------------------------------------------------------------------
 template <bool BF>
 __global__ __launch_bounds__(1024) void k_lora_down_token(LoraArgs a) {
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int64_t m = blockIdx.x;
-    const int ad = adapter_of(a, m);
-    if (ad < 0) return;                                      // its h is not read
     const rsrc_t rx = make_rsrc(a.X + m * a.K, a.K * 2);
+    const uint32_t KB = (uint32_t)a.K * 2;
+    constexpr int U = 8;
+    u32x4 x[U], w[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) x[q] = bload16(rx, lane * 16 + q * 1024);
+    const int ad = adapter_of(a, m);
+    if (threadIdx.x == 0) a.ad[m] = ad;
+    if (ad < 0) return;                                      // its h is not read
     for (int j = wave; j < a.r; j += 16) {
-        const rsrc_t ra = make_rsrc(a.A + ((int64_t)ad * a.r + j) * a.K, a.K * 2);
+        const rsrc_t ra = make_rsrc(a.A + ((int64_t)ad * a.r + j) * a.K, KB);
         float s = 0.0f;
-        for (uint32_t k = lane * 16; k < (uint32_t)a.K * 2; k += 4096) {
-            u32x4 x[4], w[4];
+        for (uint32_t k = lane * 16; k - lane * 16 < KB; k += U * 1024) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                x[q] = bload16(rx, k + q * 1024);
-                w[q] = bload16(ra, k + q * 1024);
+            for (int q = 0; q < U; ++q) w[q] = bload16(ra, k + q * 1024);
+            if (KB > U * 1024) {
+#pragma unroll
+                for (int q = 0; q < U; ++q) x[q] = bload16(rx, k + q * 1024);
             }
+            __builtin_amdgcn_sched_barrier(0);               // every load in flight before the first use
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < U; ++q)
 #pragma unroll
                 for (int p = 0; p < 8; ++p)
                     s = __builtin_fmaf(wide((uint16_t)(x[q][p >> 1] >> (16 * (p & 1))), BF),
@@ -114,28 +162,47 @@ __global__ __launch_bounds__(1024) void k_lora_down_token(LoraArgs a) {
     }
 }
 
-// The int8 product for few tokens: 16 output columns per block, K split over
-// its 8 waves, the weight rows straight into MFMA operands.
+// The int8 product for few tokens: 16 output columns per block, K split over 8
+// waves that bring the weight rows straight into MFMA operands.  Wave t < MT also
+// owns the 16 x 16 outputs of tokens 16 t ..: its tokens' adapters are requested
+// before the weights and the first 16 ranks of B behind them, so that neither
+// waits for the other.
 template <int MT, bool BF>
 __global__ __launch_bounds__(512) void k_lora_stream(LoraArgs a) {
     __shared__ v4i part[8][MT][64];
     const int lane = threadIdx.x & 63, wave = wave_id();
-    const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * 16 * MT;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
     const uint32_t K = (uint32_t)a.K;
     const int r16 = lane & 15, c16 = (lane >> 4) * 16;
+    const int64_t mo = wave * 16 + r16, no = n0 + 4 * (lane >> 4);           // the lane's outputs, if its wave owns any
+    const bool live = wave < MT && mo < a.M && no < a.N;
+    const int cols = live ? (int)(a.N - no < 4 ? a.N - no : 4) : 0;
+    int ad = -1;
+    float sx = 0.0f, sw[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    v4f h[4];
+    if (live) {
+        ad = a.ad[mo];
+        sx = a.s_x[mo];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sw[q] = a.s_w[no + min(q, cols - 1)];
+    }
+    const rsrc_t rh = make_rsrc(a.h, live ? a.M * a.r * 4 : 0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)                              // not written for a token without an adapter, nor used
+        h[q] = __builtin_bit_cast(v4f, bload16(rh, q * 4 < a.r ? (uint32_t)(mo * a.r + q * 4) * 4 : kOOB));
     const rsrc_t rw = make_rsrc(a.Wq + n0 * a.K, (a.N - n0) * a.K);
-    const rsrc_t rx = make_rsrc(a.Xq + m0 * a.K, (a.M - m0) * a.K);
+    const rsrc_t rx = make_rsrc(a.Xq, a.M * a.K);
     const uint32_t ow = n0 + r16 < a.N ? (uint32_t)r16 * K : kOOB;
     uint32_t ox[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) ox[m] = m0 + m * 16 + r16 < a.M ? (uint32_t)(m * 16 + r16) * K : kOOB;
+    for (int m = 0; m < MT; ++m) ox[m] = m * 16 + r16 < a.M ? (uint32_t)(m * 16 + r16) * K : kOOB;
     v4i acc[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[m] = v4i{0, 0, 0, 0};
     const int nk = (int)((K + 63) / 64);
-    constexpr int U = 8;
-    for (int s = wave; s < nk; s += 8 * U) {
-        u32x4 w[U], x[U][MT];
+    constexpr int U = MT == 4 ? 4 : 8;
+    u32x4 w[U], x[U][MT];
+    auto load = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
         for (int q = 0; q < U; ++q) {
             const uint32_t kb = (uint32_t)(s + 8 * q) * 64 + c16;
@@ -145,90 +212,121 @@ __global__ __launch_bounds__(512) void k_lora_stream(LoraArgs a) {
             for (int m = 0; m < MT; ++m) x[q][m] = bload16(rx, in ? ox[m] + kb : kOOB);
         }
         __builtin_amdgcn_sched_barrier(0);                   // every load in flight before the first use
+    };
+    __builtin_amdgcn_sched_barrier(0);
+    load(wave);
+    u32x4 b[4][2];
+    const bool adapt = live && ad >= 0;
+    const uint16_t* bp = a.B + ((int64_t)(adapt ? ad : 0) * a.N + (adapt ? no : 0)) * a.r;
+    if (adapt) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                if (q < cols && p * 8 < a.r) b[q][p] = *reinterpret_cast<const u32x4*>(bp + (int64_t)q * a.r + p * 8);
+    }
+    for (int s = wave; s < nk;) {
 #pragma unroll
         for (int q = 0; q < U; ++q)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
                 acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, w[q]),
                                                                __builtin_bit_cast(v4i, x[q][m]), acc[m], 0, 0, 0);
+        s += 8 * U;
+        if (s < nk) load(s);
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) part[wave][m][lane] = acc[m];
-    __syncthreads();
-    for (int it = threadIdx.x; it < MT * 64; it += 512) {
-        const int t = it >> 6, ln = it & 63;
-        const int64_t m = m0 + t * 16 + (ln & 15), n = n0 + 4 * (ln >> 4);
-        if (m >= a.M || n >= a.N) continue;
-        v4i c = part[0][t][ln];
+    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto dot8 = [&](const u32x4& v, const v4f& h0, const v4f& h1, float& sum) __attribute__((always_inline)) {
 #pragma unroll
-        for (int w = 1; w < 8; ++w) c += part[w][t][ln];
-        const int cols = (int)(a.N - n < 4 ? a.N - n : 4);
-        const int ad = adapter_of(a, m);
-        const float sx = a.s_x[m];
-        float v[4];
+        for (int p = 0; p < 8; ++p)
+            sum = __builtin_fmaf(p < 4 ? h0[p & 3] : h1[p & 3], wide((uint16_t)(v[p >> 1] >> (16 * (p & 1))), BF), sum);
+    };
+    if (adapt) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            v[q] = q < cols ? (float)c[q] * sx * a.s_w[n + q] : 0.0f;
-            if (ad >= 0 && q < cols) {
-                const uint16_t* b = a.B + ((int64_t)ad * a.N + n + q) * a.r;
-                float d = 0.0f;
-                for (int j = 0; j < a.r; j += 8) {
-                    const u32x4 bv = *reinterpret_cast<const u32x4*>(b + j);
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int p = 0; p < 8; ++p)
-                        d = __builtin_fmaf(a.h[m * a.r + j + p], wide((uint16_t)(bv[p >> 1] >> (16 * (p & 1))), BF), d);
-                }
-                v[q] += d;
-            }
+            for (int p = 0; p < 2; ++p)
+                if (q < cols && p * 8 < a.r) dot8(b[q][p], h[2 * p], h[2 * p + 1], d[q]);
+        for (int j = 16; j < a.r; j += 8) {
+            const float* hp = a.h + mo * a.r + j;
+            const v4f h0 = *reinterpret_cast<const v4f*>(hp), h1 = *reinterpret_cast<const v4f*>(hp + 4);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (q < cols) dot8(*reinterpret_cast<const u32x4*>(bp + (int64_t)q * a.r + j), h0, h1, d[q]);
         }
-        store4(a.out, m * a.N + n, a.dt, v, cols, a.vec);
     }
+    __syncthreads();
+    if (!live) return;
+    v4i c = part[0][wave][lane];
+#pragma unroll
+    for (int p = 1; p < 8; ++p) c += part[p][wave][lane];
+    float v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = (float)c[q] * sx * sw[q] + d[q];
+    store4(a.out, mo * a.N + no, a.dt, v, cols, a.vec);
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: 16 tokens x 32 ranks per block on MFMA, K split over 16 waves.
-// Block z takes every gridDim.z-th request of the tile that has an adapter;
-// rows without one are not written (and not read).
+// Many tokens: 16 tokens x 32 ranks per block on MFMA, K split over the blocks
+// z and their 4 waves so that up to 8192 columns are one batch of loads.  The
+// tile's adapters are taken in turn with the tokens' rows kept in registers; a
+// token keeps the products with its own.  The splits are summed, in order, where
+// h is read.
 // ---------------------------------------------------------------------------
 template <bool BF>
-__global__ __launch_bounds__(1024) void k_lora_down_tile(LoraArgs a) {
-    __shared__ v4f part[16][2][64];
-    __shared__ float hrow[16][33];
+__global__ __launch_bounds__(256) void k_lora_down_tile(LoraArgs a) {
+    __shared__ v4f part[4][2][64];
     const int lane = threadIdx.x & 63, wave = wave_id();
-    const int64_t m0 = (int64_t)blockIdx.x * 16, m1 = m0 + 16 < a.M ? m0 + 16 : a.M;
-    const int g = blockIdx.y;                                // group of 32 ranks
+    const int64_t m0 = (int64_t)blockIdx.x * 16;
+    const int groups = (a.r + 31) / 32;
+    const int g = blockIdx.y % groups, z = blockIdx.z;       // group of 32 ranks, part of K
+    const int nth0 = blockIdx.y / groups, nths = gridDim.y / groups;         // this block's share of the tile's adapters
     const int r16 = lane & 15;
     const uint32_t c16 = (lane >> 4) * 16;
     const uint32_t KB = (uint32_t)a.K * 2;
     const rsrc_t rx = make_rsrc(a.X + m0 * a.K, (a.M - m0) * a.K * 2);
     const uint32_t ox = m0 + r16 < a.M ? (uint32_t)r16 * KB : kOOB;
-    const int steps = (int)((KB + 63) / 64);
     const bool wide32 = g * 32 + 16 < a.r;                   // the group's second 16 ranks exist
-    int s = request_of(a, m0), nth = 0;
-    for (s = s < 0 ? 0 : s; s < a.R; ++s) {
-        if (a.seg[s] >= m1) break;
-        const int64_t b = a.seg[s] > m0 ? a.seg[s] : m0, e = a.seg[s + 1] < m1 ? a.seg[s + 1] : m1;
-        const int ad = adapter(a, s);
-        if (e <= b || ad < 0) continue;
-        if (nth++ % (int)gridDim.z != (int)blockIdx.z) continue;
+    constexpr int U = 8;
+    const int steps = (int)((KB + 63) / 64), stride = 4 * a.splits, first = z * 4 + wave;
+    u32x4 x[U], p0[U], p1[U];
+    auto load_x = [&](int st) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const uint32_t kb = (uint32_t)(st + stride * q) * 64 + c16;
+            x[q] = bload16(rx, kb < KB ? ox + kb : kOOB);
+        }
+    };
+    const int found = adapters16(a, m0);
+    const int mine = m0 + r16 < a.M ? found : -1;
+    if (blockIdx.y == 0 && z == 0 && threadIdx.x < 16 && m0 + r16 < a.M) a.ad[m0 + r16] = mine;
+    uint32_t left = (uint32_t)__ballot(mine >= 0) & 0xffffu; // rows whose adapter has not had its turn
+    uint32_t done = 0;                                       // rows that this block computes
+    v4f h0 = v4f{0, 0, 0, 0}, h1 = v4f{0, 0, 0, 0};
+    for (int nth = 0; left; ++nth) {
+        const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
+        const uint32_t rows = (uint32_t)__ballot(mine == ad) & 0xffffu;
+        left &= ~rows;
+        if (nth % nths != nth0) continue;
+        if (!done && steps <= stride * U) load_x(first);
+        done |= rows;
         const rsrc_t ra = make_rsrc(a.A + (int64_t)ad * a.r * a.K, (int64_t)a.r * KB);
         const int j0 = g * 32 + r16, j1 = j0 + 16;
         const uint32_t o0 = j0 < a.r ? (uint32_t)j0 * KB : kOOB, o1 = j1 < a.r ? (uint32_t)j1 * KB : kOOB;
         v4f acc[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
-        constexpr int U = 8;
-        for (int st = wave; st < steps; st += 16 * U) {
-            u32x4 x[U], p0[U], p1[U];
+        for (int st = first; st < steps; st += stride * U) {
+            if (steps > stride * U) load_x(st);
 #pragma unroll
             for (int q = 0; q < U; ++q) {
-                const uint32_t kb = (uint32_t)(st + 16 * q) * 64 + c16;
-                const bool in = kb < KB;
-                x[q] = bload16(rx, in ? ox + kb : kOOB);
-                p0[q] = bload16(ra, in ? o0 + kb : kOOB);
+                const uint32_t kb = (uint32_t)(st + stride * q) * 64 + c16;
+                p0[q] = bload16(ra, kb < KB ? o0 + kb : kOOB);
             }
             if (wide32) {
 #pragma unroll
                 for (int q = 0; q < U; ++q) {
-                    const uint32_t kb = (uint32_t)(st + 16 * q) * 64 + c16;
+                    const uint32_t kb = (uint32_t)(st + stride * q) * 64 + c16;
                     p1[q] = bload16(ra, kb < KB ? o1 + kb : kOOB);
                 }
             }
@@ -240,43 +338,25 @@ __global__ __launch_bounds__(1024) void k_lora_down_tile(LoraArgs a) {
                 for (int q = 0; q < U; ++q) acc[1] = mfma16<BF>(p1[q], x[q], acc[1]);
             }
         }
-        part[wave][0][lane] = acc[0];
-        part[wave][1][lane] = acc[1];
-        __syncthreads();
-        if (threadIdx.x < 128) {
-            const int f = threadIdx.x >> 6, ln = threadIdx.x & 63, row = ln & 15;
-            v4f c = part[0][f][ln];
+        const float al = a.alpha[ad];
 #pragma unroll
-            for (int w = 1; w < 16; ++w) c += part[w][f][ln];
-            const float al = a.alpha[ad];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) hrow[row][f * 16 + 4 * (ln >> 4) + q] = c[q] * al;
+        for (int q = 0; q < 4; ++q) {
+            h0[q] = mine == ad ? acc[0][q] * al : h0[q];
+            h1[q] = mine == ad ? acc[1][q] * al : h1[q];
         }
-        __syncthreads();
-        // hi + lo = h 2^-e with the row's largest |h| in [2^7, 2^8)
-        if (threadIdx.x < 512) {
-            const int row = threadIdx.x >> 5, j = threadIdx.x & 31;
-            const int64_t m = m0 + row;
-            const float v = hrow[row][j];
-            float mx = __builtin_fabsf(v);
+    }
+    if (!done) return;
+    part[wave][0][lane] = h0;
+    part[wave][1][lane] = h1;
+    __syncthreads();
+    if (threadIdx.x < 128) {
+        const int f = threadIdx.x >> 6, ln = threadIdx.x & 63;
+        const int64_t m = m0 + (ln & 15);
+        v4f c = part[0][f][ln];
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 32));
-            // 2^e from the exponent bits, kept within normal numbers; an
-            // infinite or NaN row keeps its values
-            const uint32_t ex = (__builtin_bit_cast(uint32_t, mx) >> 23) & 0xff;
-            const int sh = ex == 0xff || mx == 0.0f ? 0 : clampi((int)ex - 127 - 7, -120, 120);
-            const float up = __builtin_bit_cast(float, (uint32_t)(127 + sh) << 23);
-            const float t = v * __builtin_bit_cast(float, (uint32_t)(127 - sh) << 23);
-            if (m >= b && m < e) {
-                const uint16_t hi = BF ? f2bf(t) : f2h(t);
-                const uint16_t lo = BF ? f2bf(t - wide(hi, true)) : f2h(t - h2f(hi));
-                uint16_t* o = a.h16 + ((int64_t)g * a.M + m) * 64 + j;
-                o[0] = hi;
-                o[32] = lo;
-                if (j == 0) a.hs[(int64_t)g * a.M + m] = up;
-            }
-        }
-        __syncthreads();
+        for (int w = 1; w < 4; ++w) c += part[w][f][ln];
+        if (done >> (ln & 15) & 1)
+            *reinterpret_cast<v4f*>(a.hp + (((int64_t)z * groups + g) * a.M + m) * 32 + f * 16 + 4 * (ln >> 4)) = c;
     }
 }
 
@@ -289,75 +369,139 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
     const rsrc_t ra = make_rsrc(a.Xq + m0 * a.K, (a.M - m0) * a.K);
     const rsrc_t rw = make_rsrc(a.Wq + n0 * a.K, (a.N - n0) * a.K);
     const uint32_t K = (uint32_t)a.K;
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int r16 = lane & 15, q16 = lane >> 4;
+    const int64_t mw = m0 + (wave / C::WN) * C::TM, nw = n0 + (wave % C::WN) * C::TN;   // the wave's tile
+    int ad[C::FM];                                           // requested before the product, as are the row scales
+    float sx[C::FM];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+        const int64_t m = mw + i * 16 + r16;
+        ad[i] = m < a.M ? a.ad[m] : -1;
+        sx[i] = m < a.M ? a.s_x[m] : 0.0f;
+    }
     v4i acc[C::FM][C::FN];
     tile::product<C>(
         ra, rw, K, smem, [&](int r) -> uint32_t { return m0 + r < a.M ? (uint32_t)r * K : kOOB; },
         [&](int r) -> uint32_t { return n0 + r < a.N ? (uint32_t)r * K : kOOB; }, acc);
-    const int lane = threadIdx.x & 63, wave = wave_id();
-    const int r16 = lane & 15, q16 = lane >> 4;
-    const int64_t mw = m0 + (wave / C::WN) * C::TM, nw = n0 + (wave % C::WN) * C::TN;   // the wave's tile
-    v4f o[C::FM][C::FN];
-    {
-        float sx[C::FM];
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i) sx[i] = mw + i * 16 + r16 < a.M ? a.s_x[mw + i * 16 + r16] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
-            float sw[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t n = nw + j * 16 + 4 * q16 + q;
-                sw[q] = n < a.N ? a.s_w[n] : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) o[i][j][q] = (float)acc[i][j][q] * sx[i] * sw[q];
-        }
-    }
-    // the adapters of the requests in the wave's rows
-    const int64_t me = mw + C::TM < a.M ? mw + C::TM : a.M;
+    // The adapters' part, 32 ranks at a time: the tile's rows of h (hi and lo) into
+    // the freed LDS, 16-byte chunk c of row r at c ^ (r & 7), with their scales; then the distinct adapters of
+    // the wave's rows in turn, the next one's rows of B in flight while one is
+    // multiplied.  A row takes the product of its own adapter alone.
+    constexpr int HC = C::BM * 8 / C::THREADS;               // quads of ranks of h per thread
+    static_assert(HC * C::THREADS == C::BM * 8 && C::BM * 132 <= C::LDS, "h of the tile");
     const int groups = (a.r + 31) / 32;
-    if (mw < me) {
-        int s = request_of(a, mw);
-        for (s = s < 0 ? 0 : s; s < a.R; ++s) {
-            const int64_t sb = a.seg[s], se = a.seg[s + 1];
-            if (sb >= me) break;
-            const int ad = __builtin_amdgcn_readfirstlane(adapter(a, s));
-            if (se <= mw || se <= sb || ad < 0) continue;
-            for (int g = 0; g < groups; ++g) {
-                const rsrc_t rb = make_rsrc(a.B + ((int64_t)ad * a.N + nw) * a.r, (a.N - nw) * a.r * 2);
-                u32x4 bf[C::FN];
-                const int k8 = g * 32 + q16 * 8;             // the lane's ranks
+    const rsrc_t none = make_rsrc(a.B, 0);
+    v4f hc[HC];
+    u32x4 b0[C::FN], b1[C::FN];
+    bool left[C::FM];
+    auto next = [&]() __attribute__((always_inline)) {       // an adapter that has not had its turn, or -1
+        int w = -1;
+#pragma unroll
+        for (int i = C::FM - 1; i >= 0; --i) {
+            const uint64_t b = __ballot(left[i]);
+            if (b) w = __builtin_amdgcn_readlane(ad[i], (int)__builtin_ctzll(b));
+        }
+        return w;
+    };
+    auto load_b = [&](int w, int g, u32x4* b) __attribute__((always_inline)) {
+        const rsrc_t rb = w >= 0 ? make_rsrc(a.B + ((int64_t)w * a.N + nw) * a.r, (a.N - nw) * a.r * 2) : none;
+        const int k8 = g * 32 + q16 * 8;                     // the lane's ranks
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+            b[j] = bload16(rb, k8 < a.r ? (uint32_t)((j * 16 + r16) * a.r + k8) * 2 : kOOB);
+    };
+    int cur = -1;
+    auto request = [&](int g) __attribute__((always_inline)) {               // what group g needs first
+#pragma unroll
+        for (int q = 0; q < HC; ++q) hc[q] = v4f{0, 0, 0, 0};
+        for (int z = 0; z < a.splits; ++z) {                 // (rows without an adapter hold anything)
+            const rsrc_t rh = make_rsrc(a.hp + (((int64_t)z * groups + g) * a.M + m0) * 32, (a.M - m0) * 128);
+#pragma unroll
+            for (int q = 0; q < HC; ++q)
+                hc[q] += __builtin_bit_cast(v4f, bload16(rh, (uint32_t)(q * C::THREADS + threadIdx.x) * 16));
+        }
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) left[i] = ad[i] >= 0;
+        cur = next();
+        load_b(cur, g, b0);
+    };
+    request(0);
+    v4f o[C::FM][C::FN];
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+        float sw[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int64_t n = nw + j * 16 + 4 * q16 + q;
+            sw[q] = n < a.N ? a.s_w[n] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[i][j][q] = (float)acc[i][j][q] * sx[i] * sw[q];
+    }
+    float* ups = reinterpret_cast<float*>(smem + C::BM * 128);               // 2^e of a row
+    for (int g = 0; g < groups; ++g) {
+        if (g > 0) {
+            request(g);
+            __syncthreads();                                 // the last group's h has been read
+        }
+#pragma unroll
+        for (int q = 0; q < HC; ++q) {
+            // thread: 4 ranks of row r; the row's largest |h| over its 8 threads, 2^e
+            // from its exponent bits with hi in [2^7, 2^8), kept within normal
+            // numbers; an infinite or NaN row keeps its values
+            const int P = q * C::THREADS + threadIdx.x, r = P >> 3, c = P & 7;
+            float mx = fmaxf(fmaxf(__builtin_fabsf(hc[q][0]), __builtin_fabsf(hc[q][1])),
+                             fmaxf(__builtin_fabsf(hc[q][2]), __builtin_fabsf(hc[q][3])));
+#pragma unroll
+            for (int o = 4; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, QA_WAVE));
+            const uint32_t ex = (__builtin_bit_cast(uint32_t, mx) >> 23) & 0xff;
+            const int sh = ex == 0xff || mx == 0.0f ? 0 : clampi((int)ex - 127 - 7, -120, 120);
+            const float down = __builtin_bit_cast(float, (uint32_t)(127 - sh) << 23);
+            uint16_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float t = hc[q][e] * down;
+                hi[e] = BF ? f2bf(t) : f2h(t);
+                lo[e] = BF ? f2bf(t - wide(hi[e], true)) : f2h(t - h2f(hi[e]));
+            }
+            uint8_t* row = smem + r * 128 + (c & 1) * 8;
+            *reinterpret_cast<u32x2*>(row + (((c >> 1) ^ (r & 7)) << 4)) =
+                u32x2{hi[0] | ((uint32_t)hi[1] << 16), hi[2] | ((uint32_t)hi[3] << 16)};
+            *reinterpret_cast<u32x2*>(row + ((((c >> 1) + 4) ^ (r & 7)) << 4)) =
+                u32x2{lo[0] | ((uint32_t)lo[1] << 16), lo[2] | ((uint32_t)lo[3] << 16)};
+            if (c == 0) ups[r] = __builtin_bit_cast(float, (uint32_t)(127 + sh) << 23);
+        }
+        __syncthreads();
+        while (cur >= 0) {
+            bool mine[C::FM];
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) {
+                mine[i] = ad[i] == cur;
+                left[i] = left[i] && !mine[i];
+            }
+            const int nxt = next();
+            load_b(nxt, g, b1);
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) {
+                if (!__any(mine[i])) continue;
+                const int r = (wave / C::WN) * C::TM + i * 16 + r16;
+                const float up = ups[r];
+                const u32x4 hi = *reinterpret_cast<const u32x4*>(smem + r * 128 + ((q16 ^ (r & 7)) << 4));
+                const u32x4 lo = *reinterpret_cast<const u32x4*>(smem + r * 128 + (((q16 + 4) ^ (r & 7)) << 4));
 #pragma unroll
                 for (int j = 0; j < C::FN; ++j) {
-                    const int64_t n = nw + j * 16 + r16;
-                    bf[j] = bload16(rb, n < a.N && k8 < a.r ? (uint32_t)((j * 16 + r16) * a.r + k8) * 2 : kOOB);
-                }
+                    v4f d = mfma16<BF>(b0[j], lo, v4f{0, 0, 0, 0});
+                    d = mfma16<BF>(b0[j], hi, d);
 #pragma unroll
-                for (int i = 0; i < C::FM; ++i) {
-                    if (mw + i * 16 + 16 <= sb || mw + i * 16 >= se) continue;
-                    const int64_t m = mw + i * 16 + r16;
-                    const bool mine = m >= sb && m < se && m < a.M;
-                    const uint16_t* hp = a.h16 + ((int64_t)g * a.M + (mine ? m : 0)) * 64 + q16 * 8;
-                    u32x4 hi{0, 0, 0, 0}, lo{0, 0, 0, 0};
-                    float up = 0.0f;
-                    if (mine) {
-                        hi = *reinterpret_cast<const u32x4*>(hp);
-                        lo = *reinterpret_cast<const u32x4*>(hp + 32);
-                        up = a.hs[(int64_t)g * a.M + m];
-                    }
-#pragma unroll
-                    for (int j = 0; j < C::FN; ++j) {
-                        v4f d = mfma16<BF>(bf[j], lo, v4f{0, 0, 0, 0});
-                        d = mfma16<BF>(bf[j], hi, d);
-                        // a row of another request has zeros here, unless its
-                        // neighbour's adapter is infinite: it is left as it is
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) o[i][j][q] = mine ? __builtin_fmaf(d[q], up, o[i][j][q]) : o[i][j][q];
-                    }
+                    for (int q = 0; q < 4; ++q) o[i][j][q] = mine[i] ? __builtin_fmaf(d[q], up, o[i][j][q]) : o[i][j][q];
                 }
             }
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) b0[j] = b1[j];
+            cur = nxt;
         }
     }
 #pragma unroll
@@ -379,10 +523,15 @@ constexpr int64_t FEW = 64;                                  // tokens of the on
 constexpr size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 }  // namespace
 
-size_t lora_scratch_bytes(int64_t M, int64_t r) {
-    if (M <= FEW) return up256((size_t)M * (size_t)r * 4);
-    const size_t groups = (size_t)(r + 31) / 32;
-    return up256(groups * (size_t)M * 128) + up256(groups * (size_t)M * 4);
+// Parts of K in k_lora_down_tile: 1024 columns to a block, so that its 4 waves
+// have all their loads in flight at once; at most 8, since every column tile of
+// the second launch sums them.
+static int lora_splits(int64_t K) { return (int)(K >= 8192 ? 8 : (K + 1023) / 1024); }
+
+size_t lora_scratch_bytes(int64_t M, int64_t K, int64_t r) {
+    const size_t ad = up256((size_t)M * 4);
+    if (M <= FEW) return ad + up256((size_t)M * (size_t)r * 4);
+    return ad + up256((size_t)lora_splits(K) * ((size_t)(r + 31) / 32) * (size_t)M * 128);
 }
 
 template <class C, bool BF>
@@ -402,18 +551,30 @@ static hipError_t run_lora(const LoraArgs& a, hipStream_t st) {
         hipLaunchKernelGGL(k_lora_down_token<BF>, dim3((unsigned)a.M), dim3(1024), 0, st, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         const unsigned nb = (unsigned)((a.N + 15) / 16);
-        if (a.M <= 16) hipLaunchKernelGGL((k_lora_stream<1, BF>), dim3(nb, 1), dim3(512), 0, st, a);
-        else if (a.M <= 32) hipLaunchKernelGGL((k_lora_stream<2, BF>), dim3(nb, 1), dim3(512), 0, st, a);
-        else hipLaunchKernelGGL((k_lora_stream<4, BF>), dim3(nb, 1), dim3(512), 0, st, a);
+        if (a.M <= 16) hipLaunchKernelGGL((k_lora_stream<1, BF>), dim3(nb), dim3(512), 0, st, a);
+        else if (a.M <= 32) hipLaunchKernelGGL((k_lora_stream<2, BF>), dim3(nb), dim3(512), 0, st, a);
+        else hipLaunchKernelGGL((k_lora_stream<4, BF>), dim3(nb), dim3(512), 0, st, a);
         return hipGetLastError();
     }
-    const unsigned z = a.R > 4 ? 4 : (a.R > 0 ? a.R : 1);
-    hipLaunchKernelGGL(k_lora_down_tile<BF>, dim3((unsigned)((a.M + 15) / 16), (unsigned)((a.r + 31) / 32), z),
-                       dim3(1024), 0, st, a);
+    // Short requests put several adapters into a tile of 16 tokens: then up to four blocks share them.
+    const int64_t share = a.R * 16 > a.M / 2 ? 4 : (a.R * 16 > a.M / 8 ? 2 : 1);
+    hipLaunchKernelGGL(k_lora_down_tile<BF>,
+                       dim3((unsigned)((a.M + 15) / 16), (unsigned)((a.r + 31) / 32 * share), (unsigned)a.splits),
+                       dim3(256), 0, st, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int64_t big = ((a.M + 127) / 128) * ((a.N + 255) / 256);
-    if (big >= 192) return run_lora_tile<tile::Cfg<128, 256, 2, 4, 3>, BF>(a, st);
-    return run_lora_tile<tile::Cfg<64, 128, 2, 2, 3>, BF>(a, st);
+    // By the number of 128 x 128 tiles, at K = 4096, rank 16 (us of the call):
+    //   M x N         tiles   64 x 128   128 x 128   128 x 192
+    //   512 x 4096      128       27.6        36.4        42.1
+    //   1024 x 4096     256       36.6        38.9        43.9
+    //   1536 x 4096     384       52.4        46.3        61.4
+    //   2048 x 4096     512       63.7        53.3        62.7
+    //   1024 x 11008    688       83.0        73.9        64.2
+    //   2048 x 11008   1376        150         124         119
+    // Up to 512 tiles fit the 256 CUs two at a time.
+    const int64_t tiles = ((a.M + 127) / 128) * ((a.N + 127) / 128);
+    if (tiles <= 256) return run_lora_tile<tile::Cfg<64, 128, 2, 4, 3>, BF>(a, st);
+    if (tiles <= 512) return run_lora_tile<tile::Cfg<128, 128, 2, 4, 2>, BF>(a, st);
+    return run_lora_tile<tile::Cfg<128, 192, 2, 4, 2>, BF>(a, st);
 }
 
 hipError_t launch_lora_i8(const int8_t* Xq, const float* s_x, const void* X, bool bf16, int64_t M, int64_t K,
@@ -425,9 +586,11 @@ hipError_t launch_lora_i8(const int8_t* Xq, const float* s_x, const void* X, boo
     a.M = M; a.K = K; a.N = N; a.Wq = Wq; a.s_w = s_w;
     a.A = static_cast<const uint16_t*>(A); a.B = static_cast<const uint16_t*>(B); a.alpha = alpha;
     a.seg = seg; a.which = which; a.r = r; a.L = L; a.R = R;
-    a.h = static_cast<float*>(scratch);
-    a.h16 = static_cast<uint16_t*>(scratch);
-    a.hs = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + up256((size_t)((r + 31) / 32) * (size_t)M * 128));
+    uint8_t* ws = static_cast<uint8_t*>(scratch);
+    a.ad = reinterpret_cast<int32_t*>(ws);
+    ws += up256((size_t)M * 4);
+    a.h = a.hp = reinterpret_cast<float*>(ws);
+    a.splits = lora_splits(K);
     a.out = out; a.dt = out_dtype;
     a.vec = N % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (out_dtype == 0 ? 15 : 7)) == 0;
     return bf16 ? run_lora<true>(a, st) : run_lora<false>(a, st);

@@ -38,7 +38,7 @@ namespace qa {
 
 namespace {
 
-constexpr float NEG = -__builtin_inff();
+constexpr float NEG = -__builtin_inff(), FMAX = 3.4028234663852886e38f;
 constexpr int CAP = 16;                      // values that may reach the bound
 constexpr int MAXK = 32;
 
@@ -70,24 +70,6 @@ __device__ __forceinline__ T reduce(T v, F f) {
 template <int LPT> __device__ __forceinline__ float rmax(float v) { return reduce<LPT>(v, [](float a, float b) { return fmaxf(a, b); }); }
 template <int LPT> __device__ __forceinline__ float rsum(float v) { return reduce<LPT>(v, [](float a, float b) { return a + b; }); }
 template <int LPT> __device__ __forceinline__ int rmin(int v) { return reduce<LPT>(v, [](int a, int b) { return min(a, b); }); }
-
-// exp(x) for x <= 88: the exponent of 2 in two parts, so that the result is off
-// by about the exponential's own rounding whatever the size of x.  (The library
-// function's range handling costs three times as much, once per expert.)
-__device__ __forceinline__ float fexp(float x) {
-    constexpr float L2E = 1.44269502162933349609375f, L2E_LO = 1.925963033500011079e-8f, LN2 = 0.693147182464599609375f;
-    x = fmaxf(x, -104.0f);                                   // exp(-104) is 0 in fp32
-    const float t = x * L2E;
-    const float lo = __builtin_fmaf(x, L2E, -t) + x * L2E_LO;
-    const float e = __builtin_amdgcn_exp2f(t);
-    return __builtin_fmaf(e, lo * LN2, e);
-}
-// 1 / (1 + exp(-x)), with one correction of the reciprocal; below -88 about 2^-127.
-__device__ __forceinline__ float sigmoid(float x) {
-    const float d = 1.0f + fexp(fminf(-x, 88.0f));
-    const float r = __builtin_amdgcn_rcpf(d);
-    return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
-}
 
 // The order of floats as unsigned numbers (no NaN; -0 counts as 0).
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -160,7 +142,7 @@ struct RouteArgs {
     const float* bias;       // or nullptr
     int32_t* ids;
     float* w;
-    int32_t* hist;           // [E][nb] counts per block of tokens
+    int32_t* hist;           // [nb][E] counts per block of tokens
     int32_t* order;          // written here when one block holds every token
     int32_t* offsets;
     int64_t T, ld;
@@ -287,19 +269,21 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
     // the choice goes by the logits themselves
     const bool by_logit = !a.sigmoid && !a.bias && (a.groups == 1 || !a.top2);
     float c[EPL], s[EPL];                                    // chosen by (-inf: not to be chosen), score
-    if (a.vec) {
-        if (l * EPL < a.E) ldv<DT, EPL>(xp + (size_t)l * EPL * (DT == 0 ? 4 : 2), c);
-    } else {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (l * EPL + i < a.E) c[i] = ldx<DT>(xp, l * EPL + i);
-    }
+    for (int i = 0; i < EPL; ++i) c[i] = NEG;
+    if (live) {
+        if (a.vec) {
+            if (l * EPL < a.E) ldv<DT, EPL>(xp + (size_t)l * EPL * (DT == 0 ? 4 : 2), c);
+        } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        // NaN masks; +inf counts as the largest finite value
-        const bool in = live && l * EPL + i < a.E && c[i] == c[i];
-        c[i] = in ? fminf(c[i], 3.4028234663852886e38f) : NEG;
+            for (int i = 0; i < EPL; ++i)
+                if (l * EPL + i < a.E) c[i] = ldx<DT>(xp, l * EPL + i);
+        }
     }
+    // NaN masks (the maximum of NaN and a number is the number); +inf counts as
+    // the largest finite value
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c[i] = fminf(fmaxf(c[i], NEG), FMAX);
     float mx = c[0];
 #pragma unroll
     for (int i = 1; i < EPL; ++i) mx = fmaxf(mx, c[i]);
@@ -312,13 +296,20 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
     } else {
         den = 0.0f;
         const float m0 = mx == NEG ? 0.0f : mx;
+        if (by_logit) {
+            // only the sum is wanted: 2^((x - max) log2 e), whose relative error
+            // grows with max - x, where the term itself vanishes
+            constexpr float L2E = 1.44269502162933349609375f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            s[i] = fexp(c[i] - m0);
-            den += s[i];
-        }
-        den = rsum<LPT>(den);
-        if (!by_logit) {
+            for (int i = 0; i < EPL; ++i) den += __builtin_amdgcn_exp2f((c[i] - m0) * L2E);
+            den = rsum<LPT>(den);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                s[i] = fexp(c[i] - m0);
+                den += s[i];
+            }
+            den = rsum<LPT>(den);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) s[i] = s[i] / den;
         }
@@ -342,11 +333,14 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
     // the bound: the k-th largest of the lanes' maxima
     bool few = false;
     if (LPT == 16 && a.k <= 8) {
-        const int before = count15<1>(top, l, [&](float o, float v, int ol) { return o > v || (o == v && ol < l); });
-        const float bound = reduce<16>(before < a.k ? top : __builtin_inff(), [](float p, float q) { return fminf(p, q); });
+        // (a lane whose maximum fewer than k lanes exceed has one as large as the
+        // k-th largest; the least of those is the bound)
+        const int before = count15<1>(top, l, [](float o, float v, int) { return o > v; });
+        float bound = reduce<16>(before < a.k ? top : FMAX, [](float p, float q) { return fminf(p, q); });
+        bound = fmaxf(bound, -FMAX);                         // masked experts never reach it
         int n = 0;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) n += c[i] >= bound && c[i] != NEG ? 1 : 0;
+        for (int i = 0; i < EPL; ++i) n += c[i] >= bound ? 1 : 0;
         const int upto = prefix16(n);
         const int total = reduce<16>(upto, [](int p, int q) { return max(p, q); });
         few = !__any(total > CAP);
@@ -354,21 +348,27 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
             int at = upto - n;
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (c[i] >= bound && c[i] != NEG) {
-                    ckey[tb][at] = ((uint64_t)ordered(c[i]) << 32) | (uint32_t)(0xffff - (l * EPL + i));
-                    cscore[tb][at] = by_logit ? c[i] : s[i];
+                if (c[i] >= bound) {
+                    ckey[tb][at] = ((uint64_t)__builtin_bit_cast(uint32_t, c[i]) << 32) | (uint32_t)(l * EPL + i);
+                    if (!by_logit) cscore[tb][at] = s[i];
                     ++at;
                 }
             sid[tb][l] = -1;
             wave_sync();
-            const bool mine = l < total;
-            const uint64_t key = mine ? ckey[tb][l] : 0;
+            // one value to a lane, as a number that orders by value and then by
+            // lower index; 0 in the lanes without one
+            const uint64_t mine = ckey[tb][l];
+            const uint32_t e = (uint32_t)mine, bits = (uint32_t)(mine >> 32);
+            const uint64_t key = l < total ? ((uint64_t)ordered(__builtin_bit_cast(float, bits)) << 32) | (0xffffu - e) : 0;
+            wave_sync();
+            ckey[tb][l] = key;
+            wave_sync();
             int rank = 0;
 #pragma unroll
-            for (int o = 0; o < CAP; ++o) rank += o < total && ckey[tb][o] > key ? 1 : 0;
-            if (mine && rank < a.k) {
-                sid[tb][rank] = 0xffff - (int)(key & 0xffff);
-                swt[tb][rank] = cscore[tb][l];
+            for (int o = 0; o < CAP; ++o) rank += ckey[tb][o] > key ? 1 : 0;
+            if (l < total && rank < a.k) {
+                sid[tb][rank] = (int)e;
+                swt[tb][rank] = by_logit ? __builtin_bit_cast(float, bits) : cscore[tb][l];
             }
         }
     }
@@ -420,7 +420,7 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
     }
     __syncthreads();
     if (a.nb > 1) {
-        for (int e = threadIdx.x; e < a.E; e += THREADS) a.hist[(int64_t)e * a.nb + blockIdx.x] = __popcll(mask[e]);
+        for (int e = threadIdx.x; e < a.E; e += THREADS) a.hist[(int64_t)blockIdx.x * a.E + e] = __popcll(mask[e]);
         return;
     }
     // one block holds every token: the experts' starts and the pairs' places here
@@ -456,21 +456,41 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
 }
 
 // Exclusive prefix of an expert's counts over the blocks, in place, and its
-// total: one block per expert, thread t on the `per` blocks from t per.
-__global__ __launch_bounds__(256) void k_route_scan(int32_t* __restrict__ hist, int32_t* __restrict__ total, int32_t nb,
-                                                    int32_t per) {
-    __shared__ int32_t wsum[4];
-    int32_t* h = hist + (int64_t)blockIdx.x * nb;
-    const int64_t b0 = (int64_t)threadIdx.x * per, b1 = min(b0 + per, (int64_t)nb);
-    int s = 0, all;
-    for (int64_t b = b0; b < b1; ++b) s += h[b];
-    int at = block_prefix<256>(s, wsum, &all);
+// total.  A block takes 16 experts (a row's 64 bytes side by side), its threads
+// 64 ranges of `per` rows each.
+__global__ __launch_bounds__(1024) void k_route_scan(int32_t* __restrict__ hist, int32_t* __restrict__ total, int32_t E,
+                                                     int32_t nb, int32_t per) {
+    __shared__ int32_t sums[16][65];
+    const int e = blockIdx.x * 16 + (threadIdx.x & 15), part = threadIdx.x >> 4;
+    const int64_t b0 = (int64_t)part * per, b1 = min(b0 + per, (int64_t)nb);
+    int s = 0;
+    if (e < E) {
+#pragma unroll 8
+        for (int64_t b = b0; b < b1; ++b) s += hist[b * E + e];
+    }
+    sums[threadIdx.x & 15][part] = s;
+    __syncthreads();
+    {
+        const int lane = threadIdx.x & 63, w = wave_id();    // wave w scans expert w's 64 sums
+        const int v = sums[w][lane];
+        int t = v;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int u = __shfl_up(t, o, QA_WAVE);
+            if (lane >= o) t += u;
+        }
+        sums[w][lane] = t - v;
+        if (lane == 63 && blockIdx.x * 16 + w < E) total[blockIdx.x * 16 + w] = t;
+    }
+    __syncthreads();
+    if (e >= E) return;
+    int at = sums[threadIdx.x & 15][part];
+#pragma unroll 8
     for (int64_t b = b0; b < b1; ++b) {
-        const int v = h[b];
-        h[b] = at;
+        const int v = hist[b * E + e];
+        hist[b * E + e] = at;
         at += v;
     }
-    if (threadIdx.x == 0) total[blockIdx.x] = all;
 }
 
 // Every pair of the block's tokens to its place: expert start + the expert's
@@ -478,7 +498,7 @@ __global__ __launch_bounds__(256) void k_route_scan(int32_t* __restrict__ hist, 
 template <int TB>
 __global__ __launch_bounds__(512) void k_route_scatter(const int32_t* __restrict__ ids, const int32_t* __restrict__ pre,
                                                        const int32_t* __restrict__ total, int64_t T, int32_t E,
-                                                       int32_t k, int32_t nb, int32_t* __restrict__ order,
+                                                       int32_t k, int32_t* __restrict__ order,
                                                        int32_t* __restrict__ offsets) {
     constexpr int RT = 512, PP = (TB * MAXK + RT - 1) / RT;  // pairs per thread
     extern __shared__ uint8_t smem[];
@@ -493,11 +513,10 @@ __global__ __launch_bounds__(512) void k_route_scatter(const int32_t* __restrict
         const int p = threadIdx.x + i * RT;
         id[i] = p < np ? ids[p0 + p] : -1;
     }
-    // thread t takes experts 2t, 2t + 1
-    const int e0 = threadIdx.x * 2;
+    const int e0 = threadIdx.x * 2;                          // thread t takes experts 2t, 2t + 1
     const int v0 = e0 < E ? total[e0] : 0, v1 = e0 + 1 < E ? total[e0 + 1] : 0;
-    const int q0 = e0 < E ? pre[(int64_t)e0 * nb + blockIdx.x] : 0;
-    const int q1 = e0 + 1 < E ? pre[(int64_t)(e0 + 1) * nb + blockIdx.x] : 0;
+    const int q0 = e0 < E ? pre[(int64_t)blockIdx.x * E + e0] : 0;
+    const int q1 = e0 + 1 < E ? pre[(int64_t)blockIdx.x * E + e0 + 1] : 0;
     for (int e = threadIdx.x; e < E; e += RT) mask[e] = 0;
     int all;
     const int st = block_prefix<RT>(v0 + v1, wsum, &all);    // its barrier also ends the clearing
@@ -528,14 +547,15 @@ __global__ void k_route_none(int32_t* offsets, int32_t E) {
 }
 
 // Tokens per block.  A block is one pass over its tokens, so few tokens want
-// small blocks (4096 x 256: 16 tokens fill 256 blocks, 64 tokens only 64); many
-// want few counts to scan.  Up to 64 tokens one block of 64 does the grouping
-// as well, without the other two launches.
-static int route_tb(int64_t T) { return T <= 64 || T > 16384 ? 64 : 16; }
+// small blocks (4096 x 256: 16 tokens fill 256 blocks, 64 tokens only 64: 12.3
+// against 19.8 us of the first launch); many want few counts to scan (50001 x 128:
+// 32.7 against 33.5 us for the call).  Up to 64 tokens one block of 64 does the
+// grouping as well, without the other two launches.  Above 256 experts a token
+// takes a whole wave, 16 to a block.
+static int route_tb(int64_t T, int64_t E) { return E <= 256 && (T <= 64 || T > 16384) ? 64 : 16; }
 
 size_t route_scratch_bytes(int64_t T, int64_t E) {
-    const int64_t tb = E > 256 ? 16 : route_tb(T);
-    const int64_t nb = (T + tb - 1) / tb;
+    const int64_t tb = route_tb(T, E), nb = (T + tb - 1) / tb;
     return (size_t)(E * nb + E) * 4;
 }
 
@@ -574,7 +594,7 @@ hipError_t launch_route(const void* x, int dtype, int64_t T, int64_t E, int64_t 
         hipLaunchKernelGGL(k_route_none, dim3(1), dim3(256), 0, st, offsets, (int32_t)E);
         return hipGetLastError();
     }
-    const int tb = E > 256 ? 16 : route_tb(T);
+    const int tb = route_tb(T, E);
     const int nb = (int)((T + tb - 1) / tb);
     int32_t* hist = static_cast<int32_t*>(scratch);
     int32_t* total = hist + E * nb;
@@ -583,14 +603,15 @@ hipError_t launch_route(const void* x, int dtype, int64_t T, int64_t E, int64_t 
     hipError_t e = dtype == 0 ? route_by_experts<0>(a, tb, st)
                               : (dtype == 1 ? route_by_experts<1>(a, tb, st) : route_by_experts<2>(a, tb, st));
     if (e != hipSuccess || nb == 1) return e;
-    hipLaunchKernelGGL(k_route_scan, dim3((unsigned)E), dim3(256), 0, st, hist, total, nb, (nb + 255) / 256);
+    hipLaunchKernelGGL(k_route_scan, dim3((unsigned)((E + 15) / 16)), dim3(1024), 0, st, hist, total, (int32_t)E, nb,
+                       (nb + 63) / 64);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (tb == 64)
         hipLaunchKernelGGL(k_route_scatter<64>, dim3(nb), dim3(512), (size_t)E * 12, st, ids, hist, total, T, (int32_t)E,
-                           k, nb, order, offsets);
+                           k, order, offsets);
     else
         hipLaunchKernelGGL(k_route_scatter<16>, dim3(nb), dim3(512), (size_t)E * 12, st, ids, hist, total, T, (int32_t)E,
-                           k, nb, order, offsets);
+                           k, order, offsets);
     return hipGetLastError();
 }
 

@@ -928,7 +928,7 @@ qa_status qa_experts_int8(const int8_t* Xq, const float* s_x, int64_t T, int64_t
 // ----------------------------------------------------------------- adapters
 size_t qa_qlinear_int8_lora_workspace(int64_t M, int64_t K, int32_t r) {
     if (M < 0 || M > kMaxI32 || K <= 0 || r < 8 || r > kMaxRank || r % 8 != 0) return 0;
-    return up(qa::lora_scratch_bytes(M, r));
+    return up(qa::lora_scratch_bytes(M, K, r));
 }
 
 qa_status qa_qlinear_int8_lora(const int8_t* Xq, const float* s_x, const void* X, qa_dtype dtype, int64_t M,

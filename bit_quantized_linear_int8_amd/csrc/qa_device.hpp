@@ -263,4 +263,22 @@ __device__ __forceinline__ float absmax8f(const float* x) {
     return a;
 }
 
+// exp(x) for x <= 88: the exponent of 2 in two parts, so that the result is off
+// by about the exponential's own rounding whatever the size of x.  (The library
+// function's range handling costs three times as much.)
+__device__ __forceinline__ float fexp(float x) {
+    constexpr float L2E = 1.44269502162933349609375f, L2E_LO = 1.925963033500011079e-8f, LN2 = 0.693147182464599609375f;
+    x = fmaxf(x, -104.0f);                                   // exp(-104) is 0 in fp32
+    const float t = x * L2E;
+    const float lo = __builtin_fmaf(x, L2E, -t) + x * L2E_LO;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(e, lo * LN2, e);
+}
+// 1 / (1 + exp(-x)), with one correction of the reciprocal; below -88 about 2^-127.
+__device__ __forceinline__ float sigmoid(float x) {
+    const float d = 1.0f + fexp(fminf(-x, 88.0f));
+    const float r = __builtin_amdgcn_rcpf(d);
+    return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+
 }  // namespace qa

@@ -223,7 +223,7 @@ hipError_t launch_experts_i8(const int8_t* Xq, const float* s_x, int64_t T, int6
                              void* scratch, hipStream_t st);
 
 // The int8 linear with the low-rank adapters of R requests.
-size_t lora_scratch_bytes(int64_t M, int64_t r);
+size_t lora_scratch_bytes(int64_t M, int64_t K, int64_t r);
 hipError_t launch_lora_i8(const int8_t* Xq, const float* s_x, const void* X, bool bf16, int64_t M, int64_t K,
                           const int8_t* Wq, const float* s_w, int64_t N, const void* A, const void* B,
                           const float* alpha, int r, int L, const int32_t* seg, const int32_t* which, int R, void* out,

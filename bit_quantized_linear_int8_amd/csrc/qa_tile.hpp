@@ -1,14 +1,24 @@
 // qa_tile.hpp -- the int8 tile product shared by the grouped and the adapter
 // linears: acc[FM][FN] = A rows x B rows^T with rows picked by the caller.
 //
-// Both operands are K-contiguous int8 rows.  A stage holds BK = 64 bytes of K
+// Both operands are K-contiguous int8 rows.  A stage holds BK = 128 bytes of K
 // of the tile's BM rows of A followed by its BN rows of B; it is filled by
-// direct global -> LDS loads (one instruction: 64 lanes x 16 bytes = 16 rows),
+// direct global -> LDS loads (one instruction: 64 lanes x 16 bytes = 8 rows),
 // and since every lane names its own address, the rows may come from anywhere:
-// gathered tokens, or gate and up rows in turn.  STAGES stages, all but one in flight.
-// The 16-byte chunk c of row r is stored at chunk c ^ ((r >> 1) & 3), which
+// gathered tokens, or gate and up rows in turn.  STAGES stages, all but one in
+// flight.  The 16-byte chunk c of row r is stored at chunk c ^ (r & 7), which
 // makes the fragment reads of 8 consecutive rows hit 8 different bank groups;
 // the permutation is produced by the chunk that each lane fetches.
+//
+// What bounds it: the loads into LDS and the fragment reads out of it, not the
+// MFMAs (a wave with nothing but fragment reads and MFMAs reaches 3.4 POPS).
+// 64-byte stages fetch every 128-byte line twice from L2, in two stages: at
+// 8192 x 8192 x 4096 a 128 x 128 tile went from 1.61 to 1.97 POPS with 128-byte
+// stages.  Two blocks on a CU overlap one's reads with the other's MFMAs and
+// hide its prologue and epilogue, so the tile is as large as two blocks' LDS
+// allow: 128 x 192 with two stages (80 KB) 2.04 POPS, against 1.81 for 128 x 256
+// (96 KB, one block), and 102 against 118 us at 2048 x 11008 x 4096.  The
+// library's int8 product reaches 2.13 POPS on this card at 8192^3.
 //
 // The MFMA takes B first, so it makes the transposed 16 x 16 tile: lane l,
 // element e of acc[i][j] is row 16 i + l % 16, column 16 j + 4 (l / 16) + e of
@@ -22,19 +32,19 @@ namespace tile {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-template <int BM_, int BN_, int WM_, int WN_, int STAGES_ = 4>
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
 struct Cfg {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN;
-    static constexpr int BK = 64, STAGES = STAGES_, THREADS = 64 * NW;
+    static constexpr int BK = 128, STAGES = STAGES_, THREADS = 64 * NW;
     static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
-    static constexpr int INS = (BM + BN) / 16 / NW;          // load instructions of a wave per stage
+    static constexpr int INS = (BM + BN) / 8 / NW;           // load instructions of a wave per stage
     static constexpr int STAGE = (BM + BN) * BK, LDS = STAGES * STAGE;
     static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "wave tiles are whole fragments");
-    static_assert((BM + BN) % (16 * NW) == 0, "a stage's rows split evenly over the waves");
-    static_assert(STAGES >= 2 && STAGES <= 4, "the waits know one to three stages ahead");
+    static_assert((BM + BN) % (8 * NW) == 0 && BM % 8 == 0, "a stage's rows split evenly over the waves");
+    static_assert(STAGES == 2 || STAGES == 3, "the waits know one or two stages ahead");
 };
 
-__device__ __forceinline__ int swz(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
+__device__ __forceinline__ int swz(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
 // s_waitcnt immediate waiting for vmcnt <= n only (gfx9 encoding)
 constexpr int vmcnt(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
@@ -71,7 +81,7 @@ __device__ __forceinline__ void product(rsrc_t rsa, rsrc_t rsb, uint32_t K, uint
 #pragma unroll
     for (int q = 0; q < C::INS; ++q) {
         const int P = (q * C::NW + wave) * 64 + lane;        // 16-byte chunk of the stage
-        const int r = P >> 2, c = (P & 3) ^ ((r >> 1) & 3);
+        const int r = P >> 3, c = (P & 7) ^ (r & 7);
         const uint32_t base = r < C::BM ? row_a(r) : row_b(r - C::BM);
         off[q] = base == kOOB ? kOOB : base + c * 16;
         ck[q] = c * 16;
@@ -82,7 +92,7 @@ __device__ __forceinline__ void product(rsrc_t rsa, rsrc_t rsb, uint32_t K, uint
         const uint32_t k0 = (uint32_t)kt * C::BK;
 #pragma unroll
         for (int q = 0; q < C::INS; ++q) {
-            const bool a = (q * C::NW + wave) * 16 < C::BM;
+            const bool a = (q * C::NW + wave) * 8 < C::BM;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(a ? rsa : rsb, (lds_void*)(st + (q * C::NW + wave) * 1024), 16,
                                                      k0 + ck[q] < K ? off[q] + k0 : kOOB, 0, 0, 0);
         }
@@ -97,9 +107,7 @@ __device__ __forceinline__ void product(rsrc_t rsa, rsrc_t rsb, uint32_t K, uint
         if (q < nk) issue(q);
     const int c = lane >> 4;
     for (int kt = 0; kt < nk; ++kt) {
-        const int left = nk - 1 - kt;                        // younger stages in flight: at most AHEAD - 1
-        if (AHEAD >= 3 && left >= 2) __builtin_amdgcn_s_waitcnt(vmcnt(2 * C::INS));
-        else if (AHEAD >= 2 && left >= 1) __builtin_amdgcn_s_waitcnt(vmcnt(C::INS));
+        if (AHEAD == 2 && kt + 1 < nk) __builtin_amdgcn_s_waitcnt(vmcnt(C::INS));    // stage kt + 1 may be in flight
         else __builtin_amdgcn_s_waitcnt(vmcnt(0));
         block_barrier();
         // stage kt + AHEAD takes the buffer of stage kt - 1, whose reads every
@@ -107,18 +115,21 @@ __device__ __forceinline__ void product(rsrc_t rsa, rsrc_t rsb, uint32_t K, uint
         if (kt + AHEAD < nk) issue(kt + AHEAD);
         const uint8_t* sa = smem + (kt % C::STAGES) * C::STAGE;
         const uint8_t* sb = sa + C::BM * C::BK;
-        v4i fa[C::FM], fb[C::FN];
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-            fa[i] = *reinterpret_cast<const v4i*>(sa + swz(wm * C::TM + i * 16 + (lane & 15), c));
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-            fb[j] = *reinterpret_cast<const v4i*>(sb + swz(wn * C::TN + j * 16 + (lane & 15), c));
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j)
+        for (int ks = 0; ks < 2; ++ks) {
+            v4i fa[C::FM], fb[C::FN];
 #pragma unroll
             for (int i = 0; i < C::FM; ++i)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+                fa[i] = *reinterpret_cast<const v4i*>(sa + swz(wm * C::TM + i * 16 + (lane & 15), c + 4 * ks));
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+                fb[j] = *reinterpret_cast<const v4i*>(sb + swz(wn * C::TN + j * 16 + (lane & 15), c + 4 * ks));
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        }
     }
     __syncthreads();
 }
