@@ -84,31 +84,51 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& a, int64_t m) {
     return s < 0 || s >= a.R ? -1 : adapter(a, s);
 }
 
-// The same for the 16 tokens from m0: lane l gets that of token m0 + l % 16.
-__device__ __forceinline__ int adapters16(const LoraArgs& a, int64_t m0) {
-    const int lane = threadIdx.x & 63, r = lane & 15;
-    if (a.R == 0) return -1;
-    int s = -1;
-    if (a.R < 256) {
-        int v[4], n = 0;
+// Tokens [b, e) and request (-1: none) of block x of the requests' tiles of 16
+// tokens, requests in order: every wave counts the tiles of 256 requests at a
+// time, four to a lane, and sums them over the lanes.
+__device__ __forceinline__ int tile_of(const LoraArgs& a, int x, int64_t& b, int64_t& e) {
+    const int lane = threadIdx.x & 63;
+    for (int s0 = 0; s0 < a.R; s0 += 256) {
+        int64_t c[5];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = q * 64 <= a.R ? a.seg[min(q * 64 + lane, a.R)] : 0;
-        for (int q = 0; q * 64 <= a.R; ++q) {
-            const int w = v[q];
-            const bool in = q * 64 + lane <= a.R;
-            const uint64_t first = __ballot(in && w <= m0), last = __ballot(in && w <= m0 + 15);
-            n += __popcll(first);
-            for (uint64_t b = last & ~first; b; b &= b - 1)  // starts inside the tile
-                n += __builtin_amdgcn_readlane(w, (int)__builtin_ctzll(b)) <= m0 + r ? 1 : 0;
+        for (int q = 0; q < 5; ++q) c[q] = a.seg[min(s0 + lane * 4 + q, a.R)];
+        int n[4], sum = 0;
+#pragma unroll
+        for (int q = 0; q < 5; ++q) c[q] = c[q] < 0 ? 0 : (c[q] > a.M ? a.M : c[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            n[q] = c[q + 1] > c[q] ? (int)((c[q + 1] - c[q] + 15) >> 4) : 0;
+            sum += n[q];
         }
-        s = n - 1;
-    } else {
-        s = __builtin_amdgcn_readfirstlane(request_of(a, m0));
-        int n = s;
-        for (int i = s + 1; i <= a.R && a.seg[i] <= m0 + 15; ++i) n = a.seg[i] <= m0 + r ? i : n;
-        s = n;
+        int upto = sum;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int u = __shfl_up(upto, o, QA_WAVE);
+            if (lane >= o) upto += u;
+        }
+        const uint64_t in = __ballot(x < upto);
+        if (in) {
+            const int l = (int)__builtin_ctzll(in);          // the lane that holds the request
+            int at = upto - sum, s = -1;
+            int64_t mb = 0, me = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (s < 0 && x < at + n[q]) {
+                    s = s0 + lane * 4 + q;
+                    mb = c[q] + (int64_t)(x - at) * 16;
+                    me = c[q + 1];
+                }
+                at += n[q];
+            }
+            b = __builtin_amdgcn_readlane((int)mb, l);
+            e = __builtin_amdgcn_readlane((int)me, l);
+            e = e < b + 16 ? e : b + 16;
+            return __builtin_amdgcn_readlane(s, l);
+        }
+        x -= __builtin_amdgcn_readlane(upto, 63);
     }
-    return s < 0 || s >= a.R ? -1 : adapter(a, s);
+    return -1;
 }
 
 template <bool BF>
@@ -269,85 +289,65 @@ __global__ __launch_bounds__(512) void k_lora_stream(LoraArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: 16 tokens x 32 ranks per block on MFMA, K split over the blocks
-// z and their 4 waves so that up to 8192 columns are one batch of loads.  The
-// tile's adapters are taken in turn with the tokens' rows kept in registers; a
-// token keeps the products with its own.  The splits are summed, in order, where
-// h is read.
+// Many tokens: up to 16 tokens of one request x 32 ranks per block on MFMA, K
+// split over the blocks z and their 4 waves so that up to 8192 columns are one
+// batch of loads.  (Tiles of 16 tokens across requests, their adapters one after
+// the other, took 18.7 us for 777 tokens of 48 requests at K = 4096, rank 64.)
+// The splits are summed, in order, where h is read.
 // ---------------------------------------------------------------------------
 template <bool BF>
 __global__ __launch_bounds__(256) void k_lora_down_tile(LoraArgs a) {
     __shared__ v4f part[4][2][64];
     const int lane = threadIdx.x & 63, wave = wave_id();
-    const int64_t m0 = (int64_t)blockIdx.x * 16;
-    const int groups = (a.r + 31) / 32;
-    const int g = blockIdx.y % groups, z = blockIdx.z;       // group of 32 ranks, part of K
-    const int nth0 = blockIdx.y / groups, nths = gridDim.y / groups;         // this block's share of the tile's adapters
+    const int g = blockIdx.y, z = blockIdx.z;                // group of 32 ranks, part of K
     const int r16 = lane & 15;
+    if (g == 0 && z == 0 && threadIdx.x < 16) {              // tokens before the first and after the last request
+        const int64_t m = (int64_t)blockIdx.x * 16 + threadIdx.x;
+        if (m < a.M && (a.R == 0 || m < a.seg[0] || m >= a.seg[a.R])) a.ad[m] = -1;
+    }
+    int64_t m0 = 0, m1 = 0;
+    const int s = tile_of(a, blockIdx.x, m0, m1);
+    if (s < 0) return;
+    const int ad = __builtin_amdgcn_readfirstlane(adapter(a, s));
+    if (g == 0 && z == 0 && threadIdx.x < m1 - m0) a.ad[m0 + threadIdx.x] = ad;
+    if (ad < 0) return;
     const uint32_t c16 = (lane >> 4) * 16;
     const uint32_t KB = (uint32_t)a.K * 2;
-    const rsrc_t rx = make_rsrc(a.X + m0 * a.K, (a.M - m0) * a.K * 2);
-    const uint32_t ox = m0 + r16 < a.M ? (uint32_t)r16 * KB : kOOB;
+    const rsrc_t rx = make_rsrc(a.X + m0 * a.K, (m1 - m0) * KB);
+    const rsrc_t ra = make_rsrc(a.A + (int64_t)ad * a.r * a.K, (int64_t)a.r * KB);
+    const uint32_t ox = m0 + r16 < m1 ? (uint32_t)r16 * KB : kOOB;
+    const int j0 = g * 32 + r16, j1 = j0 + 16;
+    const uint32_t o0 = j0 < a.r ? (uint32_t)j0 * KB : kOOB, o1 = j1 < a.r ? (uint32_t)j1 * KB : kOOB;
     const bool wide32 = g * 32 + 16 < a.r;                   // the group's second 16 ranks exist
+    const float al = a.alpha[ad];
     constexpr int U = 8;
     const int steps = (int)((KB + 63) / 64), stride = 4 * a.splits, first = z * 4 + wave;
-    u32x4 x[U], p0[U], p1[U];
-    auto load_x = [&](int st) __attribute__((always_inline)) {
+    v4f acc[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
+    for (int st = first; st < steps; st += stride * U) {
+        u32x4 x[U], p0[U], p1[U];
 #pragma unroll
         for (int q = 0; q < U; ++q) {
             const uint32_t kb = (uint32_t)(st + stride * q) * 64 + c16;
             x[q] = bload16(rx, kb < KB ? ox + kb : kOOB);
+            p0[q] = bload16(ra, kb < KB ? o0 + kb : kOOB);
         }
-    };
-    const int found = adapters16(a, m0);
-    const int mine = m0 + r16 < a.M ? found : -1;
-    if (blockIdx.y == 0 && z == 0 && threadIdx.x < 16 && m0 + r16 < a.M) a.ad[m0 + r16] = mine;
-    uint32_t left = (uint32_t)__ballot(mine >= 0) & 0xffffu; // rows whose adapter has not had its turn
-    uint32_t done = 0;                                       // rows that this block computes
-    v4f h0 = v4f{0, 0, 0, 0}, h1 = v4f{0, 0, 0, 0};
-    for (int nth = 0; left; ++nth) {
-        const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
-        const uint32_t rows = (uint32_t)__ballot(mine == ad) & 0xffffu;
-        left &= ~rows;
-        if (nth % nths != nth0) continue;
-        if (!done && steps <= stride * U) load_x(first);
-        done |= rows;
-        const rsrc_t ra = make_rsrc(a.A + (int64_t)ad * a.r * a.K, (int64_t)a.r * KB);
-        const int j0 = g * 32 + r16, j1 = j0 + 16;
-        const uint32_t o0 = j0 < a.r ? (uint32_t)j0 * KB : kOOB, o1 = j1 < a.r ? (uint32_t)j1 * KB : kOOB;
-        v4f acc[2] = {v4f{0, 0, 0, 0}, v4f{0, 0, 0, 0}};
-        for (int st = first; st < steps; st += stride * U) {
-            if (steps > stride * U) load_x(st);
+        if (wide32) {
 #pragma unroll
             for (int q = 0; q < U; ++q) {
                 const uint32_t kb = (uint32_t)(st + stride * q) * 64 + c16;
-                p0[q] = bload16(ra, kb < KB ? o0 + kb : kOOB);
-            }
-            if (wide32) {
-#pragma unroll
-                for (int q = 0; q < U; ++q) {
-                    const uint32_t kb = (uint32_t)(st + stride * q) * 64 + c16;
-                    p1[q] = bload16(ra, kb < KB ? o1 + kb : kOOB);
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);               // every load in flight before the first use
-#pragma unroll
-            for (int q = 0; q < U; ++q) acc[0] = mfma16<BF>(p0[q], x[q], acc[0]);
-            if (wide32) {
-#pragma unroll
-                for (int q = 0; q < U; ++q) acc[1] = mfma16<BF>(p1[q], x[q], acc[1]);
+                p1[q] = bload16(ra, kb < KB ? o1 + kb : kOOB);
             }
         }
-        const float al = a.alpha[ad];
+        __builtin_amdgcn_sched_barrier(0);                   // every load in flight before the first use
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            h0[q] = mine == ad ? acc[0][q] * al : h0[q];
-            h1[q] = mine == ad ? acc[1][q] * al : h1[q];
+        for (int q = 0; q < U; ++q) acc[0] = mfma16<BF>(p0[q], x[q], acc[0]);
+        if (wide32) {
+#pragma unroll
+            for (int q = 0; q < U; ++q) acc[1] = mfma16<BF>(p1[q], x[q], acc[1]);
         }
     }
-    if (!done) return;
-    part[wave][0][lane] = h0;
-    part[wave][1][lane] = h1;
+    part[wave][0][lane] = acc[0];
+    part[wave][1][lane] = acc[1];
     __syncthreads();
     if (threadIdx.x < 128) {
         const int f = threadIdx.x >> 6, ln = threadIdx.x & 63;
@@ -355,8 +355,8 @@ __global__ __launch_bounds__(256) void k_lora_down_tile(LoraArgs a) {
         v4f c = part[0][f][ln];
 #pragma unroll
         for (int w = 1; w < 4; ++w) c += part[w][f][ln];
-        if (done >> (ln & 15) & 1)
-            *reinterpret_cast<v4f*>(a.hp + (((int64_t)z * groups + g) * a.M + m) * 32 + f * 16 + 4 * (ln >> 4)) = c;
+        if (m < m1)
+            *reinterpret_cast<v4f*>(a.hp + (((int64_t)z * gridDim.y + g) * a.M + m) * 32 + f * 16 + 4 * (ln >> 4)) = c * al;
     }
 }
 
@@ -378,6 +378,7 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
     for (int i = 0; i < C::FM; ++i) {
         const int64_t m = mw + i * 16 + r16;
         ad[i] = m < a.M ? a.ad[m] : -1;
+        if (ad[i] >= a.L) ad[i] = -1;                        // no adapter was written: starts that descend
         sx[i] = m < a.M ? a.s_x[m] : 0.0f;
     }
     v4i acc[C::FM][C::FN];
@@ -556,11 +557,10 @@ static hipError_t run_lora(const LoraArgs& a, hipStream_t st) {
         else hipLaunchKernelGGL((k_lora_stream<4, BF>), dim3(nb), dim3(512), 0, st, a);
         return hipGetLastError();
     }
-    // Short requests put several adapters into a tile of 16 tokens: then up to four blocks share them.
-    const int64_t share = a.R * 16 > a.M / 2 ? 4 : (a.R * 16 > a.M / 8 ? 2 : 1);
+    // upper bound of the requests' tiles: the whole ones and a ragged one each
+    const int64_t most = (a.M + 15) / 16 + (a.R < a.M ? a.R : a.M);
     hipLaunchKernelGGL(k_lora_down_tile<BF>,
-                       dim3((unsigned)((a.M + 15) / 16), (unsigned)((a.r + 31) / 32 * share), (unsigned)a.splits),
-                       dim3(256), 0, st, a);
+                       dim3((unsigned)most, (unsigned)((a.r + 31) / 32), (unsigned)a.splits), dim3(256), 0, st, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     // By the number of 128 x 128 tiles, at K = 4096, rank 16 (us of the call):
     //   M x N         tiles   64 x 128   128 x 128   128 x 192

@@ -77,6 +77,57 @@ __device__ __forceinline__ void st8(void* p, int64_t j0, const float* x) {
     }
 }
 
+// Rows that start anywhere: eight elements from `at`, at their own alignment
+// (the hardware splits accesses that cross a line), moved back to the row's last
+// eight where the row ends before them; shifted() then brings the wanted ones to
+// the front and zeros behind them.  K >= 8.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> ldu8(const uint8_t* row, int64_t at, int64_t K) {
+    Raw8<DT> o;
+    __builtin_memcpy(&o, row + (at < K - 8 ? at : K - 8) * Elem<DT>::BYTES, sizeof(o));
+    return o;
+}
+__device__ __forceinline__ int past(int64_t at, int64_t K) {
+    const int64_t s = at - (K - 8);
+    return s < 0 ? 0 : (s > 8 ? 8 : (int)s);
+}
+__device__ __forceinline__ void shifted(float* x, int s) {
+    if (!__any(s > 0)) return;
+#pragma unroll
+    for (int b = 4; b >= 1; b >>= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = s & b ? (j + b < 8 ? x[j + b] : 0.0f) : x[j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = s >= 8 ? 0.0f : x[j];
+}
+// Store of the elements of eight from `at` that the row has.
+template <int DT>
+__device__ __forceinline__ void stu8(uint8_t* row, int64_t at, int64_t K, const float* x) {
+    if (at + 8 <= K) {
+        if constexpr (DT == 0) {
+            __builtin_memcpy(row + at * 4, x, 32);
+        } else {
+            uint16_t h[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] = DT == 1 ? f2h(x[j]) : f2bf(x[j]);
+            __builtin_memcpy(row + at * 2, h, 16);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (at + j < K) st1<DT>(row, at + j, x[j]);
+}
+__device__ __forceinline__ void stu_codes(int8_t* row, int64_t at, int64_t K, u32x2 c) {
+    if (at + 8 <= K) {
+        __builtin_memcpy(row + at, &c, 8);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (at + j < K) row[at + j] = (int8_t)(c[j >> 2] >> (8 * (j & 3)));
+}
+
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, QA_WAVE);
@@ -120,9 +171,9 @@ struct NormArgs {
     float eps;
 };
 
-// EVEN: K % 8 == 0 and every row of every array starts at a 16-byte boundary,
-// so chunks are loaded and stored whole with range-checked 16-byte loads.
-// Otherwise elements go one by one, consecutive lanes on consecutive elements.
+// EVEN: K % 8 == 0 and every row of every array starts at a 16-byte boundary:
+// range-checked 16-byte loads.  Otherwise the same chunks of eight at any
+// alignment (ldu8).  Lane l of the row owns the chunks l, l + LANES, ...
 template <int DT, int WPR, int NC, bool EVEN>
 __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_rmsnorm_i8(NormArgs a) {
     constexpr int WPB = WPR < 4 ? 4 : WPR;                   // waves per block
@@ -136,10 +187,7 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_rmsnorm_i8(NormArg
     const uint8_t* rp = static_cast<const uint8_t*>(a.R) + rw * a.ldr * Elem<DT>::BYTES;
     const int lp = part * 64 + lane;                         // lane of the row
     constexpr int LANES = 64 * WPR;
-    // element of chunk i, position j
-    auto el = [&](int i, int j) -> int64_t {
-        return EVEN ? ((int64_t)i * LANES + lp) * 8 + j : ((int64_t)i * 8 + j) * LANES + lp;
-    };
+    auto el = [&](int i) -> int64_t { return ((int64_t)i * LANES + lp) * 8; };
     float h[NC][8], g[NC][8];
     if constexpr (EVEN) {
         const rsrc_t rx = make_rsrc(xp, live ? a.K * Elem<DT>::BYTES : 0);
@@ -148,11 +196,11 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_rmsnorm_i8(NormArg
         Raw8<DT> vx[NC], vr[NC], vg[NC];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            vx[i] = bld8<DT>(rx, (uint32_t)el(i, 0), true);
-            vr[i] = bld8<DT>(rr, (uint32_t)el(i, 0), true);
+            vx[i] = bld8<DT>(rx, (uint32_t)el(i), true);
+            vr[i] = bld8<DT>(rr, (uint32_t)el(i), true);
         }
 #pragma unroll
-        for (int i = 0; i < NC; ++i) vg[i] = bld8<DT>(rg, (uint32_t)el(i, 0), true);
+        for (int i = 0; i < NC; ++i) vg[i] = bld8<DT>(rg, (uint32_t)el(i), true);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             float t[8];
@@ -163,16 +211,27 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_rmsnorm_i8(NormArg
             widen8<DT>(vg[i], g[i]);
         }
     } else {
+        Raw8<DT> vx[NC], vr[NC], vg[NC];
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
+        for (int i = 0; i < NC; ++i) {
+            vx[i] = ldu8<DT>(xp, el(i), a.K);
+            if (a.R) vr[i] = ldu8<DT>(rp, el(i), a.K);
+            vg[i] = ldu8<DT>(static_cast<const uint8_t*>(a.g), el(i), a.K);
+        }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t e = el(i, j);
-                const bool in = live && e < a.K;
-                h[i][j] = in ? ld1<DT>(xp, e) : 0.0f;
-                if (a.R) h[i][j] += in ? ld1<DT>(rp, e) : 0.0f;
-                g[i][j] = in ? ld1<DT>(a.g, e) : 0.0f;
+        for (int i = 0; i < NC; ++i) {
+            const int s = past(el(i), a.K);
+            widen8<DT>(vx[i], h[i]);
+            if (a.R) {
+                float t[8];
+                widen8<DT>(vr[i], t);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[i][j] += t[j];
             }
+            shifted(h[i], s);
+            widen8<DT>(vg[i], g[i]);
+            shifted(g[i], s);
+        }
     }
     float ss = 0.0f;
 #pragma unroll
@@ -194,11 +253,9 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_rmsnorm_i8(NormArg
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             if constexpr (EVEN) {
-                if (el(i, 0) < a.K) st8<DT>(o, el(i, 0), h[i]);
+                if (el(i) < a.K) st8<DT>(o, el(i), h[i]);
             } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (el(i, j) < a.K) st1<DT>(o, el(i, j), h[i][j]);
+                stu8<DT>(o, el(i), a.K, h[i]);
             }
         }
     }
@@ -227,25 +284,22 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_rmsnorm_i8(NormArg
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         if constexpr (EVEN) {
-            if (el(i, 0) < a.K) {
-                st_codes8(q + el(i, 0), codes8_any(h[i], s, r, fine));
-                if (a.y) st8<DT>(yo, el(i, 0), h[i]);
+            if (el(i) < a.K) {
+                st_codes8(q + el(i), codes8_any(h[i], s, r, fine));
+                if (a.y) st8<DT>(yo, el(i), h[i]);
             }
         } else {
-            const u32x2 c = codes8_any(h[i], s, r, fine);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (el(i, j) < a.K) {
-                    q[el(i, j)] = (int8_t)(c[j >> 2] >> (8 * (j & 3)));
-                    if (a.y) st1<DT>(yo, el(i, j), h[i][j]);
-                }
+            stu_codes(q, el(i), a.K, codes8_any(h[i], s, r, fine));
+            if (a.y) stu8<DT>(yo, el(i), a.K, h[i]);
         }
     }
 }
 
-// Rows past 16384 values: one block of 16 waves per row, the row read once for
-// each reduction and once for the codes.  The sum is stored in the last pass,
-// by the thread that has just read the element, so it may replace x or r.
+// Rows past 16384 values (and under 8): one block of 16 waves per row, the row
+// read once for each reduction and once for the codes.  The sum is stored in the
+// last pass, by the thread that has just read the elements, so it may replace x
+// or r; a row's last chunk is read element by element, not moved back, so that no
+// other thread's elements are read then.
 template <int DT>
 __global__ __launch_bounds__(1024) void k_rmsnorm_i8_long(NormArgs a) {
     __shared__ float red[16];
@@ -253,11 +307,29 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_i8_long(NormArgs a) {
     const int64_t row = blockIdx.x;
     const uint8_t* xp = static_cast<const uint8_t*>(a.X) + row * a.ldx * Elem<DT>::BYTES;
     const uint8_t* rp = static_cast<const uint8_t*>(a.R) + row * a.ldr * Elem<DT>::BYTES;
-    auto at = [&](int64_t e) { return ld1<DT>(xp, e) + (a.R ? ld1<DT>(rp, e) : 0.0f); };
+    auto load = [&](const void* p, int64_t at, float* x) {
+        if (at + 8 <= a.K) {
+            widen8<DT>(ldu8<DT>(static_cast<const uint8_t*>(p), at, a.K), x);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = at + j < a.K ? ld1<DT>(p, at + j) : 0.0f;
+        }
+    };
+    auto sum8 = [&](int64_t at, float* h) {
+        load(xp, at, h);
+        if (a.R) {
+            float t[8];
+            load(rp, at, t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] += t[j];
+        }
+    };
     float ss = 0.0f;
-    for (int64_t e = threadIdx.x; e < a.K; e += 1024) {
-        const float h = at(e);
-        ss = __builtin_fmaf(h, h, ss);
+    for (int64_t at = threadIdx.x * 8; at < a.K; at += 8192) {
+        float h[8];
+        sum8(at, h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(h[j], h[j], ss);
     }
     ss = wave_sum(ss);
     if (lane == 0) red[wave] = ss;
@@ -269,8 +341,13 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_i8_long(NormArgs a) {
     const float ms = ss / (float)a.K;
     const float rstd = 1.0f / __builtin_sqrtf(ms + a.eps);
     float amax = 0.0f;
-    for (int64_t e = threadIdx.x; e < a.K; e += 1024)
-        amax = fmaxf(amax, __builtin_fabsf(at(e) * rstd * ld1<DT>(a.g, e)));
+    for (int64_t at = threadIdx.x * 8; at < a.K; at += 8192) {
+        float h[8], g[8];
+        sum8(at, h);
+        load(a.g, at, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, __builtin_fabsf(h[j] * rstd * g[j]));
+    }
     amax = wave_max(amax);
     if (lane == 0) red[wave] = amax;
     __syncthreads();
@@ -280,12 +357,15 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_i8_long(NormArgs a) {
     float s, r;
     const bool fine = row_scale(ms, amax, s, r);
     if (threadIdx.x == 0) a.s[row] = s;
-    int8_t* q = a.q + row * a.K;
-    for (int64_t e = threadIdx.x; e < a.K; e += 1024) {
-        const float h = at(e), y = h * rstd * ld1<DT>(a.g, e);
-        if (a.sum) st1<DT>(static_cast<uint8_t*>(a.sum) + row * a.lds * Elem<DT>::BYTES, e, h);
-        if (a.y) st1<DT>(static_cast<uint8_t*>(a.y) + row * a.K * Elem<DT>::BYTES, e, y);
-        q[e] = fine ? (int8_t)__builtin_rintf(y / s) : (int8_t)0;
+    for (int64_t at = threadIdx.x * 8; at < a.K; at += 8192) {
+        float h[8], g[8], y[8];
+        sum8(at, h);
+        load(a.g, at, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = h[j] * rstd * g[j];
+        if (a.sum) stu8<DT>(static_cast<uint8_t*>(a.sum) + row * a.lds * Elem<DT>::BYTES, at, a.K, h);
+        if (a.y) stu8<DT>(static_cast<uint8_t*>(a.y) + row * a.K * Elem<DT>::BYTES, at, a.K, y);
+        stu_codes(a.q + row * a.K, at, a.K, codes8_any(y, s, r, fine));
     }
 }
 
@@ -296,7 +376,8 @@ static void norm_dispatch(const NormArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((k_rmsnorm_i8<DT, WPR, NC, EVEN>),                                                          \
                        dim3((unsigned)((a.rows + (WPR < 4 ? 4 / WPR : 1) - 1) / (WPR < 4 ? 4 / WPR : 1))),        \
                        dim3(WPR < 4 ? 256 : 64 * WPR), 0, st, a)
-    if (nch <= 64) QA_NORM(1, 1);
+    if (a.K < 8) hipLaunchKernelGGL((k_rmsnorm_i8_long<DT>), dim3((unsigned)a.rows), dim3(1024), 0, st, a);
+    else if (nch <= 64) QA_NORM(1, 1);
     else if (nch <= 128) QA_NORM(1, 2);
     else if (nch <= 256) QA_NORM(2, 2);
     else if (nch <= 512) QA_NORM(4, 2);
