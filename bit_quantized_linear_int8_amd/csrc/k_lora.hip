@@ -142,8 +142,8 @@ __device__ __forceinline__ v4f mfma16(u32x4 x, u32x4 y, v4f c) {
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Few tokens: one block per token, its 16 waves on a rank each.  The token's
-// row is requested before its adapter is looked up.
+// Few tokens: a block per token and 16 ranks, a wave on each.  The token's row
+// is requested before its adapter is looked up.
 // ---------------------------------------------------------------------------
 template <bool BF>
 __global__ __launch_bounds__(1024) void k_lora_down_token(LoraArgs a) {
@@ -156,60 +156,66 @@ __global__ __launch_bounds__(1024) void k_lora_down_token(LoraArgs a) {
 #pragma unroll
     for (int q = 0; q < U; ++q) x[q] = bload16(rx, lane * 16 + q * 1024);
     const int ad = adapter_of(a, m);
-    if (threadIdx.x == 0) a.ad[m] = ad;
-    if (ad < 0) return;                                      // its h is not read
-    for (int j = wave; j < a.r; j += 16) {
-        const rsrc_t ra = make_rsrc(a.A + ((int64_t)ad * a.r + j) * a.K, KB);
-        float s = 0.0f;
-        for (uint32_t k = lane * 16; k - lane * 16 < KB; k += U * 1024) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) a.ad[m] = ad;
+    const int j = blockIdx.y * 16 + wave;
+    if (ad < 0 || j >= a.r) return;                          // (without an adapter its h is not read)
+    const rsrc_t ra = make_rsrc(a.A + ((int64_t)ad * a.r + j) * a.K, KB);
+    float s = 0.0f;
+    for (uint32_t k = lane * 16; k - lane * 16 < KB; k += U * 1024) {
 #pragma unroll
-            for (int q = 0; q < U; ++q) w[q] = bload16(ra, k + q * 1024);
-            if (KB > U * 1024) {
+        for (int q = 0; q < U; ++q) w[q] = bload16(ra, k + q * 1024);
+        if (KB > U * 1024) {
 #pragma unroll
-                for (int q = 0; q < U; ++q) x[q] = bload16(rx, k + q * 1024);
-            }
-            __builtin_amdgcn_sched_barrier(0);               // every load in flight before the first use
-#pragma unroll
-            for (int q = 0; q < U; ++q)
-#pragma unroll
-                for (int p = 0; p < 8; ++p)
-                    s = __builtin_fmaf(wide((uint16_t)(x[q][p >> 1] >> (16 * (p & 1))), BF),
-                                       wide((uint16_t)(w[q][p >> 1] >> (16 * (p & 1))), BF), s);
+            for (int q = 0; q < U; ++q) x[q] = bload16(rx, k + q * 1024);
         }
+        __builtin_amdgcn_sched_barrier(0);                   // every load in flight before the first use
 #pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, QA_WAVE);
-        if (lane == 0) a.h[m * a.r + j] = s * a.alpha[ad];
+        for (int q = 0; q < U; ++q)
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+                s = __builtin_fmaf(wide((uint16_t)(x[q][p >> 1] >> (16 * (p & 1))), BF),
+                                   wide((uint16_t)(w[q][p >> 1] >> (16 * (p & 1))), BF), s);
     }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, QA_WAVE);
+    if (lane == 0) a.h[m * a.r + j] = s * a.alpha[ad];
 }
 
 // The int8 product for few tokens: 16 output columns per block, K split over 8
-// waves that bring the weight rows straight into MFMA operands.  Wave t < MT also
-// owns the 16 x 16 outputs of tokens 16 t ..: its tokens' adapters are requested
-// before the weights and the first 16 ranks of B behind them, so that neither
-// waits for the other.
+// waves that bring the weight rows straight into MFMA operands.  The waves also
+// share the adapters' part: wave w has the 16 x 16 outputs of tokens 16 (w % MT) ..
+// and every (8 / MT)-th chunk of 16 ranks from w / MT.  Its tokens' adapters are
+// requested before the weights and its first chunk of B behind them, so that
+// neither waits for the other (with the adapter looked up here and B read after
+// the weights, 9.3 us instead of 7.3 at 16 x 4096 x 4096, rank 16).
 template <int MT, bool BF>
 __global__ __launch_bounds__(512) void k_lora_stream(LoraArgs a) {
     __shared__ v4i part[8][MT][64];
+    __shared__ v4f dpart[8][64];
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     const uint32_t K = (uint32_t)a.K;
     const int r16 = lane & 15, c16 = (lane >> 4) * 16;
-    const int64_t mo = wave * 16 + r16, no = n0 + 4 * (lane >> 4);           // the lane's outputs, if its wave owns any
-    const bool live = wave < MT && mo < a.M && no < a.N;
+    const int j0 = wave / MT * 16;                           // the wave's first rank
+    const int64_t mo = (wave % MT) * 16 + r16, no = n0 + 4 * (lane >> 4);    // the lane's outputs
+    const bool live = mo < a.M && no < a.N;
     const int cols = live ? (int)(a.N - no < 4 ? a.N - no : 4) : 0;
-    int ad = -1;
+    const int ad = live && j0 < a.r ? a.ad[mo] : -1;
+    const bool first = wave < MT && live;                    // this wave also ends its tile
     float sx = 0.0f, sw[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    v4f h[4];
-    if (live) {
-        ad = a.ad[mo];
+    if (first) {
         sx = a.s_x[mo];
 #pragma unroll
         for (int q = 0; q < 4; ++q) sw[q] = a.s_w[no + min(q, cols - 1)];
     }
-    const rsrc_t rh = make_rsrc(a.h, live ? a.M * a.r * 4 : 0);
+    const rsrc_t rh = make_rsrc(a.h, a.M * a.r * 4);         // (rows of tokens without an adapter hold anything)
+    auto load_h = [&](int j, v4f* h) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)                              // not written for a token without an adapter, nor used
-        h[q] = __builtin_bit_cast(v4f, bload16(rh, q * 4 < a.r ? (uint32_t)(mo * a.r + q * 4) * 4 : kOOB));
+        for (int q = 0; q < 4; ++q)
+            h[q] = __builtin_bit_cast(v4f, bload16(rh, live && j + q * 4 < a.r ? (uint32_t)(mo * a.r + j + q * 4) * 4 : kOOB));
+    };
+    v4f h[4];
+    load_h(j0, h);
     const rsrc_t rw = make_rsrc(a.Wq + n0 * a.K, (a.N - n0) * a.K);
     const rsrc_t rx = make_rsrc(a.Xq, a.M * a.K);
     const uint32_t ow = n0 + r16 < a.N ? (uint32_t)r16 * K : kOOB;
@@ -235,16 +241,20 @@ __global__ __launch_bounds__(512) void k_lora_stream(LoraArgs a) {
     };
     __builtin_amdgcn_sched_barrier(0);
     load(wave);
-    u32x4 b[4][2];
-    const bool adapt = live && ad >= 0;
+    const bool adapt = ad >= 0;
     const uint16_t* bp = a.B + ((int64_t)(adapt ? ad : 0) * a.N + (adapt ? no : 0)) * a.r;
-    if (adapt) {
+    auto load_b = [&](int j, u32x4 (*b)[2]) __attribute__((always_inline)) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-                if (q < cols && p * 8 < a.r) b[q][p] = *reinterpret_cast<const u32x4*>(bp + (int64_t)q * a.r + p * 8);
-    }
+            for (int p = 0; p < 2; ++p) {
+                b[q][p] = u32x4{0, 0, 0, 0};
+                if (adapt && q < cols && j + p * 8 < a.r)
+                    b[q][p] = *reinterpret_cast<const u32x4*>(bp + (int64_t)q * a.r + j + p * 8);
+            }
+    };
+    u32x4 b[4][2];
+    load_b(j0, b);
     for (int s = wave; s < nk;) {
 #pragma unroll
         for (int q = 0; q < U; ++q)
@@ -257,31 +267,31 @@ __global__ __launch_bounds__(512) void k_lora_stream(LoraArgs a) {
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) part[wave][m][lane] = acc[m];
-    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto dot8 = [&](const u32x4& v, const v4f& h0, const v4f& h1, float& sum) __attribute__((always_inline)) {
-#pragma unroll
-        for (int p = 0; p < 8; ++p)
-            sum = __builtin_fmaf(p < 4 ? h0[p & 3] : h1[p & 3], wide((uint16_t)(v[p >> 1] >> (16 * (p & 1))), BF), sum);
-    };
-    if (adapt) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-                if (q < cols && p * 8 < a.r) dot8(b[q][p], h[2 * p], h[2 * p + 1], d[q]);
-        for (int j = 16; j < a.r; j += 8) {
-            const float* hp = a.h + mo * a.r + j;
-            const v4f h0 = *reinterpret_cast<const v4f*>(hp), h1 = *reinterpret_cast<const v4f*>(hp + 4);
+    v4f d = v4f{0, 0, 0, 0};
+    for (int j = j0; j < a.r; j += 128 / MT) {
+        if (j != j0) {
+            load_h(j, h);
+            load_b(j, b);
+        }
+        if (adapt)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                if (q < cols) dot8(*reinterpret_cast<const u32x4*>(bp + (int64_t)q * a.r + j), h0, h1, d[q]);
-        }
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    if (j + p * 8 < a.r)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            d[q] = __builtin_fmaf(h[2 * p + (e >> 2)][e & 3],
+                                                  wide((uint16_t)(b[q][p][e >> 1] >> (16 * (e & 1))), BF), d[q]);
     }
+    dpart[wave][lane] = d;
     __syncthreads();
-    if (!live) return;
+    if (!first) return;
     v4i c = part[0][wave][lane];
 #pragma unroll
     for (int p = 1; p < 8; ++p) c += part[p][wave][lane];
+#pragma unroll
+    for (int p = 1; p < 8 / MT; ++p) d += dpart[p * MT + wave][lane];
     float v[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[q] = (float)c[q] * sx * sw[q] + d[q];
@@ -520,7 +530,10 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
 }
 
 namespace {
-constexpr int64_t FEW = 64;                                  // tokens of the one-block-per-token form
+// The form for few tokens, by both sides' times at K = 4096, rank 16: 17.8 us at
+// 64 x 4096 and 27.1 at 32 x 11008 (39.1 at 64), the tiles 29.8 from 65 tokens on.
+constexpr int64_t FEW = 64;
+bool few_tokens(int64_t M, int64_t N) { return M <= 32 || (M <= FEW && N <= 8192); }
 constexpr size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 }  // namespace
 
@@ -531,7 +544,7 @@ static int lora_splits(int64_t K) { return (int)(K >= 8192 ? 8 : (K + 1023) / 10
 
 size_t lora_scratch_bytes(int64_t M, int64_t K, int64_t r) {
     const size_t ad = up256((size_t)M * 4);
-    if (M <= FEW) return ad + up256((size_t)M * (size_t)r * 4);
+    // (the form for few tokens needs less: M r floats)
     return ad + up256((size_t)lora_splits(K) * ((size_t)(r + 31) / 32) * (size_t)M * 128);
 }
 
@@ -548,8 +561,8 @@ static hipError_t run_lora_tile(const LoraArgs& a, hipStream_t st) {
 template <bool BF>
 static hipError_t run_lora(const LoraArgs& a, hipStream_t st) {
     hipError_t e;
-    if (a.M <= FEW) {
-        hipLaunchKernelGGL(k_lora_down_token<BF>, dim3((unsigned)a.M), dim3(1024), 0, st, a);
+    if (few_tokens(a.M, a.N)) {
+        hipLaunchKernelGGL(k_lora_down_token<BF>, dim3((unsigned)a.M, (unsigned)((a.r + 15) / 16)), dim3(1024), 0, st, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         const unsigned nb = (unsigned)((a.N + 15) / 16);
         if (a.M <= 16) hipLaunchKernelGGL((k_lora_stream<1, BF>), dim3(nb), dim3(512), 0, st, a);
