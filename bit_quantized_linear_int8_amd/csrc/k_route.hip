@@ -24,7 +24,11 @@
 // that the k chosen reach (k lanes hold a value as large), and few others do:
 // the values that reach it go to LDS, one to a lane, and a value's rank among
 // them is its slot.  Only where more than 16 reach it (k > 8, many ties) the
-// rounds are run.  Measured at 50001 x 128, k = 8: see launch_route.
+// rounds are run.  First launch at 50001 x 128 (bf16, k = 8): 28.8 us with the
+// rounds, 18.6 with the bound; at 4096 x 256 in 8 groups 34 and 9.1.  At 50001
+// tokens it issues 415 vector instructions per wave of four tokens, 9 us of the
+// SIMDs' time; reading the logits is 2.5 us.  32 tokens to a block run it in 14.8
+// us, but the counts of twice the blocks cost that again in the two launches after.
 //
 // The grouping is stable (ascending pair index within an expert) and uses no
 // order-dependent atomics: a token chooses an expert at most once, so a block of
@@ -132,6 +136,17 @@ __device__ __forceinline__ int count15(float v, int l, F f) {
         // row_ror:N hands lane l the value of lane (l - N) mod 16
         const float o = __builtin_bit_cast(float, ror16<N>(__builtin_bit_cast(int, v)));
         return (f(o, v, (l + 16 - N) & 15) ? 1 : 0) + count15<N + 1>(v, l, f);
+    }
+}
+
+// How many of the other 15 lanes' m1 and m2 are larger than v.
+template <int N>
+__device__ __forceinline__ int count15x2(float m1, float m2, float v) {
+    if constexpr (N == 16) return 0;
+    else {
+        const float a = __builtin_bit_cast(float, ror16<N>(__builtin_bit_cast(int, m1)));
+        const float b = __builtin_bit_cast(float, ror16<N>(__builtin_bit_cast(int, m2)));
+        return (a > v ? 1 : 0) + (b > v ? 1 : 0) + count15x2<N + 1>(m1, m2, v);
     }
 }
 
@@ -335,8 +350,22 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
     if (LPT == 16 && a.k <= 8) {
         // (a lane whose maximum fewer than k lanes exceed has one as large as the
         // k-th largest; the least of those is the bound)
-        const int before = count15<1>(top, l, [](float o, float v, int) { return o > v; });
-        float bound = reduce<16>(before < a.k ? top : FMAX, [](float p, float q) { return fminf(p, q); });
+        auto more = [](float o, float v, int) { return o > v; };
+        float least = FMAX;
+        if (a.groups == 1) {
+            if (count15<1>(top, l, more) < a.k) least = top;
+        } else {
+            // the kept groups' experts lie in few lanes: the lanes' two largest
+            float m1 = NEG, m2 = NEG;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                m2 = fmaxf(m2, fminf(m1, c[i]));
+                m1 = fmaxf(m1, c[i]);
+            }
+            if (count15x2<1>(m1, m2, m1) < a.k) least = m1;
+            if (count15x2<1>(m1, m2, m2) + (m1 > m2 ? 1 : 0) < a.k) least = m2;
+        }
+        float bound = reduce<16>(least, [](float p, float q) { return fminf(p, q); });
         bound = fmaxf(bound, -FMAX);                         // masked experts never reach it
         int n = 0;
 #pragma unroll
@@ -463,10 +492,13 @@ __global__ __launch_bounds__(1024) void k_route_scan(int32_t* __restrict__ hist,
     __shared__ int32_t sums[16][65];
     const int e = blockIdx.x * 16 + (threadIdx.x & 15), part = threadIdx.x >> 4;
     const int64_t b0 = (int64_t)part * per, b1 = min(b0 + per, (int64_t)nb);
-    int s = 0;
-    if (e < E) {
-#pragma unroll 8
-        for (int64_t b = b0; b < b1; ++b) s += hist[b * E + e];
+    constexpr int V = 16;                                    // counts kept: up to 1024 blocks are read once
+    int v[V], s = 0;
+    for (int64_t b = b0; b < b1; b += V) {
+#pragma unroll
+        for (int q = 0; q < V; ++q) v[q] = e < E && b + q < b1 ? hist[(b + q) * E + e] : 0;
+#pragma unroll
+        for (int q = 0; q < V; ++q) s += v[q];
     }
     sums[threadIdx.x & 15][part] = s;
     __syncthreads();
@@ -485,11 +517,17 @@ __global__ __launch_bounds__(1024) void k_route_scan(int32_t* __restrict__ hist,
     __syncthreads();
     if (e >= E) return;
     int at = sums[threadIdx.x & 15][part];
-#pragma unroll 8
-    for (int64_t b = b0; b < b1; ++b) {
-        const int v = hist[b * E + e];
-        hist[b * E + e] = at;
-        at += v;
+    for (int64_t b = b0; b < b1; b += V) {
+        if (per > V) {
+#pragma unroll
+            for (int q = 0; q < V; ++q) v[q] = b + q < b1 ? hist[(b + q) * E + e] : 0;
+        }
+#pragma unroll
+        for (int q = 0; q < V; ++q)
+            if (b + q < b1) {
+                hist[(b + q) * E + e] = at;
+                at += v[q];
+            }
     }
 }
 
@@ -549,7 +587,7 @@ __global__ void k_route_none(int32_t* offsets, int32_t E) {
 // Tokens per block.  A block is one pass over its tokens, so few tokens want
 // small blocks (4096 x 256: 16 tokens fill 256 blocks, 64 tokens only 64: 12.3
 // against 19.8 us of the first launch); many want few counts to scan (50001 x 128:
-// 32.7 against 33.5 us for the call).  Up to 64 tokens one block of 64 does the
+// 32.7 against 33.5 us for the call, both measured before the bound's last form).  Up to 64 tokens one block of 64 does the
 // grouping as well, without the other two launches.  Above 256 experts a token
 // takes a whole wave, 16 to a block.
 static int route_tb(int64_t T, int64_t E) { return E <= 256 && (T <= 64 || T > 16384) ? 64 : 16; }
