@@ -367,9 +367,6 @@ static int64_t most_tiles(const ExpertArgs& a) { return a.P / C::BM + (a.E < a.P
 
 template <class C, bool GATED>
 static hipError_t run_tile(const ExpertArgs& a, hipStream_t st) {
-    static const hipError_t once = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_experts_tile<C, GATED>),
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
-    if (once != hipSuccess) return once;
     const int64_t nc = GATED ? C::BN / 2 : C::BN;
     const int64_t tn = (a.N + nc - 1) / nc;
     const int64_t tm = most_tiles<C>(a);

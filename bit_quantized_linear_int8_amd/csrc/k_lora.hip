@@ -550,9 +550,6 @@ size_t lora_scratch_bytes(int64_t M, int64_t K, int64_t r) {
 
 template <class C, bool BF>
 static hipError_t run_lora_tile(const LoraArgs& a, hipStream_t st) {
-    static const hipError_t once = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_lora_tile<C, BF>),
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
-    if (once != hipSuccess) return once;
     const int tm = (int)((a.M + C::BM - 1) / C::BM), tn = (int)((a.N + C::BN - 1) / C::BN);
     hipLaunchKernelGGL((k_lora_tile<C, BF>), dim3((unsigned)(tm * tn)), dim3(C::THREADS), C::LDS, st, a, tm, tn);
     return hipGetLastError();

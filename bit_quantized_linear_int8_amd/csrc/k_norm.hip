@@ -390,14 +390,22 @@ static void norm_dispatch(const NormArgs& a, hipStream_t st) {
 hipError_t launch_rmsnorm_i8(const void* X, int64_t ldx, const void* R, int64_t ldr, const void* g, int dtype,
                              int64_t rows, int64_t K, float eps, int8_t* q, float* s, void* sum, int64_t lds, void* y,
                              hipStream_t st) {
-    const NormArgs a{X, R, g, sum, y, q, s, rows, K, ldx, ldr, lds, eps};
     const int64_t step = dtype == 0 ? 4 : 8;                 // elements in 16 bytes
     auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
     const bool even = K % 8 == 0 && al(X) && al(R) && al(g) && al(q) && al(sum) && al(y) && ldx % step == 0 &&
                       (!R || ldr % step == 0) && (!sum || lds % step == 0);
-    if (dtype == 0) { if (even) norm_dispatch<0, true>(a, st); else norm_dispatch<0, false>(a, st); }
-    else if (dtype == 1) { if (even) norm_dispatch<1, true>(a, st); else norm_dispatch<1, false>(a, st); }
-    else { if (even) norm_dispatch<2, true>(a, st); else norm_dispatch<2, false>(a, st); }
+    // a launch counts its threads in 32 bits: 2^21 rows of 1024 threads at a time
+    const int64_t el = dtype == 0 ? 4 : 2;
+    auto at = [](const void* p, int64_t bytes) -> void* {
+        return p ? const_cast<uint8_t*>(static_cast<const uint8_t*>(p)) + bytes : nullptr;
+    };
+    for (int64_t r = 0; r < rows; r += (int64_t)1 << 21) {
+        const NormArgs a{at(X, r * ldx * el), at(R, r * ldr * el), g, at(sum, r * lds * el), at(y, r * K * el),
+                         q + r * K, s + r, rows - r < ((int64_t)1 << 21) ? rows - r : (int64_t)1 << 21, K, ldx, ldr, lds, eps};
+        if (dtype == 0) { if (even) norm_dispatch<0, true>(a, st); else norm_dispatch<0, false>(a, st); }
+        else if (dtype == 1) { if (even) norm_dispatch<1, true>(a, st); else norm_dispatch<1, false>(a, st); }
+        else { if (even) norm_dispatch<2, true>(a, st); else norm_dispatch<2, false>(a, st); }
+    }
     return hipGetLastError();
 }
 

@@ -335,7 +335,8 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const bool in = c[i] != NEG;
-            c[i] = in ? s[i] + (a.bias ? a.bias[min(l * EPL + i, a.E - 1)] : 0.0f) : NEG;
+            // (a NaN bias masks its expert, as a NaN logit does)
+            c[i] = in ? fmaxf(s[i] + (a.bias ? a.bias[min(l * EPL + i, a.E - 1)] : 0.0f), NEG) : NEG;
             top = fmaxf(top, c[i]);
         }
     }
@@ -605,10 +606,6 @@ static hipError_t run_route(RouteArgs a, hipStream_t st) {
     const int m = a.gsize / EPL;
     const bool in_lanes = LPT == 16 && a.gsize % EPL == 0 && (m & (m - 1)) == 0;
     const size_t rows = a.groups > 1 && !in_lanes ? (size_t)TB * (a.E + 1) * 4 : (size_t)a.E * 4;
-    static const hipError_t once =                           // 64 rows of 257 floats beside 28 KB of static LDS
-        hipFuncSetAttribute(reinterpret_cast<const void*>(&k_route<DT, LPT, EPL, TB>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, 96 << 10);
-    if (once != hipSuccess) return once;
     hipLaunchKernelGGL((k_route<DT, LPT, EPL, TB>), dim3(a.nb), dim3(TB * LPT), (size_t)a.E * 8 + rows, st, a);
     return hipGetLastError();
 }

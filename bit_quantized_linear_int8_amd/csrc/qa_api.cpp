@@ -139,11 +139,13 @@ constexpr int64_t kMaxI32 = 2147483647;
 constexpr int64_t kMaxExperts = 1024;       // a block's threads in the routing and tile plans
 constexpr int64_t kMaxSlots = 32;           // experts per token
 constexpr int64_t kMaxRank = 256;
+constexpr int64_t kMaxTokens = (int64_t)1 << 23;    // a launch counts its threads in 32 bits
+constexpr int64_t kMaxTiles = (int64_t)1 << 23;     // of 512 threads
 
 bool experts_shape_ok(int64_t T, int64_t K, int32_t k, int64_t E, int64_t F) {
     return T >= 0 && T <= kMaxI32 && E >= 1 && E <= kMaxExperts && k >= 1 && k <= kMaxSlots && K > 0 && K % 16 == 0 &&
            K <= kMaxK_i8 && F > 0 && F % 16 == 0 && F <= kMaxK_i8 && T * K <= kMaxI32 && 2 * F * K <= kMaxI32 &&
-           T * k <= ((int64_t)1 << 26);
+           T * k <= kMaxTokens && (T * k / 64 + E) * ((2 * F > K ? 2 * F : K) / 128 + 1) < kMaxTiles;
 }
 
 bool valid_dtype(qa_dtype d) { return d == QA_F32 || d == QA_F16 || d == QA_BF16; }
@@ -864,7 +866,7 @@ qa_status qa_rmsnorm_int8(const void* X, int64_t ldx, const void* residual_or_nu
 
 // ----------------------------------------------------------------- experts
 size_t qa_route_experts_workspace(int64_t T, int64_t E, int32_t k) {
-    if (T < 0 || T > kMaxI32 || E < 1 || E > kMaxExperts || k < 1 || k > kMaxSlots) return 0;
+    if (T < 0 || T > kMaxTokens || E < 1 || E > kMaxExperts || k < 1 || k > kMaxSlots) return 0;
     return up(qa::route_scratch_bytes(T, E));
 }
 
@@ -872,9 +874,8 @@ qa_status qa_route_experts(const void* logits, qa_dtype dtype, int64_t T, int64_
                            const float* bias_or_null, qa_score score, int32_t n_groups, int32_t top_groups,
                            int32_t group_top, int32_t k, int32_t renorm, float scale, int32_t* ids, float* weights,
                            int32_t* order, int32_t* offsets, void* workspace, size_t workspace_bytes, void* stream) {
-    if (T < 0 || T > kMaxI32 || E < 1 || E > kMaxExperts || ld < E || k < 1 || k > kMaxSlots || k > E ||
-        T * k > kMaxI32)
-        return fail(QA_ERR_SHAPE, "qa_route_experts: need T >= 0, 1 <= E <= 1024, ld >= E, 1 <= k <= min(32, E), T k < 2^31");
+    if (T < 0 || T > kMaxTokens || E < 1 || E > kMaxExperts || ld < E || k < 1 || k > kMaxSlots || k > E)
+        return fail(QA_ERR_SHAPE, "qa_route_experts: need 0 <= T <= 2^23, 1 <= E <= 1024, ld >= E, 1 <= k <= min(32, E)");
     if (n_groups < 1 || n_groups > 32 || E % n_groups != 0 || top_groups < 1 || top_groups > n_groups ||
         k > top_groups * (E / n_groups))
         return fail(QA_ERR_SHAPE, "qa_route_experts: need 1 <= n_groups <= 32 dividing E, 1 <= top_groups <= n_groups, "
@@ -907,7 +908,8 @@ qa_status qa_experts_int8(const int8_t* Xq, const float* s_x, int64_t T, int64_t
                           qa_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
     if (!experts_shape_ok(T, K, k, E, F))
         return fail(QA_ERR_SHAPE, "qa_experts_int8: need T >= 0, 1 <= E <= 1024, 1 <= k <= 32, K and F multiples of 16 "
-                                  "in 16..131072, T K and 2 F K below 2^31, T k <= 2^26");
+                                  "in 16..131072, T K and 2 F K below 2^31, T k <= 2^23, "
+                                  "(T k / 64 + E) (max(2 F, K) / 128 + 1) < 2^23");
     if (!valid_dtype(out_dtype)) return fail(QA_ERR_VALUE, "qa_experts_int8: bad out_dtype %d", (int)out_dtype);
     if (T == 0) return ok();
     if (!Xq || !s_x || !weights || !order || !offsets || !W13 || !s13 || !W2 || !s2 || !out || !workspace)
@@ -927,7 +929,7 @@ qa_status qa_experts_int8(const int8_t* Xq, const float* s_x, int64_t T, int64_t
 
 // ----------------------------------------------------------------- adapters
 size_t qa_qlinear_int8_lora_workspace(int64_t M, int64_t K, int32_t r) {
-    if (M < 0 || M > kMaxI32 || K <= 0 || r < 8 || r > kMaxRank || r % 8 != 0) return 0;
+    if (M < 0 || M > kMaxTokens || K <= 0 || r < 8 || r > kMaxRank || r % 8 != 0) return 0;
     return up(qa::lora_scratch_bytes(M, K, r));
 }
 
@@ -936,11 +938,11 @@ qa_status qa_qlinear_int8_lora(const int8_t* Xq, const float* s_x, const void* X
                                const float* alpha, int32_t r, int64_t L, const int32_t* seg, const int32_t* which,
                                int64_t R, void* out, qa_dtype out_dtype, void* workspace, size_t workspace_bytes,
                                void* stream) {
-    if (M < 0 || M > kMaxI32 || N < 0 || N > kMaxI32 || L < 0 || L > kMaxI32 || R < 0 || R > kMaxI32 - 1 || K <= 0 ||
+    if (M < 0 || M > kMaxTokens || N < 0 || N > kMaxI32 || L < 0 || L > kMaxI32 || R < 0 || R > kMaxI32 - 1 || K <= 0 ||
         K % 16 != 0 || K > kMaxK_i8 || r < 8 || r > kMaxRank || r % 8 != 0 ||
-        ((M + 63) / 64) * ((N + 127) / 128) > kMaxI32)
-        return fail(QA_ERR_SHAPE, "qa_qlinear_int8_lora: need M, N, L, R >= 0, K %% 16 == 0, 0 < K <= %lld, r %% 8 == 0, "
-                                  "8 <= r <= %d",
+        (M + 63) / 64 * ((N + 127) / 128) >= kMaxTiles)
+        return fail(QA_ERR_SHAPE, "qa_qlinear_int8_lora: need M, N, L, R >= 0, M <= 2^23, (M / 64) (N / 128) < 2^23, "
+                                  "K %% 16 == 0, 0 < K <= %lld, r %% 8 == 0, 8 <= r <= %d",
                     (long long)kMaxK_i8, (int)kMaxRank);
     if ((dtype != QA_F16 && dtype != QA_BF16) || !valid_dtype(out_dtype))
         return fail(QA_ERR_VALUE, "qa_qlinear_int8_lora: dtype must be fp16 or bf16, out_dtype fp32, fp16 or bf16");

@@ -634,14 +634,14 @@ qa_status qa_rmsnorm_int8(const void* X, int64_t ldx, const void* residual_or_nu
  *   offsets i32 [E + 1]: expert e's pairs are order[offsets[e] .. offsets[e+1])
  * Softmax without a bias (and with groups valued by their largest expert)
  * chooses by the logits themselves, which have the same order.
- * A logit of -infinity or NaN masks its expert; +infinity counts as the
- * largest finite value.  Where fewer than k experts are left, the last slots
+ * A logit (or bias) of -infinity or NaN masks its expert; a logit of +infinity
+ * counts as the largest finite value.  Where fewer than k experts are left, the last slots
  * are expert -1 with weight 0 and are in no expert's range.
  *   workspace  qa_route_experts_workspace(T, E, k) bytes (any content)
  * The result does not depend on the order in which blocks run.  T == 0 writes
  * offsets alone (zeros).
- * Errors (QA_ERR_SHAPE): T < 0, E outside 1..1024, ld < E, k outside
- * 1..min(32, E), T k > 2^31 - 1, n_groups outside 1..32 or not dividing E,
+ * Errors (QA_ERR_SHAPE): T outside 0..2^23, E outside 1..1024, ld < E, k
+ * outside 1..min(32, E), n_groups outside 1..32 or not dividing E,
  * top_groups outside 1..n_groups, k > top_groups E / n_groups; (QA_ERR_VALUE)
  * bad dtype, score or group_top, scale not finite; NULL pointers, alignment to
  * the elements, small workspace.
@@ -673,9 +673,10 @@ qa_status qa_route_experts(const void* logits, qa_dtype dtype, int64_t T, int64_
  *   out      [T x K] of out_dtype
  *   workspace  qa_experts_int8_workspace(T, K, k, E, F) bytes (any content)
  * Errors (QA_ERR_SHAPE): T < 0, E outside 1..1024, k outside 1..32, K or F not
- * a positive multiple of 16 up to 131072, T K or 2 F K >= 2^31, T k > 2^26;
- * bad out_dtype; NULL pointers; Xq, W13, W2, s13, s2, out not 16-byte, others
- * not 4-byte, workspace not 256-byte aligned; small workspace.
+ * a positive multiple of 16 up to 131072, T K or 2 F K >= 2^31, T k > 2^23,
+ * (T k / 64 + E) (max(2 F, K) / 128 + 1) >= 2^23; bad out_dtype; NULL
+ * pointers; Xq, W13, W2, s13, s2, out not 16-byte, others not 4-byte,
+ * workspace not 256-byte aligned; small workspace.
  * ------------------------------------------------------------------------- */
 size_t qa_experts_int8_workspace(int64_t T, int64_t K, int32_t k, int64_t E, int64_t F);
 qa_status qa_experts_int8(const int8_t* Xq, const float* s_x, int64_t T, int64_t K, const float* weights,
@@ -701,9 +702,9 @@ qa_status qa_experts_int8(const int8_t* Xq, const float* s_x, int64_t T, int64_t
  *   out      [M x N] of out_dtype
  *   workspace  qa_qlinear_int8_lora_workspace(M, K, r) bytes (any content)
  * With R == 0 or L == 0 the adapter arrays may be NULL.
- * Errors (QA_ERR_SHAPE): M, N, L or R negative or past 2^31 - 1, K not a
- * positive multiple of 16 up to 131072, r not a multiple of 8 in 8..256;
- * (QA_ERR_VALUE) dtype not fp16 / bf16, bad out_dtype; NULL pointers; Xq, X,
+ * Errors (QA_ERR_SHAPE): M, N, L or R negative, M > 2^23, N, L or R past
+ * 2^31 - 1, ceil(M / 64) ceil(N / 128) >= 2^23, K not a positive multiple of
+ * 16 up to 131072, r not a multiple of 8 in 8..256; (QA_ERR_VALUE) dtype not fp16 / bf16, bad out_dtype; NULL pointers; Xq, X,
  * Wq, A, B not 16-byte, others not 4-byte, workspace not 256-byte aligned;
  * small workspace.
  * ------------------------------------------------------------------------- */

@@ -45,7 +45,7 @@ ROUTE = dict(x=A, dt=0, T=10, E=64, ld=64, bias=A, score=0, groups=1, top=1, gto
 @pytest.mark.parametrize("kw,status", [
     (dict(x=None), NULL), (dict(ids=None), NULL), (dict(w=None), NULL), (dict(order=None), NULL),
     (dict(offsets=None), NULL), (dict(ws=None), NULL), (dict(T=0, offsets=None), NULL),
-    (dict(T=-1), SHAPE), (dict(T=1 << 31), SHAPE), (dict(T=1 << 30), SHAPE), (dict(E=0), SHAPE),
+    (dict(T=-1), SHAPE), (dict(T=1 << 31), SHAPE), (dict(T=(1 << 23) + 1), SHAPE), (dict(E=0), SHAPE),
     (dict(E=1025, ld=1025), SHAPE), (dict(ld=63), SHAPE), (dict(k=0), SHAPE), (dict(k=33), SHAPE),
     (dict(E=3, k=4), SHAPE), (dict(groups=0), SHAPE), (dict(groups=64, top=64), SHAPE), (dict(groups=5, top=5), SHAPE),
     (dict(groups=4, top=0), SHAPE), (dict(groups=4, top=5), SHAPE), (dict(groups=32, top=1), SHAPE),
@@ -68,7 +68,8 @@ EXPERTS = dict(Xq=A, sx=A, T=6, K=64, w=A, order=A, offsets=A, E=4, k=2, W13=A, 
     (dict(F=0), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(k=0), SHAPE), (dict(k=33), SHAPE),
     (dict(T=1 << 26, K=32), SHAPE),                         # T K
     (dict(K=65536, F=16384), SHAPE),                        # 2 F K
-    (dict(T=1 << 26, K=16, k=2), SHAPE),                    # T k
+    (dict(T=1 << 22, K=16, k=3), SHAPE),                    # T k
+    (dict(T=1 << 22, K=64, F=131072, k=2), SHAPE),          # tiles
     (dict(dt=3), VALUE),
     (dict(Xq=MIS), ALIGN), (dict(W13=ctypes.c_void_p(0x10008)), ALIGN), (dict(s2=ctypes.c_void_p(0x10004)), ALIGN),
     (dict(out=ctypes.c_void_p(0x10008)), ALIGN), (dict(ws=ctypes.c_void_p(0x10010)), ALIGN), (dict(sx=MIS), ALIGN),
@@ -86,7 +87,7 @@ LORA = dict(Xq=A, sx=A, X=A, dt=1, M=6, K=64, Wq=A, sw=A, N=48, A=A, B=A, alpha=
                                                                          "seg", "which", "out", "ws")] + [
     (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=0), SHAPE), (dict(K=72), SHAPE), (dict(K=131088), SHAPE),
     (dict(r=0), SHAPE), (dict(r=12), SHAPE), (dict(r=264), SHAPE), (dict(L=-1), SHAPE), (dict(R=-1), SHAPE),
-    (dict(R=(1 << 31) - 1), SHAPE), (dict(M=1 << 31), SHAPE), (dict(M=(1 << 31) - 1, N=(1 << 31) - 1), SHAPE),
+    (dict(R=(1 << 31) - 1), SHAPE), (dict(M=(1 << 23) + 1), SHAPE), (dict(M=1 << 23, N=1 << 13), SHAPE),
     (dict(dt=0), VALUE), (dict(dt=7), VALUE), (dict(odt=3), VALUE),
     (dict(Xq=MIS), ALIGN), (dict(B=ctypes.c_void_p(0x10008)), ALIGN), (dict(seg=MIS), ALIGN), (dict(out=MIS), ALIGN),
     (dict(ws=ctypes.c_void_p(0x10020)), ALIGN), (dict(wsb=64), WORKSPACE),

@@ -145,6 +145,21 @@ def test_masked_and_extreme_logits(dt, score, bias, groups, top_groups, group_to
     check(x, 8, bias=b, score=score, groups=groups, top_groups=top_groups, group_top=group_top)
 
 
+@pytest.mark.parametrize("E,k,groups", [(64, 8, 1), (64, 8, 8), (64, 20, 1), (600, 8, 1)])
+def test_a_bias_that_is_no_number_masks_its_expert(E, k, groups):
+    x = logits_of(130, E, "f32", seed=9)
+    bias = torch.linspace(-0.2, 0.2, E, device=DEV)
+    kw = dict(score=qa.QA_SCORE_SIGMOID, groups=groups, top_groups=max(1, groups // 2), group_top=2)
+    low = bias.clone()
+    low[::3] = -math.inf
+    bias[::3] = float("nan")
+    got, want = qa.qa_route_experts(x, k, bias=bias, **kw), qa.qa_route_experts(x, k, bias=low, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert (got[0] % 3 != 0).all() or (got[0] < 0).any()
+    none = qa.qa_route_experts(x, k, bias=torch.full((E,), float("nan"), device=DEV), **kw)
+    assert (none[0] == -1).all() and (none[1] == 0).all() and (none[3] == 0).all()
+
+
 def test_two_infinite_logits_share_the_weight():
     x = torch.zeros(1, 8, device=DEV)
     x[0, 2] = x[0, 5] = math.inf
