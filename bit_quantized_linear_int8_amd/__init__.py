@@ -635,6 +635,13 @@ def _s(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
+def _like(stream, X, dtype):
+    """A contiguous tensor of X's shape (empty_like is the cheapest allocation on the host)."""
+    if stream is None and X.is_contiguous():
+        return torch.empty_like(X, dtype=dtype)
+    return _empty(stream, X.shape, dtype=dtype, device=X.device)
+
+
 def qa_rmsnorm_int8(X, g, residual=None, eps=1e-6, want_y=False, total=None, stream=None):
     """Residual addition + RMS norm + int8 codes per row.
 
@@ -653,13 +660,13 @@ def qa_rmsnorm_int8(X, g, residual=None, eps=1e-6, want_y=False, total=None, str
         ldr = _rows(residual, "residual", X.dtype)
         _shape(residual, "residual", (rows, K))
         if total is None:
-            total = _empty(stream, (rows, K), dtype=X.dtype, device=X.device)
+            total = _like(stream, X, X.dtype)
     if total is not None:
         lds = _rows(total, "total", X.dtype)
         _shape(total, "total", (rows, K))
-    Xq = _empty(stream, (rows, K), dtype=torch.int8, device=X.device)
+    Xq = _like(stream, X, torch.int8)
     s = _empty(stream, rows, dtype=torch.float32, device=X.device)
-    y = _empty(stream, (rows, K), dtype=X.dtype, device=X.device) if want_y else None
+    y = _like(stream, X, X.dtype) if want_y else None
     _check("qa_rmsnorm_int8",
            lib().qa_rmsnorm_int8(_a(X), ldx, _a(residual), ldr, _a(g), _DTYPE_CODE[X.dtype], rows, K, float(eps),
                                  _a(Xq), _a(s), _a(total), lds, _a(y), _s(stream)))
@@ -684,15 +691,22 @@ def qa_route_experts(logits, k: int, bias=None, score=QA_SCORE_SOFTMAX, groups=1
         _shape(bias, "bias", (E,))
     d = logits.device
     n = max(k, 0)
-    ids = _empty(stream, (T, n), dtype=torch.int32, device=d)
+    p, need = T * n, qa_route_experts_workspace(T, E, k)
     w = _empty(stream, (T, n), dtype=torch.float32, device=d)
-    order = _empty(stream, T * n, dtype=torch.int32, device=d)
-    offsets = _empty(stream, E + 1, dtype=torch.int32, device=d)
-    workspace = _workspace(stream, qa_route_experts_workspace(T, E, k), d, workspace)
+    # ids, order and offsets are views of one allocation (host time), with the workspace behind them when it is small
+    own = workspace is None and need <= 1 << 16
+    ints = _empty(stream, 2 * p + E + 1 + (need // 4 if own else 0), dtype=torch.int32, device=d)
+    ids, order = ints.as_strided((T, n), (n, 1), 0), ints.as_strided((p,), (1,), p)
+    offsets = ints.as_strided((E + 1,), (1,), 2 * p)
+    if own:
+        ws, ws_bytes = ints.data_ptr() + 4 * (2 * p + E + 1), need
+    else:
+        workspace = _workspace(stream, need, d, workspace)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
     _check("qa_route_experts",
            lib().qa_route_experts(_a(logits), _DTYPE_CODE[logits.dtype], T, E, ld, _a(bias), int(score), int(groups),
                                   int(top_groups), int(group_top), k, int(bool(renorm)), float(scale), _a(ids), _a(w),
-                                  _a(order), _a(offsets), _a(workspace), workspace.numel(), _s(stream)))
+                                  _a(order), _a(offsets), ws, ws_bytes, _s(stream)))
     return ids, w, order, offsets
 
 
