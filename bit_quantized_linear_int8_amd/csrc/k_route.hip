@@ -22,11 +22,12 @@
 // The choice: k rounds of "largest left" cost each lane its EPL registers in
 // every round.  Instead the k-th largest of the lanes' own maxima is a bound
 // that the k chosen reach (k lanes hold a value as large), and few others do:
-// the values that reach it go to LDS, one to a lane, and a value's rank among
-// them is its slot.  Only where more than 16 reach it (k > 8, many ties) the
-// rounds are run.  First launch at 50001 x 128 (bf16, k = 8): 28.8 us with the
-// rounds, 18.6 with the bound; at 4096 x 256 in 8 groups 34 and 9.1.  At 50001
-// tokens it issues 415 vector instructions per wave of four tokens, 9 us of the
+// the values that reach it go to LDS, one or two to a lane, and a value's rank
+// among them is its slot.  For more than 8, or with groups, the bound is taken from
+// the lanes' two largest.  Only where more than 32 reach it (many ties), for k > 16
+// and above 256 experts the rounds are run.  First launch at 50001 x 128 (bf16,
+// k = 8): 28.8 us with the rounds, 17.6 with the bound; at 4096 x 256 in 8 groups
+// 34 and 9.3.  At 50001 tokens it issues 415 vector instructions per wave of four tokens, 9 us of the
 // SIMDs' time; reading the logits is 2.5 us.  32 tokens to a block run it in 14.8
 // us, but the counts of twice the blocks cost that again in the two launches after.
 //
@@ -43,7 +44,7 @@ namespace qa {
 namespace {
 
 constexpr float NEG = -__builtin_inff(), FMAX = 3.4028234663852886e38f;
-constexpr int CAP = 16;                      // values that may reach the bound
+constexpr int CAP = 32;                      // values that may reach the bound
 constexpr int MAXK = 32;
 
 // LDS accesses of a wave's lanes before this are seen by its lanes after it.
@@ -348,15 +349,15 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
     }
     // the bound: the k-th largest of the lanes' maxima
     bool few = false;
-    if (LPT == 16 && a.k <= 8) {
+    if (LPT == 16 && a.k <= 16) {
         // (a lane whose maximum fewer than k lanes exceed has one as large as the
         // k-th largest; the least of those is the bound)
         auto more = [](float o, float v, int) { return o > v; };
         float least = FMAX;
-        if (a.groups == 1) {
+        if (a.groups == 1 && a.k <= 8) {
             if (count15<1>(top, l, more) < a.k) least = top;
         } else {
-            // the kept groups' experts lie in few lanes: the lanes' two largest
+            // more than 8, or the kept groups' experts in few lanes: the lanes' two largest
             float m1 = NEG, m2 = NEG;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
@@ -384,22 +385,40 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
                     ++at;
                 }
             sid[tb][l] = -1;
+            const bool wide = __any(total > 16);
             wave_sync();
-            // one value to a lane, as a number that orders by value and then by
-            // lower index; 0 in the lanes without one
-            const uint64_t mine = ckey[tb][l];
-            const uint32_t e = (uint32_t)mine, bits = (uint32_t)(mine >> 32);
-            const uint64_t key = l < total ? ((uint64_t)ordered(__builtin_bit_cast(float, bits)) << 32) | (0xffffu - e) : 0;
-            wave_sync();
-            ckey[tb][l] = key;
-            wave_sync();
-            int rank = 0;
+            // one value (or two) to a lane, as a number that orders by value and
+            // then by lower index; 0 in the places without one
+            uint64_t key[2];
+            uint32_t e[2], bits[2];
+            int rank[2] = {0, 0};
 #pragma unroll
-            for (int o = 0; o < CAP; ++o) rank += ckey[tb][o] > key ? 1 : 0;
-            if (l < total && rank < a.k) {
-                sid[tb][rank] = (int)e;
-                swt[tb][rank] = by_logit ? __builtin_bit_cast(float, bits) : cscore[tb][l];
+            for (int h = 0; h < 2; ++h) {
+                const uint64_t mine = ckey[tb][h * 16 + l];
+                e[h] = (uint32_t)mine;
+                bits[h] = (uint32_t)(mine >> 32);
+                key[h] = h * 16 + l < total ? ((uint64_t)ordered(__builtin_bit_cast(float, bits[h])) << 32) | (0xffffu - e[h]) : 0;
             }
+            wave_sync();
+            ckey[tb][l] = key[0];
+            ckey[tb][16 + l] = key[1];
+            wave_sync();
+#pragma unroll
+            for (int o = 0; o < 16; ++o) rank[0] += ckey[tb][o] > key[0] ? 1 : 0;
+            if (wide) {
+#pragma unroll
+                for (int o = 0; o < 16; ++o) {
+                    const uint64_t u = ckey[tb][16 + o];
+                    rank[0] += u > key[0] ? 1 : 0;
+                    rank[1] += (ckey[tb][o] > key[1] ? 1 : 0) + (u > key[1] ? 1 : 0);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (h * 16 + l < total && rank[h] < a.k) {
+                    sid[tb][rank[h]] = (int)e[h];
+                    swt[tb][rank[h]] = by_logit ? __builtin_bit_cast(float, bits[h]) : cscore[tb][h * 16 + l];
+                }
         }
     }
     if (!few) {

@@ -160,6 +160,33 @@ def test_a_bias_that_is_no_number_masks_its_expert(E, k, groups):
     assert (none[0] == -1).all() and (none[1] == 0).all() and (none[3] == 0).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups,top_groups", [(70, 16, 16, 1, 1), (66, 31, 9, 1, 1), (65, 128, 12, 1, 1),
+                                                     (40, 256, 16, 1, 1), (33, 256, 16, 16, 1), (33, 96, 14, 4, 2),
+                                                     (20, 96, 16, 32, 9), (20, 256, 17, 8, 4)])
+def test_more_than_eight(score, T, E, k, groups, top_groups):
+    x = logits_of(T, E, "f32", seed=11)
+    x[1] = -math.inf
+    x[2, 5:] = -math.inf                                      # fewer than k left
+    x[3, ::2] = float("nan")
+    x[4, :E // 2] = x[4, 0]                                   # equal from the bound's place on
+    kw = dict(groups=groups, top_groups=top_groups, group_top=2)
+    check(x, k, score=score, **kw)
+    check(x, k, score=score, bias=torch.linspace(-0.3, 0.3, E, device=DEV), renorm=False, **kw)
+    check(torch.randint(-2, 3, (T, E), device=DEV, generator=torch.Generator(device=DEV).manual_seed(E)).float(), k,
+          score=score, **kw)
+
+
+@pytest.mark.parametrize("same", [15, 16, 17, 31, 32, 33, 40])
+@pytest.mark.parametrize("k", [8, 12])
+def test_so_many_equal_largest(same, k):
+    """16 or 32 values at the bound are taken another way than one more."""
+    for E in (64, 200):
+        x = logits_of(50, E, "f32", seed=same).clamp(-4, 4)
+        at = torch.rand(50, E, device=DEV, generator=torch.Generator(device=DEV).manual_seed(k)).topk(same, 1).indices
+        check(x.scatter(1, at, 6.0), k)
+
+
 def test_two_infinite_logits_share_the_weight():
     x = torch.zeros(1, 8, device=DEV)
     x[0, 2] = x[0, 5] = math.inf
