@@ -79,6 +79,19 @@ def test_against_64_bits(dt, T, K, F, E, k):
     check(*make(T, K, F, E, k), dt=dt)
 
 
+@pytest.mark.parametrize("F", [240, 256, 272, 1024, 1040, 2048, 2064, 4096, 4112, 6160])
+@pytest.mark.parametrize("T,k", [(3, 2), (37, 1)])
+def test_widths_of_the_hidden_rows(T, k, F):
+    check(*make(T, 48, F, 2, k), dt="f32")
+
+
+@pytest.mark.parametrize("T,K,k", [(1, 16, 7), (5, 1040, 8), (3, 4112, 9), (33, 80, 20), (2, 32, 32)])
+def test_many_slots_to_a_token(T, K, k):
+    ids = torch.rand(T, 32, device=DEV, generator=torch.Generator(device=DEV).manual_seed(k)).topk(k, 1).indices.to(torch.int32)
+    ids[:, ::5] = -1
+    check(*make(T, K, 32, 32, k, ids=ids), dt="f32")
+
+
 @pytest.mark.parametrize("T", [20, 600])
 def test_uneven_experts(T):
     """Experts without tokens, one that takes nearly all, tokens without experts and half-filled slots."""
