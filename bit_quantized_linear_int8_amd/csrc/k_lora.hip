@@ -143,7 +143,8 @@ __device__ __forceinline__ v4f mfma16(u32x4 x, u32x4 y, v4f c) {
 
 // ---------------------------------------------------------------------------
 // Few tokens: a block per token and 16 ranks, a wave on each.  The token's row
-// is requested before its adapter is looked up.
+// is requested before its adapter is looked up.  Bound by latency: 5.0 us at 16
+// tokens, K = 4096, rank 16.
 // ---------------------------------------------------------------------------
 template <bool BF>
 __global__ __launch_bounds__(1024) void k_lora_down_token(LoraArgs a) {
@@ -187,7 +188,8 @@ __global__ __launch_bounds__(1024) void k_lora_down_token(LoraArgs a) {
 // and every (8 / MT)-th chunk of 16 ranks from w / MT.  Its tokens' adapters are
 // requested before the weights and its first chunk of B behind them, so that
 // neither waits for the other (with the adapter looked up here and B read after
-// the weights, 9.3 us instead of 7.3 at 16 x 4096 x 4096, rank 16).
+// the weights, 9.3 us instead of 7.4 at 16 x 4096 x 4096, rank 16, where 19 MB of
+// weights and adapters make 2.6 TB/s: a launch of one round, bound by latency).
 template <int MT, bool BF>
 __global__ __launch_bounds__(512) void k_lora_stream(LoraArgs a) {
     __shared__ v4i part[8][MT][64];
@@ -304,6 +306,11 @@ __global__ __launch_bounds__(512) void k_lora_stream(LoraArgs a) {
 // batch of loads.  (Tiles of 16 tokens across requests, their adapters one after
 // the other, took 18.7 us for 777 tokens of 48 requests at K = 4096, rank 64.)
 // The splits are summed, in order, where h is read.
+// 12.6 us at 777 tokens of 48 requests, 32 adapters of rank 64, K = 4096 (23 MB
+// that memory has to bring: 1.9 TB/s of the whole, 3 of what is left after a
+// launch's own 5 us), 11 at 2048 tokens of 8 requests, rank 16.  Twice the tokens
+// or the ranks per block, half the loads ahead at more waves and contiguous tiles
+// per XCD all measure 12.3 to 13.4: neither the L1, the L2 nor the waves bound it.
 // ---------------------------------------------------------------------------
 template <bool BF>
 __global__ __launch_bounds__(256) void k_lora_down_tile(LoraArgs a) {
@@ -370,6 +377,12 @@ __global__ __launch_bounds__(256) void k_lora_down_tile(LoraArgs a) {
     }
 }
 
+// Many tokens: the int8 product on LDS tiles; the adapters' part joins the fp32
+// tile before the one rounding.  2048 x 11008 x 4096, rank 16 (8 requests): 113 to
+// 127 us, of which the product alone is 100 (1.85 POPS) and the adapters' part the
+// epilogue's latency; bound by the tile product's loads and LDS reads.  777 x 4096
+// x 4096, rank 64 (48 requests): 34 us, 6 of them the adapters'; there a stage's
+// chain on the CU is the bound (0.36 us each, 32 of them).
 template <class C, bool BF>
 __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t tiles_m, int32_t tiles_n) {
     extern __shared__ uint8_t smem[];
@@ -530,10 +543,17 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
 }
 
 namespace {
-// The form for few tokens, by both sides' times at K = 4096, rank 16: 17.8 us at
-// 64 x 4096 and 27.1 at 32 x 11008 (39.1 at 64), the tiles 29.8 from 65 tokens on.
-constexpr int64_t FEW = 64;
-bool few_tokens(int64_t M, int64_t N) { return M <= 32 || (M <= FEW && N <= 8192); }
+// The form for few tokens, while its blocks of 16 columns fit the CUs at once, by
+// both sides' times at K = 4096, rank 16 (us of the call, stream and tiles of 64 x 64):
+//   tokens \ columns    4096          8192          11008         16384
+//   16                               17.4  21.2    21.6  21.2    26.5  21.6
+//   32                15.1  21.6    20.4  21.9    26.8  21.6    33.5  22.3
+//   64                17.4  21.9    27.2  22.2    37.3  22.1
+// (48 tokens at 5120 columns: 24.0 and 21.4.)
+bool few_tokens(int64_t M, int64_t N) {
+    const int64_t blocks = (N + 15) / 16;
+    return M <= 16 ? blocks <= 768 : M <= 32 ? blocks <= 512 : M <= 64 && blocks <= 256;
+}
 constexpr size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 }  // namespace
 
@@ -572,16 +592,21 @@ static hipError_t run_lora(const LoraArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(k_lora_down_tile<BF>,
                        dim3((unsigned)most, (unsigned)((a.r + 31) / 32), (unsigned)a.splits), dim3(256), 0, st, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    // By the number of 128 x 128 tiles, at K = 4096, rank 16 (us of the call):
-    //   M x N         tiles   64 x 128   128 x 128   128 x 192
-    //   512 x 4096      128       27.6        36.4        42.1
-    //   1024 x 4096     256       36.6        38.9        43.9
-    //   1536 x 4096     384       52.4        46.3        61.4
-    //   2048 x 4096     512       63.7        53.3        62.7
-    //   1024 x 11008    688       83.0        73.9        64.2
-    //   2048 x 11008   1376        150         124         119
-    // Up to 512 tiles fit the 256 CUs two at a time.
-    const int64_t tiles = ((a.M + 127) / 128) * ((a.N + 127) / 128);
+    // By size, at K = 4096, rank 16 (us of the call; T: tiles of 64 x 64, of 128 x 128):
+    //   M x N           T            64 x 64   64 x 128   128 x 128   128 x 192
+    //   128 x 4096      128, 32         21.5       24.4        33.8        36.6
+    //   320 x 4096      320, 96         23.5       24.8
+    //   512 x 4096      512, 128        26.7       27.6        36.4        42.1
+    //   777 x 4096      832, 224        56         44          48          55 (rank 64)
+    //   1024 x 4096    1024, 256        45.6       36.6        38.9        43.9
+    //   1536 x 4096    1536, 384                   52.4        46.3        61.4
+    //   2048 x 4096    2048, 512        75.5       63.7        53.3        62.7
+    //   1024 x 11008   2752, 688        95.7       83.0        73.9        64.2
+    //   2048 x 11008   5504, 1376        178        150         124         119
+    // A tile alone on its CU takes as long as two (a stage's chain of barrier, LDS
+    // reads and MFMAs), so small tiles as long as 512 of them fit two at a time.
+    const int64_t small = ((a.M + 63) / 64) * ((a.N + 63) / 64), tiles = ((a.M + 127) / 128) * ((a.N + 127) / 128);
+    if (small <= 512) return run_lora_tile<tile::Cfg<64, 64, 2, 4, 3>, BF>(a, st);
     if (tiles <= 256) return run_lora_tile<tile::Cfg<64, 128, 2, 4, 3>, BF>(a, st);
     if (tiles <= 512) return run_lora_tile<tile::Cfg<128, 128, 2, 4, 2>, BF>(a, st);
     return run_lora_tile<tile::Cfg<128, 192, 2, 4, 2>, BF>(a, st);

@@ -74,6 +74,17 @@ def test_against_64_bits(dt, out, M, K, N, r, L, R):
     check(make(M, K, N, r, L, *spread(M, R, L), dt=dt), out=out, dt=dt)
 
 
+@pytest.mark.parametrize("M,N", [(1, 12288), (16, 12292), (1, 12289), (32, 8192), (17, 8200), (33, 4096), (64, 4104), (48, 4097)])
+def test_both_sides_of_few(M, N):
+    check(make(M, 48, N, 24, 3, *spread(M, 4, 3)))
+
+
+@pytest.mark.parametrize("M,N", [(500, 4096), (513, 3600), (520, 4200), (1030, 4500), (1100, 7700), (129, 16400)])
+def test_every_size_of_tile(M, N):
+    """K of one whole and one ragged stage."""
+    check(make(M, 144, N, 40, 3, *spread(M, 5, 3)), out="f32")
+
+
 @pytest.mark.parametrize("M", [9, 90])
 def test_tokens_outside_every_request(M):
     """The first request starts after token 0 and the last one ends before the end."""
