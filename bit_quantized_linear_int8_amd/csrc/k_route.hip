@@ -27,9 +27,11 @@
 // the lanes' two largest.  Only where more than 32 reach it (many ties), for k > 16
 // and above 256 experts the rounds are run.  First launch at 50001 x 128 (bf16,
 // k = 8): 28.8 us with the rounds, 17.6 with the bound; at 4096 x 256 in 8 groups
-// 34 and 9.3.  At 50001 tokens it issues 415 vector instructions per wave of four tokens, 9 us of the
-// SIMDs' time; reading the logits is 2.5 us.  32 tokens to a block run it in 14.8
-// us, but the counts of twice the blocks cost that again in the two launches after.
+// 34 and 9.3.  At 50001 tokens it issues 415 vector instructions per wave of four
+// tokens, 9 us of the SIMDs' time; reading the logits is 2.5 us.  32 tokens to a
+// block run it in 14.8 us, but the counts of twice the blocks cost that again in
+// the two launches after (k_route_scan 5.6 us, k_route_scatter 3.2 to 5.2: little
+// more than launches).
 //
 // The grouping is stable (ascending pair index within an expert) and uses no
 // order-dependent atomics: a token chooses an expert at most once, so a block of
@@ -607,9 +609,10 @@ __global__ void k_route_none(int32_t* offsets, int32_t E) {
 // Tokens per block.  A block is one pass over its tokens, so few tokens want
 // small blocks (4096 x 256: 16 tokens fill 256 blocks, 64 tokens only 64: 12.3
 // against 19.8 us of the first launch); many want few counts to scan (50001 x 128:
-// 32.7 against 33.5 us for the call, both measured before the bound's last form).  Up to 64 tokens one block of 64 does the
-// grouping as well, without the other two launches.  Above 256 experts a token
-// takes a whole wave, 16 to a block.
+// 32.7 against 33.5 us for the call, both measured before the bound's last form).
+// Up to 64 tokens one block of 64 does the grouping as well, without the other two
+// launches (32 x 64: 4.4 us in all).  Above 256 experts a token takes a whole wave,
+// 16 to a block.
 static int route_tb(int64_t T, int64_t E) { return E <= 256 && (T <= 64 || T > 16384) ? 64 : 16; }
 
 size_t route_scratch_bytes(int64_t T, int64_t E) {
