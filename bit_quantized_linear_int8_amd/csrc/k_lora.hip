@@ -378,8 +378,8 @@ __global__ __launch_bounds__(256) void k_lora_down_tile(LoraArgs a) {
 }
 
 // Many tokens: the int8 product on LDS tiles; the adapters' part joins the fp32
-// tile before the one rounding.  2048 x 11008 x 4096, rank 16 (8 requests): 113 to
-// 127 us, of which the product alone is 100 (1.85 POPS) and the adapters' part the
+// tile before the one rounding.  2048 x 11008 x 4096, rank 16 (8 requests): 108 to 118
+// us, of which the product alone is 100 (1.85 POPS) and the adapters' part the
 // epilogue's latency; bound by the tile product's loads and LDS reads.  777 x 4096
 // x 4096, rank 64 (48 requests): 34 us, 6 of them the adapters'; there a stage's
 // chain on the CU is the bound (0.36 us each, 32 of them).
@@ -394,30 +394,39 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
     const uint32_t K = (uint32_t)a.K;
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int r16 = lane & 15, q16 = lane >> 4;
-    const int64_t mw = m0 + (wave / C::WN) * C::TM, nw = n0 + (wave % C::WN) * C::TN;   // the wave's tile
-    int ad[C::FM];                                           // requested before the product, as are the row scales
+    int ad[C::FM];
     float sx[C::FM];
+    auto rows = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i) {
-        const int64_t m = mw + i * 16 + r16;
-        ad[i] = m < a.M ? a.ad[m] : -1;
-        if (ad[i] >= a.L) ad[i] = -1;                        // no adapter was written: starts that descend
-        sx[i] = m < a.M ? a.s_x[m] : 0.0f;
-    }
+        for (int i = 0; i < C::FM; ++i) {
+            const int64_t m = m0 + (wave / C::WN) * C::TM + i * 16 + r16;
+            ad[i] = m < a.M ? a.ad[m] : -1;
+            if (ad[i] >= a.L) ad[i] = -1;                    // no adapter was written: starts that descend
+            sx[i] = m < a.M ? a.s_x[m] : 0.0f;
+        }
+    };
+    // Where registers allow, the rows' adapters and scales are requested before the
+    // product and the next adapter's rows of B during a multiplication; the largest
+    // tile takes both as it comes to them, without spills (4096 x 11008 x 4096, rank
+    // 16: 224 us against 235, of the call).
+    constexpr bool EARLY = C::FM * C::FN <= 8;
+    if (EARLY) rows();
     v4i acc[C::FM][C::FN];
     tile::product<C>(
         ra, rw, K, smem, [&](int r) -> uint32_t { return m0 + r < a.M ? (uint32_t)r * K : kOOB; },
         [&](int r) -> uint32_t { return n0 + r < a.N ? (uint32_t)r * K : kOOB; }, acc);
+    const int64_t mw = m0 + (wave / C::WN) * C::TM, nw = n0 + (wave % C::WN) * C::TN;   // the wave's tile
+    if (!EARLY) rows();
     // The adapters' part, 32 ranks at a time: the tile's rows of h (hi and lo) into
     // the freed LDS, 16-byte chunk c of row r at c ^ (r & 7), with their scales; then the distinct adapters of
-    // the wave's rows in turn, the next one's rows of B in flight while one is
-    // multiplied.  A row takes the product of its own adapter alone.
+    // the wave's rows in turn (EARLY: the next one's rows of B in flight while one is
+    // multiplied).  A row takes the product of its own adapter alone.
     constexpr int HC = C::BM * 8 / C::THREADS;               // quads of ranks of h per thread
     static_assert(HC * C::THREADS == C::BM * 8 && C::BM * 132 <= C::LDS, "h of the tile");
     const int groups = (a.r + 31) / 32;
     const rsrc_t none = make_rsrc(a.B, 0);
     v4f hc[HC];
-    u32x4 b0[C::FN], b1[C::FN];
+    u32x4 b0[C::FN], b1[EARLY ? C::FN : 1];
     bool left[C::FM];
     auto next = [&]() __attribute__((always_inline)) {       // an adapter that has not had its turn, or -1
         int w = -1;
@@ -507,7 +516,7 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
                 left[i] = left[i] && !mine[i];
             }
             const int nxt = next();
-            load_b(nxt, g, b1);
+            if constexpr (EARLY) load_b(nxt, g, b1);
 #pragma unroll
             for (int i = 0; i < C::FM; ++i) {
                 if (!__any(mine[i])) continue;
@@ -523,8 +532,12 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
                     for (int q = 0; q < 4; ++q) o[i][j][q] = mine[i] ? __builtin_fmaf(d[q], up, o[i][j][q]) : o[i][j][q];
                 }
             }
+            if constexpr (EARLY) {
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j) b0[j] = b1[j];
+                for (int j = 0; j < C::FN; ++j) b0[j] = b1[j];
+            } else {
+                load_b(nxt, g, b0);
+            }
             cur = nxt;
         }
     }
