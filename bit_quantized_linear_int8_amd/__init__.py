@@ -720,7 +720,9 @@ def qa_experts_int8(Xq, s_x, weights, order, offsets, W13, s13, W2, s2, out_dtyp
 
     Xq i8 [T x K], s_x f32 [T]; weights f32 [T x k], order, offsets from
     qa_route_experts; W13 i8 [E x 2F x K] (gate rows, then up rows), s13 f32
-    [E x 2F]; W2 i8 [E x K x F], s2 f32 [E x K]."""
+    [E x 2F]; W2 i8 [E x K x F], s2 f32 [E x K].  A part of the experts, e0 ..
+    e0 + E - 1: their weights and offsets[e0 : e0 + E + 1]; out is their share of
+    the sum."""
     _dev(Xq, "Xq", torch.int8)
     _dev(s_x, "s_x", torch.float32)
     _dev(weights, "weights", torch.float32)

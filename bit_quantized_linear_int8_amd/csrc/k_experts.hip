@@ -304,7 +304,9 @@ __global__ __launch_bounds__(256) void k_experts_codes(const float* __restrict__
     __shared__ float red[4];
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int64_t slot = (int64_t)blockIdx.x * (4 / WPR) + (WPR == 1 ? wave : 0);
-    if (slot >= offsets[E] || slot >= P) return;             // (the whole block with WPR == 4)
+    // slots in no expert's range have no h: those past the last range, and those
+    // before the first one where the caller holds a part of the experts
+    if (slot < offsets[0] || slot >= offsets[E] || slot >= P) return;        // (the whole block with WPR == 4)
     const float* x = h + slot * F;
     constexpr int LANES = 64 * WPR;
     const int lp = WPR == 1 ? lane : (int)threadIdx.x;

@@ -667,7 +667,9 @@ qa_status qa_route_experts(const void* logits, qa_dtype dtype, int64_t T, int64_
  *   Xq, s_x  i8 [T x K], f32 [T] (qa_rmsnorm_int8 or qa_quantize_rowwise_int8)
  *   weights, order, offsets   of qa_route_experts: f32 [T x k], i32 [T k],
  *            i32 [E + 1], ranges ascending and disjoint, each pair at most once
- *            (others give unspecified values; no access leaves the arrays)
+ *            (others give unspecified values; no access leaves the arrays).
+ *            E may be a part of the experts that were routed to: their weights
+ *            and their E + 1 starts out of the whole offsets, with all of order
  *   W13, s13 i8 [E x 2F x K] (gate rows, then up rows), f32 [E x 2F]
  *   W2, s2   i8 [E x K x F], f32 [E x K]; scales per output channel
  *   out      [T x K] of out_dtype

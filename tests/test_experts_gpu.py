@@ -148,6 +148,20 @@ def test_workspace_of_any_content():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("first,last", [(0, 3), (2, 5), (4, 9), (8, 9)])
+@pytest.mark.parametrize("T", [6, 40, 600])
+def test_a_part_of_the_experts(T, first, last):
+    """The experts that one of several devices holds: their weights and their part of `offsets`, which then starts past 0
+    and ends before the last pair.  The other experts' pairs add nothing, whatever the workspace held."""
+    c, ids = make(T, 144, 80, 9, 3)
+    part = {**c, "offsets": c["offsets"][first:last + 1]}
+    for name in ("W13", "s13", "W2", "s2"):
+        part[name] = c[name][first:last]
+    mine = torch.where((ids >= first) & (ids < last), ids - first, torch.full_like(ids, -1))
+    n = qa.qa_experts_int8_workspace(T, 144, 3, last - first, 80)
+    check(part, mine, dt="f32", workspace=torch.full((n,), 255, dtype=torch.uint8, device=DEV))
+
+
 def test_refusals():
     c, _ = make(4, 64, 32, 2, 2)
     with pytest.raises(qa.QAError):
