@@ -143,14 +143,14 @@ __device__ __forceinline__ v4f mfma16(u32x4 x, u32x4 y, v4f c) {
 
 // ---------------------------------------------------------------------------
 // Few tokens: a block per token and 16 ranks, a wave on each.  The token's row
-// is requested before its adapter is looked up.  Bound by latency: 5.0 us at 16
-// tokens, K = 4096, rank 16.
+// is requested before its adapter is looked up (without requests nothing is: X may
+// be NULL then).  Bound by latency: 5.0 us at 16 tokens, K = 4096, rank 16.
 // ---------------------------------------------------------------------------
 template <bool BF>
 __global__ __launch_bounds__(1024) void k_lora_down_token(LoraArgs a) {
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int64_t m = blockIdx.x;
-    const rsrc_t rx = make_rsrc(a.X + m * a.K, a.K * 2);
+    const rsrc_t rx = make_rsrc(a.X + m * a.K, a.R == 0 ? 0 : a.K * 2);
     const uint32_t KB = (uint32_t)a.K * 2;
     constexpr int U = 8;
     u32x4 x[U], w[U];

@@ -703,7 +703,8 @@ qa_status qa_experts_int8(const int8_t* Xq, const float* s_x, int64_t T, int64_t
  *   which    i32 [R]: adapter of a request; outside 0 .. L-1: none
  *   out      [M x N] of out_dtype
  *   workspace  qa_qlinear_int8_lora_workspace(M, K, r) bytes (any content)
- * With R == 0 or L == 0 the adapter arrays may be NULL.
+ * With R == 0 or L == 0 X, A, B, alpha, seg and which are not read and may be
+ * NULL.
  * Errors (QA_ERR_SHAPE): M, N, L or R negative, M > 2^23, N, L or R past
  * 2^31 - 1, ceil(M / 64) ceil(N / 128) >= 2^23, K not a positive multiple of
  * 16 up to 131072, r not a multiple of 8 in 8..256; (QA_ERR_VALUE) dtype not fp16 / bf16, bad out_dtype; NULL pointers; Xq, X,

@@ -114,6 +114,22 @@ def test_no_requests(M):
     check(c)
 
 
+@pytest.mark.parametrize("L,R", [(0, 0), (0, 3), (2, 0)])
+@pytest.mark.parametrize("M,N", [(4, 48), (20, 48), (64, 48), (100, 48), (700, 4100)])
+def test_adapter_arrays_that_are_null(M, N, L, R):
+    """Without requests or without adapters X, A, B, alpha, seg and which are not read, in any form of the call."""
+    c = make(M, 272, N, 16, 2, [0, M], [-1])
+    want = qa.qa_qlinear_int8_lora(**c, out_dtype=torch.float32)
+    out = torch.empty(M, N, device=DEV)
+    ws = torch.empty(qa.qa_qlinear_int8_lora_workspace(M, 272, 16), dtype=torch.uint8, device=DEV)
+    p = lambda t: t.data_ptr()
+    s = qa.lib().qa_qlinear_int8_lora(p(c["Xq"]), p(c["s_x"]), None, qa.QA_F16, M, 272, p(c["Wq"]), p(c["s_w"]), N, None,
+                                      None, None, 16, L, None, None, R, p(out), qa.QA_F32, p(ws), ws.numel(),
+                                      torch.cuda.current_stream().cuda_stream)
+    assert s == 0 and qa.last_error() == ""
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("M", [4, 100])
 def test_base_alone_is_the_int8_linear(M):
     c = make(M, 256, 64, 8, 1, [0, M], [-1])
