@@ -13,7 +13,11 @@
 //
 // The inner products h stay in fp32.  Where the second product runs on MFMA they
 // enter it as two 16-bit numbers hi + lo = h 2^-e (e from the row's largest |h| of
-// 32 ranks), so that neither the type's range nor its digits limit them.
+// 32 ranks), so that the type's range does not limit them.  That keeps h to 2^-23
+// of the row's largest in fp16 and to 2^-17 in bf16: next to an output rounded to
+// 16 bits (2^-12 or 2^-9) little, but not next to one in fp32, for which bf16 takes
+// a third number (all of fp32's digits).  A row with an infinity or NaN among its h
+// ends as NaN.
 #include "qa_tile.hpp"
 #include "qa_launch.hpp"
 
@@ -383,7 +387,11 @@ __global__ __launch_bounds__(256) void k_lora_down_tile(LoraArgs a) {
 // epilogue's latency; bound by the tile product's loads and LDS reads.  777 x 4096
 // x 4096, rank 64 (48 requests): 34 us, 6 of them the adapters'; there a stage's
 // chain on the CU is the bound (0.36 us each, 32 of them).
-template <class C, bool BF>
+//
+// THIRD: bf16 with fp32 outputs, h in three numbers: 124 us instead of 122 at 2048 x
+// 11008 x 4096, rank 16, and 142 instead of 138 at rank 64 (the largest tile spills
+// six registers then; tiles of 128 x 128 instead take 133 and 148).
+template <class C, bool BF, bool THIRD>
 __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t tiles_m, int32_t tiles_n) {
     extern __shared__ uint8_t smem[];
     int tm, tn;
@@ -418,11 +426,12 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
     const int64_t mw = m0 + (wave / C::WN) * C::TM, nw = n0 + (wave % C::WN) * C::TN;   // the wave's tile
     if (!EARLY) rows();
     // The adapters' part, 32 ranks at a time: the tile's rows of h (hi and lo) into
-    // the freed LDS, 16-byte chunk c of row r at c ^ (r & 7), with their scales; then the distinct adapters of
+    // the freed LDS, 16-byte chunk c of row r at c ^ (r & 7), with their scales (and the
+    // third number's rows of 64 bytes behind them); then the distinct adapters of
     // the wave's rows in turn (EARLY: the next one's rows of B in flight while one is
     // multiplied).  A row takes the product of its own adapter alone.
     constexpr int HC = C::BM * 8 / C::THREADS;               // quads of ranks of h per thread
-    static_assert(HC * C::THREADS == C::BM * 8 && C::BM * 132 <= C::LDS, "h of the tile");
+    static_assert(HC * C::THREADS == C::BM * 8 && C::BM * (THIRD ? 196 : 132) <= C::LDS, "h of the tile");
     const int groups = (a.r + 31) / 32;
     const rsrc_t none = make_rsrc(a.B, 0);
     v4f hc[HC];
@@ -475,6 +484,9 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
             for (int q = 0; q < 4; ++q) o[i][j][q] = (float)acc[i][j][q] * sx[i] * sw[q];
     }
     float* ups = reinterpret_cast<float*>(smem + C::BM * 128);               // 2^e of a row
+    auto third_at = [&](int r, int c) -> uint8_t* {          // 16-byte chunk c of row r of the third number
+        return smem + C::BM * 132 + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    };
     for (int g = 0; g < groups; ++g) {
         if (g > 0) {
             request(g);
@@ -484,7 +496,7 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
         for (int q = 0; q < HC; ++q) {
             // thread: 4 ranks of row r; the row's largest |h| over its 8 threads, 2^e
             // from its exponent bits with hi in [2^7, 2^8), kept within normal
-            // numbers; an infinite or NaN row keeps its values
+            // numbers (an infinite or NaN row keeps its scale)
             const int P = q * C::THREADS + threadIdx.x, r = P >> 3, c = P & 7;
             float mx = fmaxf(fmaxf(__builtin_fabsf(hc[q][0]), __builtin_fabsf(hc[q][1])),
                              fmaxf(__builtin_fabsf(hc[q][2]), __builtin_fabsf(hc[q][3])));
@@ -499,6 +511,13 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
                 const float t = hc[q][e] * down;
                 hi[e] = BF ? f2bf(t) : f2h(t);
                 lo[e] = BF ? f2bf(t - wide(hi[e], true)) : f2h(t - h2f(hi[e]));
+            }
+            if constexpr (THIRD) {
+                uint16_t z[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[e] = f2bf(hc[q][e] * down - wide(hi[e], true) - wide(lo[e], true));
+                *reinterpret_cast<u32x2*>(third_at(r, c >> 1) + (c & 1) * 8) =
+                    u32x2{z[0] | ((uint32_t)z[1] << 16), z[2] | ((uint32_t)z[3] << 16)};
             }
             uint8_t* row = smem + r * 128 + (c & 1) * 8;
             *reinterpret_cast<u32x2*>(row + (((c >> 1) ^ (r & 7)) << 4)) =
@@ -524,9 +543,13 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
                 const float up = ups[r];
                 const u32x4 hi = *reinterpret_cast<const u32x4*>(smem + r * 128 + ((q16 ^ (r & 7)) << 4));
                 const u32x4 lo = *reinterpret_cast<const u32x4*>(smem + r * 128 + (((q16 + 4) ^ (r & 7)) << 4));
+                u32x4 z = u32x4{0, 0, 0, 0};
+                if constexpr (THIRD) z = *reinterpret_cast<const u32x4*>(third_at(r, q16));
 #pragma unroll
                 for (int j = 0; j < C::FN; ++j) {
-                    v4f d = mfma16<BF>(b0[j], lo, v4f{0, 0, 0, 0});
+                    v4f d = v4f{0, 0, 0, 0};
+                    if constexpr (THIRD) d = mfma16<BF>(b0[j], z, d);
+                    d = mfma16<BF>(b0[j], lo, d);
                     d = mfma16<BF>(b0[j], hi, d);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) o[i][j][q] = mine[i] ? __builtin_fmaf(d[q], up, o[i][j][q]) : o[i][j][q];
@@ -581,14 +604,14 @@ size_t lora_scratch_bytes(int64_t M, int64_t K, int64_t r) {
     return ad + up256((size_t)lora_splits(K) * ((size_t)(r + 31) / 32) * (size_t)M * 128);
 }
 
-template <class C, bool BF>
+template <class C, bool BF, bool THIRD>
 static hipError_t run_lora_tile(const LoraArgs& a, hipStream_t st) {
     const int tm = (int)((a.M + C::BM - 1) / C::BM), tn = (int)((a.N + C::BN - 1) / C::BN);
-    hipLaunchKernelGGL((k_lora_tile<C, BF>), dim3((unsigned)(tm * tn)), dim3(C::THREADS), C::LDS, st, a, tm, tn);
+    hipLaunchKernelGGL((k_lora_tile<C, BF, THIRD>), dim3((unsigned)(tm * tn)), dim3(C::THREADS), C::LDS, st, a, tm, tn);
     return hipGetLastError();
 }
 
-template <bool BF>
+template <bool BF, bool THIRD>
 static hipError_t run_lora(const LoraArgs& a, hipStream_t st) {
     hipError_t e;
     if (few_tokens(a.M, a.N)) {
@@ -619,10 +642,10 @@ static hipError_t run_lora(const LoraArgs& a, hipStream_t st) {
     // A tile alone on its CU takes as long as two (a stage's chain of barrier, LDS
     // reads and MFMAs), so small tiles as long as 512 of them fit two at a time.
     const int64_t small = ((a.M + 63) / 64) * ((a.N + 63) / 64), tiles = ((a.M + 127) / 128) * ((a.N + 127) / 128);
-    if (small <= 512) return run_lora_tile<tile::Cfg<64, 64, 2, 4, 3>, BF>(a, st);
-    if (tiles <= 256) return run_lora_tile<tile::Cfg<64, 128, 2, 4, 3>, BF>(a, st);
-    if (tiles <= 512) return run_lora_tile<tile::Cfg<128, 128, 2, 4, 2>, BF>(a, st);
-    return run_lora_tile<tile::Cfg<128, 192, 2, 4, 2>, BF>(a, st);
+    if (small <= 512) return run_lora_tile<tile::Cfg<64, 64, 2, 4, 3>, BF, THIRD>(a, st);
+    if (tiles <= 256) return run_lora_tile<tile::Cfg<64, 128, 2, 4, 3>, BF, THIRD>(a, st);
+    if (tiles <= 512) return run_lora_tile<tile::Cfg<128, 128, 2, 4, 2>, BF, THIRD>(a, st);
+    return run_lora_tile<tile::Cfg<128, 192, 2, 4, 2>, BF, THIRD>(a, st);
 }
 
 hipError_t launch_lora_i8(const int8_t* Xq, const float* s_x, const void* X, bool bf16, int64_t M, int64_t K,
@@ -641,7 +664,8 @@ hipError_t launch_lora_i8(const int8_t* Xq, const float* s_x, const void* X, boo
     a.splits = lora_splits(K);
     a.out = out; a.dt = out_dtype;
     a.vec = N % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (out_dtype == 0 ? 15 : 7)) == 0;
-    return bf16 ? run_lora<true>(a, st) : run_lora<false>(a, st);
+    if (!bf16) return run_lora<false, false>(a, st);
+    return out_dtype == 0 ? run_lora<true, true>(a, st) : run_lora<true, false>(a, st);
 }
 
 }  // namespace qa

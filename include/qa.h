@@ -693,7 +693,11 @@ qa_status qa_experts_int8(const int8_t* Xq, const float* s_x, int64_t T, int64_t
  *             + alpha[a] sum_j (sum_k X[m][k] A[a][j][k]) B[a][n][j]
  * with a the adapter of the request that holds token m; tokens of requests
  * with adapter -1, and tokens of no request, take the first line alone.  The
- * sum is formed in fp32 and rounded once.
+ * sum is formed in fp32 and rounded once.  For many tokens the inner products
+ * over k enter the second product with a relative step of at most 2^-17 (dtype
+ * bf16, 16-bit out) or 2^-23 (otherwise) of the largest of 32 ranks; for few, and
+ * for bf16 with fp32 out, in fp32.  One that is infinite or NaN makes its token's
+ * outputs infinite or NaN.
  *   Xq, s_x  i8 [M x K], f32 [M]: the tokens' codes (qa_rmsnorm_int8)
  *   X        [M x K] of dtype (fp16 or bf16): the values the adapters see (its y)
  *   Wq, s_w  i8 [N x K], f32 [N]
@@ -707,9 +711,9 @@ qa_status qa_experts_int8(const int8_t* Xq, const float* s_x, int64_t T, int64_t
  * NULL.
  * Errors (QA_ERR_SHAPE): M, N, L or R negative, M > 2^23, N, L or R past
  * 2^31 - 1, ceil(M / 64) ceil(N / 128) >= 2^23, K not a positive multiple of
- * 16 up to 131072, r not a multiple of 8 in 8..256; (QA_ERR_VALUE) dtype not fp16 / bf16, bad out_dtype; NULL pointers; Xq, X,
- * Wq, A, B not 16-byte, others not 4-byte, workspace not 256-byte aligned;
- * small workspace.
+ * 16 up to 131072, r not a multiple of 8 in 8..256; (QA_ERR_VALUE) dtype not
+ * fp16 / bf16, bad out_dtype; NULL pointers; Xq, X, Wq, A, B not 16-byte, others
+ * not 4-byte, workspace not 256-byte aligned; small workspace.
  * ------------------------------------------------------------------------- */
 size_t qa_qlinear_int8_lora_workspace(int64_t M, int64_t K, int32_t r);
 qa_status qa_qlinear_int8_lora(const int8_t* Xq, const float* s_x, const void* X, qa_dtype dtype, int64_t M,

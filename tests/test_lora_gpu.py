@@ -151,6 +151,33 @@ def test_inner_products_past_the_range_of_fp16(M):
     check(c, out="f32")
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,K,N,top", [(20, 256, 40, 255), (100, 256, 40, 255), (100, 2304, 40, 80), (520, 256, 4200, 255),
+                                       (1030, 80, 4520, 255), (1100, 80, 7720, 255)])
+def test_inner_products_keep_their_digits(M, K, N, top, dt):
+    """Whole numbers below 2^24 with fp32 outputs: every product and sum is exact in fp32, in any order, and each column
+    of B picks one rank, so that the outputs are the inner products themselves."""
+    g = torch.Generator(device=DEV).manual_seed(M + K)
+    n = lambda *s: torch.randint(-top, top + 1, s, device=DEV, generator=g)
+    X, A, r = n(M, K), n(2, 40, K), 40
+    at = (torch.arange(M, device=DEV) < M // 3).long()
+    c = dict(Xq=torch.zeros(M, K, dtype=torch.int8, device=DEV), s_x=torch.ones(M, device=DEV), X=X.to(DT[dt]),
+             Wq=torch.zeros(N, K, dtype=torch.int8, device=DEV), s_w=torch.ones(N, device=DEV), A=A.to(DT[dt]),
+             B=torch.eye(r, device=DEV).repeat(2, N // r, 1).to(DT[dt]), alpha=torch.ones(2, device=DEV),
+             seg=torch.tensor([0, M // 3, M], dtype=torch.int32, device=DEV),
+             which=torch.tensor([1, 0], dtype=torch.int32, device=DEV))
+    want = torch.stack([X.double() @ A[i].double().T for i in range(2)])[at, torch.arange(M, device=DEV)]
+    assert 2 ** 17 < float(want.abs().max()) < 2 ** 22       # past two numbers of bf16, within two of fp16
+    out = qa.qa_qlinear_int8_lora(**c, out_dtype=torch.float32)
+    assert torch.equal(out.double(), want.repeat(1, N // r))
+
+
+@pytest.mark.parametrize("M,K,N,r,L,R", [(9, 528, 100, 24, 3, 4), (100, 272, 130, 72, 4, 11), (520, 96, 4200, 40, 3, 5),
+                                         (1100, 96, 7700, 16, 3, 6)])
+def test_bf16_adapters_with_fp32_outputs(M, K, N, r, L, R):
+    check(make(M, K, N, r, L, *spread(M, R, L), dt="bf16"), out="f32", dt="bf16")
+
+
 @pytest.mark.parametrize("M", [30, 100])
 def test_a_broken_adapter_stays_in_its_request(M):
     c = make(M, 128, 64, 16, 2, [0, 10, M], [0, 1])
