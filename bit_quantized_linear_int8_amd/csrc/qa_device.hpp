@@ -263,22 +263,26 @@ __device__ __forceinline__ float absmax8f(const float* x) {
     return a;
 }
 
-// exp(x) for x <= 88: the exponent of 2 in two parts, so that the result is off
-// by about the exponential's own rounding whatever the size of x.  (The library
-// function's range handling costs three times as much.)
-__device__ __forceinline__ float fexp(float x) {
+// exp(x) 2^shift, below 2^127: the exponent of 2 in two parts, so that the result
+// is off by about the exponential's own rounding whatever the size of x (the shift
+// is a whole number that leaves a sum no larger than x log2 e, so it rounds nothing).
+// (The library function's range handling costs three times as much.)
+__device__ __forceinline__ float fexp(float x, float shift = 0.0f) {
     constexpr float L2E = 1.44269502162933349609375f, L2E_LO = 1.925963033500011079e-8f, LN2 = 0.693147182464599609375f;
     x = fmaxf(x, -104.0f);                                   // exp(-104) is 0 in fp32
     const float t = x * L2E;
     const float lo = __builtin_fmaf(x, L2E, -t) + x * L2E_LO;
-    const float e = __builtin_amdgcn_exp2f(t);
+    const float e = __builtin_amdgcn_exp2f(t + shift);
     return __builtin_fmaf(e, lo * LN2, e);
 }
-// 1 / (1 + exp(-x)), with one correction of the reciprocal; below -88 about 2^-127.
+// 1 / (1 + exp(-x)), with one correction of the reciprocal.  Below -64 the 1 is
+// under fp32's last digit: there it is 1 / exp(-x) with exp(-x) taken 2^-64 times
+// as large, so that it stays in range down to where the result is 0 in fp32.
 __device__ __forceinline__ float sigmoid(float x) {
-    const float d = 1.0f + fexp(fminf(-x, 88.0f));
+    const bool low = x < -64.0f;
+    const float d = (low ? 0.0f : 1.0f) + fexp(fminf(-x, 110.0f), low ? -64.0f : 0.0f);
     const float r = __builtin_amdgcn_rcpf(d);
-    return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+    return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r) * (low ? 0x1p-64f : 1.0f);
 }
 
 }  // namespace qa

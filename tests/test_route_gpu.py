@@ -194,6 +194,35 @@ def test_two_infinite_logits_share_the_weight():
     assert ids[0].tolist() == [2, 5, 0] and w[0].tolist() == [0.5, 0.5, 0.0]
 
 
+@pytest.mark.parametrize("E,k", [(12, 12), (16, 8), (600, 20)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_sigmoid_scores_far_below_zero(E, k, renorm):
+    """Scores down to fp32's smallest number and to 0, chosen through a bias of zeros."""
+    x = torch.full((70, E), -300.0, device=DEV)
+    steps = torch.linspace(-104.0, -20.0, 70, device=DEV)
+    for j in range(min(k, 8)):
+        x[:, (5 * j + 3) % E] = steps - 1.25 * j
+    kw = dict(score=qa.QA_SCORE_SIGMOID, renorm=renorm)
+    ids, w, _, _ = qa.qa_route_experts(x, k, bias=torch.zeros(E, device=DEV), **kw)
+    s = torch.sigmoid(x.double())
+    picked = s.gather(1, ids.long())
+    # a score rounds to fp32's step below its smallest normal number, 2^-149; otherwise the bounds of check()
+    unit, rel = 2.0 ** -149, 240 * 2.0 ** -24
+    if renorm:
+        total = picked.sum(1, keepdim=True)
+        none = (picked < unit / 2).all(1)
+        near = (total[:, 0] < k * unit)                      # rounded away or not: nothing to compare
+        want = torch.where(total > 0, picked / total, picked)
+        room = (picked * rel + unit) / total + want * (rel + k * unit / total)
+        assert (w[none] == 0).all()
+        assert ((w.double() - want).abs() <= room)[~near].all()
+    else:
+        assert ((w.double() - picked).abs() <= picked * rel + unit).all()
+    # the largest first, as far as fp32 tells them apart
+    best = s.topk(k, 1).values
+    assert ((picked - best).abs() <= best * 2 * rel + 2 * unit).all()
+
+
 def test_strided_logits():
     x = logits_of(100, 200, "f16")
     check(x[:, 3:67], 4)
