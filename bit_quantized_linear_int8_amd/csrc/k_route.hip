@@ -8,9 +8,10 @@
 //   largest; then the k largest c_e, ties to the lower index
 //   w_j  = s_{e_j} (/ sum_j s_{e_j}) * scale
 //
-// Softmax keeps the order of the logits, so without a bias (and with groups
-// valued by their largest member) the choice is made on the logits themselves
-// and the exponentials are taken for the k chosen and the row's sum alone.
+// Both scores keep the order of the logits, so without a bias (and with groups
+// valued by their largest member) the choice is made on the logits themselves,
+// which also differ where their scores round to the same number (sigmoid(17) is 1
+// in fp32), and the exponentials are taken for the k chosen and softmax's sum alone.
 //
 // A logit of -inf or NaN masks its expert; where fewer than k are left, the
 // last slots hold expert -1 with weight 0 and are in no group.
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
     const bool live = t < a.T;
     const uint8_t* xp = static_cast<const uint8_t*>(a.x) + (live ? t : 0) * a.ld * (DT == 0 ? 4 : 2);
     // the choice goes by the logits themselves
-    const bool by_logit = !a.sigmoid && !a.bias && (a.groups == 1 || !a.top2);
+    const bool by_logit = !a.bias && (a.groups == 1 || !a.top2);
     float c[EPL], s[EPL];                                    // chosen by (-inf: not to be chosen), score
 #pragma unroll
     for (int i = 0; i < EPL; ++i) c[i] = NEG;
@@ -309,8 +310,10 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
     mx = rmax<LPT>(mx);
     float den = 1.0f;
     if (a.sigmoid) {
+        if (!by_logit) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) s[i] = sigmoid(c[i]);
+            for (int i = 0; i < EPL; ++i) s[i] = sigmoid(c[i]);
+        }
     } else {
         den = 0.0f;
         const float m0 = mx == NEG ? 0.0f : mx;
@@ -455,7 +458,10 @@ __global__ __launch_bounds__(TB * LPT) void k_route(RouteArgs a) {
         const int j = n * LPT + l;
         id[n] = j < a.k ? sid[tb][j] : -1;
         wt[n] = 0.0f;
-        if (id[n] >= 0) wt[n] = by_logit ? expf(swt[tb][j] - mx) / den : swt[tb][j];
+        if (id[n] >= 0) {
+            wt[n] = swt[tb][j];
+            if (by_logit) wt[n] = a.sigmoid ? sigmoid(wt[n]) : expf(wt[n] - mx) / den;
+        }
         sum += wt[n];
     }
     sum = rsum<LPT>(sum);

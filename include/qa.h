@@ -632,8 +632,10 @@ qa_status qa_rmsnorm_int8(const void* X, int64_t ldx, const void* residual_or_nu
  *   order   i32 [T k]: the pairs t k + j grouped by expert, ascending within
  *           an expert; places past the last pair hold -1
  *   offsets i32 [E + 1]: expert e's pairs are order[offsets[e] .. offsets[e+1])
- * Softmax without a bias (and with groups valued by their largest expert)
- * chooses by the logits themselves, which have the same order.
+ * Without a bias (and with groups valued by their largest expert) the choice
+ * goes by the logits themselves, which have the scores' order; otherwise by
+ * scores in fp32, where those of different logits may be equal (sigmoid is 1
+ * above 17, softmax 0 far below the row's largest): such ties go to the lower index.
  * A logit (or bias) of -infinity or NaN masks its expert; a logit of +infinity
  * counts as the largest finite value.  Where fewer than k experts are left, the last slots
  * are expert -1 with weight 0 and are in no expert's range.

@@ -223,6 +223,36 @@ def test_sigmoid_scores_far_below_zero(E, k, renorm):
     assert ((picked - best).abs() <= best * 2 * rel + 2 * unit).all()
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,k,groups", [(64, 8, 1), (64, 20, 1), (600, 8, 1), (128, 8, 4), (100, 6, 10)])
+def test_sigmoid_keeps_the_order_of_saturated_logits(E, k, groups, renorm):
+    """Logits past 17, where the score is 1 in fp32, and below -104, where it is 0: the largest are chosen all the same."""
+    g = torch.Generator(device=DEV).manual_seed(E + k)
+    x = torch.empty(70, E, device=DEV)
+    for t in range(70):
+        p = torch.randperm(E, device=DEV, generator=g).float()
+        x[t] = (18 + p, -89 - p / 64, -200 - p, 40 - 3 * p)[t % 4]
+    x[2::4, 7] = -90.0
+    ids, w, _, _ = qa.qa_route_experts(x, k, score=qa.QA_SCORE_SIGMOID, groups=groups, top_groups=max(1, groups // 2),
+                                       renorm=renorm)
+    v = x.view(70, groups, -1)
+    if groups > 1:
+        kept = torch.zeros(70, groups, dtype=torch.bool, device=DEV)
+        v = v.masked_fill(~kept.scatter_(1, v.amax(2).topk(groups // 2, 1).indices, True)[:, :, None], -math.inf)
+    want = v.reshape(70, E).topk(k, 1)
+    assert torch.equal(ids.long(), want.indices)
+    s = torch.sigmoid(want.values.double())
+    # fp32's step below its smallest normal number, and the bounds of check()
+    unit, rel = 2.0 ** -149, 240 * 2.0 ** -24
+    if renorm:
+        total = s.sum(1, keepdim=True)
+        some = total[:, 0] > 1e3 * unit                      # else the scores are 0 in fp32, or lost nearly all digits
+        got, ref = w.double()[some], (s / total)[some]
+        assert ((got - ref).abs() <= ref * rel + (1 + k * ref) * unit / total[some]).all() and some.sum() > 40
+    else:
+        assert ((w.double() - s).abs() <= s * rel + unit).all()
+
+
 def test_strided_logits():
     x = logits_of(100, 200, "f16")
     check(x[:, 3:67], 4)
