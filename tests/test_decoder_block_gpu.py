@@ -29,6 +29,24 @@ def test_block_against_fp32(example, lengths):
     assert rel < 0.05
 
 
+def test_single_tokens_have_the_prompts_sum_and_experts(example):
+    """The running sum does not hang on the choice of experts, and the choice on the sums' order for few tokens alone."""
+    block = example.DecoderBlock(K=512, F=256, E=8, k=2, adapters=3, seed=3)
+    g = torch.Generator(device="cuda:0").manual_seed(5)
+    x, r = (torch.randn(130, 512, device="cuda:0", generator=g).half() for _ in range(2))
+    seg, which = example.requests([64, 66], 3)
+    out, total, ids = block(x, r, seg, which)
+    seg1 = torch.tensor([0, 1], dtype=torch.int32, device="cuda:0")
+    same = 0
+    for t in (0, 63, 64, 129):
+        one, sum1, ids1 = block(x[t:t + 1], r[t:t + 1], seg1, which[t // 64:t // 64 + 1] if t < 128 else which[1:2])
+        assert (sum1[0].float() - total[t].float()).abs().max() <= 2.0 ** -9 * total[t].float().abs().max()
+        if torch.equal(ids1[0], ids[t]):
+            same += 1
+            assert float((one[0].float() - out[t].float()).norm() / out[t].float().norm()) < 0.02
+    assert same >= 3
+
+
 def test_single_tokens_agree_with_the_prompt(example):
     """A token's output does not hang on the tokens beside it, up to the order of fp32 sums in the forms for few and
     for many tokens."""

@@ -148,6 +148,13 @@ def test_workspace_of_any_content():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,K,F,E,k", [(2000, 272, 1552, 2, 2), (1111, 144, 2064, 4, 3), (4100, 96, 1536, 1, 1)])
+def test_largest_tiles(T, K, F, E, k):
+    """More than 120 rows for each expert and enough tiles of 128 rows for all of the device."""
+    assert T * k // E >= 120 and (T * k // 128) * ((2 * F + 191) // 192) >= 512
+    check(*make(T, K, F, E, k))
+
+
 @pytest.mark.parametrize("first,last", [(0, 3), (2, 5), (4, 9), (8, 9)])
 @pytest.mark.parametrize("T", [6, 40, 600])
 def test_a_part_of_the_experts(T, first, last):

@@ -85,6 +85,14 @@ def test_every_size_of_tile(M, N):
     check(make(M, 144, N, 40, 3, *spread(M, 5, 3)), out="f32")
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("K", [1040, 2064, 4112, 8208, 9216])
+@pytest.mark.parametrize("M,N,r", [(5, 80, 24), (20, 48, 128), (50, 33, 16), (100, 130, 72)])
+def test_long_rows(M, N, r, K, dt):
+    """K past one batch of the loads of every form, whole and ragged; for many tokens the inner products in 2 to 8 parts."""
+    check(make(M, K, N, r, 3, *spread(M, 6, 3), dt=dt), out="f32", dt=dt)
+
+
 @pytest.mark.parametrize("M", [9, 90])
 def test_tokens_outside_every_request(M):
     """The first request starts after token 0 and the last one ends before the end."""

@@ -264,6 +264,25 @@ def test_many_blocks(T):
     check(logits_of(T, 24, "bf16", std=1.0), 3, renorm=False)
 
 
+@pytest.mark.parametrize("T,E,k,kw", [
+    (16385, 24, 3, dict(renorm=False)), (17000, 250, 8, dict(score="sigmoid")),
+    (16449, 128, 8, dict(score="sigmoid", bias=True, groups=8, top_groups=4, group_top=2)),
+    (16400, 255, 12, dict(groups=5, top_groups=3, group_top=2))])
+def test_blocks_of_many_tokens(T, E, k, kw):
+    """More than 16384 tokens: 64 of them to a block, the last one ragged; groups inside the lanes and, at 51 experts a
+    group, in LDS."""
+    x = logits_of(T, E, "f32", seed=2)
+    x[T // 2] = -math.inf
+    x[T - 1, 2:] = -math.inf
+    bias = torch.linspace(-0.2, 0.2, E, device=DEV) if kw.get("bias") else None
+    check(x, k, **{**kw, "bias": bias})
+
+
+@pytest.mark.parametrize("T", [1, 64])
+def test_one_block_with_groups_in_lds(T):
+    check(logits_of(T, 255, "f32", seed=4), 9, groups=5, top_groups=2, group_top=2)
+
+
 def test_one_expert_takes_all():
     x = logits_of(3000, 16, "f32") * 0.1
     x[:, 7] = 50.0
