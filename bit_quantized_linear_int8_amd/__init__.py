@@ -680,7 +680,8 @@ def qa_route_experts_workspace(T: int, E: int, k: int) -> int:
 def qa_route_experts(logits, k: int, bias=None, score=QA_SCORE_SOFTMAX, groups=1, top_groups=1, group_top=1,
                      renorm=True, scale=1.0, workspace=None, stream=None):
     """The k experts of each token -> (ids i32 [T x k], weights f32 [T x k], order i32 [T k], offsets i32 [E + 1]):
-    the chosen experts in descending order of score + bias, their weights, and the pairs t k + j by expert."""
+    the chosen experts in descending order of score + bias, their weights, and the pairs t k + j by expert.  ids,
+    order and offsets are views of one allocation: clone() one that is to be kept or saved without the others."""
     if logits.dtype not in _DTYPE_CODE:
         raise TypeError("logits must be fp32, fp16 or bf16, got %s" % logits.dtype)
     ld = _rows(logits, "logits", logits.dtype)

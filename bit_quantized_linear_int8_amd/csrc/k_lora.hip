@@ -90,7 +90,9 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& a, int64_t m) {
 
 // Tokens [b, e) and request (-1: none) of block x of the requests' tiles of 16
 // tokens, requests in order: every wave counts the tiles of 256 requests at a
-// time, four to a lane, and sums them over the lanes.
+// time, four to a lane, and sums them over the lanes.  Whatever the starts hold,
+// 0 <= b < e <= M; starts that fall may put a token into two tiles or, past the
+// launch's blocks, into none.
 __device__ __forceinline__ int tile_of(const LoraArgs& a, int x, int64_t& b, int64_t& e) {
     const int lane = threadIdx.x & 63;
     for (int s0 = 0; s0 < a.R; s0 += 256) {
@@ -409,7 +411,7 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_lora_tile(LoraArgs a, int32_t
         for (int i = 0; i < C::FM; ++i) {
             const int64_t m = m0 + (wave / C::WN) * C::TM + i * 16 + r16;
             ad[i] = m < a.M ? a.ad[m] : -1;
-            if (ad[i] >= a.L) ad[i] = -1;                    // no adapter was written: starts that descend
+            if (ad[i] >= a.L) ad[i] = -1;                    // starts that fall may leave what the workspace held
             sx[i] = m < a.M ? a.s_x[m] : 0.0f;
         }
     };

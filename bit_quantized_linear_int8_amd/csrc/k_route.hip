@@ -171,7 +171,7 @@ struct RouteArgs {
     bool vec;                // rows allow whole-vector loads of EPL elements
 };
 
-// Exclusive prefix over the block's threads of two values each; *all gets the total.
+// Exclusive prefix of v over the block's threads; *all gets the total.
 template <int THREADS>
 __device__ __forceinline__ int block_prefix(int v, int32_t* wsum, int* all) {
     const int lane = threadIdx.x & 63, wave = wave_id();

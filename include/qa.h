@@ -705,7 +705,8 @@ qa_status qa_experts_int8(const int8_t* Xq, const float* s_x, int64_t T, int64_t
  *   Wq, s_w  i8 [N x K], f32 [N]
  *   A, B     [L x r x K], [L x N x r] of dtype; alpha f32 [L]
  *   seg      i32 [R + 1]: request i holds the tokens seg[i] .. seg[i + 1]
- *            (not descending; empty requests are allowed)
+ *            (not descending; empty requests are allowed; starts that fall
+ *            give unspecified values, no access leaves the arrays)
  *   which    i32 [R]: adapter of a request; outside 0 .. L-1: none
  *   out      [M x N] of out_dtype
  *   workspace  qa_qlinear_int8_lora_workspace(M, K, r) bytes (any content)
