@@ -204,7 +204,7 @@ __global__ __launch_bounds__(1024) void k_experts_plan(ExpertArgs a, int32_t* __
 }
 
 // 4099 tokens of 4 experts each, 32 experts, K = 4096, F = 2048: gate and up 340 to
-// 380 us (the clock falls under the load), 1.45 to 1.6 POPS of the pairs' own
+// 385 us (the clock falls under the load), 1.45 to 1.6 POPS of the pairs' own
 // operations, an eighth more with the ragged tiles'; down 200 to 220, 1.25 to 1.4:
 // bound as the tile product is, then by its epilogue (268 MB).  256 tokens of 8, 64
 // experts, F = 1024: 125 and 62 us, 537 and 268 MB of weights, 4.3 TB/s: bound by

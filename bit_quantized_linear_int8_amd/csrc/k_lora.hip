@@ -384,11 +384,13 @@ __global__ __launch_bounds__(256) void k_lora_down_tile(LoraArgs a) {
 }
 
 // Many tokens: the int8 product on LDS tiles; the adapters' part joins the fp32
-// tile before the one rounding.  2048 x 11008 x 4096, rank 16 (8 requests): 108 to 118
-// us, of which the product alone is 100 (1.85 POPS) and the adapters' part the
-// epilogue's latency; bound by the tile product's loads and LDS reads.  777 x 4096
-// x 4096, rank 64 (48 requests): 34 us, 6 of them the adapters'; there a stage's
-// chain on the CU is the bound (0.36 us each, 32 of them).
+// tile before the one rounding.  2048 x 11008 x 4096, rank 16 (8 requests): 112 to 136
+// us with the clock, 125 on average, of which the product alone is 100 at best (1.85
+// POPS) and the adapters' part the epilogue's latency; bound as the tile product is.
+// 777 x 4096 x 4096, rank 64 (48 requests): 33.4 us, 5 of them the adapters' (28.5
+// without any, 29.8 with one for all).  416 tiles, so 160 of the 256 CUs hold two:
+// a block alone on its CU takes 0.36 us for each of the 32 stages and 7 besides, and
+// two do not overlap wholly; waves spend 51% of their time waiting for data.
 //
 // THIRD: bf16 with fp32 outputs, h in three numbers: 124 us instead of 122 at 2048 x
 // 11008 x 4096, rank 16, and 142 instead of 138 at rank 64 (the largest tile spills

@@ -14,9 +14,10 @@
 // that take k_rmsnorm_i8_long, which reads the row three times.
 //
 // Bound by memory from a few hundred rows on (residual added, fp16 or bf16, 7
-// bytes a value): 16384 x 8192 in 156 us, 6.0 TB/s; 2048 x 4096 in 12.3 to 13.3,
-// 4.4 to 4.8; rows that are not multiples of eight values 16384 x 8191 in 211, 4.5;
-// the long form 256 x 32768 in 19, 3.1.  One row of 4096 is a launch and two
+// bytes a value): 16384 x 8192 in 157 us, 6.0 TB/s; 2048 x 4096 in 12.3 to 13.3,
+// 4.4 to 4.8 (13.0 with y kept too, 5.8; in fp32 with y 26.7, 5.3); rows that are not
+// multiples of eight values 16384 x 8191 in 194, 4.8; the long form, which reads x
+// and r three times, 256 x 32768 in 20, 2.9.  One row of 4096 is a launch and two
 // exchanges, 3.2 us.
 #include "qa_device.hpp"
 #include "qa_launch.hpp"

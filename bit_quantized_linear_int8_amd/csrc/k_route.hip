@@ -27,12 +27,15 @@
 // among them is its slot.  For more than 8, or with groups, the bound is taken from
 // the lanes' two largest.  Only where more than 32 reach it (many ties), for k > 16
 // and above 256 experts the rounds are run.  First launch at 50001 x 128 (bf16,
-// k = 8): 28.8 us with the rounds, 17.6 with the bound; at 4096 x 256 in 8 groups
-// 34 and 9.3.  At 50001 tokens it issues 415 vector instructions per wave of four
-// tokens, 9 us of the SIMDs' time; reading the logits is 2.5 us.  32 tokens to a
-// block run it in 14.8 us, but the counts of twice the blocks cost that again in
-// the two launches after (k_route_scan 5.6 us, k_route_scatter 3.2 to 5.2: little
-// more than launches).
+// k = 8): 28.8 us with the rounds, 18.4 with the bound (17.6 at best); at 4096 x 256
+// in 8 groups 34 and 9.6.  With the rounds in this form 4096 x 256 at k = 24 takes
+// 15.3, 4096 x 384 at k = 8 10.8, 4096 x 512 at k = 10 12.2.  At 50001 tokens it
+// issues 415 vector instructions per wave of four tokens, 9 us of the SIMDs' time;
+// reading the logits is 2.5 us.  The rest is waiting (56% of the waves' time): 1024
+// threads of 72 registers leave one block to a CU, with nothing to run at its
+// barriers.  32 tokens to a block run it in 14.8 us, but the counts of twice the
+// blocks cost that again in the two launches after (k_route_scan 5.6 us,
+// k_route_scatter 3.0 to 5.4: little more than launches).
 //
 // The grouping is stable (ascending pair index within an expert) and uses no
 // order-dependent atomics: a token chooses an expert at most once, so a block of

@@ -10,11 +10,15 @@
 // makes the fragment reads of 8 consecutive rows hit 8 different bank groups;
 // the permutation is produced by the chunk that each lane fetches.
 //
-// What bounds it: the loads into LDS and the fragment reads out of it, not the
-// MFMAs (a wave with nothing but fragment reads and MFMAs reaches 3.4 POPS).
-// 64-byte stages fetch every 128-byte line twice from L2, in two stages: at
-// 8192 x 8192 x 4096 a 128 x 128 tile went from 1.61 to 1.97 POPS with 128-byte
-// stages.  Two blocks on a CU overlap one's reads with the other's MFMAs and
+// What bounds it: the chain of a stage (its loads into LDS, barrier, fragment
+// reads, MFMAs), of which two blocks on a CU overlap a part.  The MFMAs are busy
+// for 35 to 42% of the time at 16396 rows of 4096 x 4096 and 2048, waves spend 45%
+// of theirs waiting for data and 36 to 41% for an instruction to issue, and LDS has no
+// bank conflicts.  A wave with nothing but fragment reads and MFMAs reaches 3.4
+// POPS; in this library's loop of 256-row tiles, half the fragment reads changed
+// nothing, so the stages' traffic is the larger part.  64-byte stages fetch every
+// 128-byte line twice from L2, in two stages: at 8192 x 8192 x 4096 a 128 x 128 tile
+// went from 1.61 to 1.97 POPS with 128-byte stages.  Two blocks on a CU overlap one's reads with the other's MFMAs and
 // hide its prologue and epilogue, so the tile is as large as two blocks' LDS
 // allow: 128 x 192 with two stages (80 KB) 2.04 POPS, against 1.81 for 128 x 256
 // (96 KB, one block), and 102 against 118 us at 2048 x 11008 x 4096.  The
