@@ -605,8 +605,8 @@ qa_status qa_gemm_w4a8_group_acc(const int8_t* Xq, const uint32_t* Wp, int64_t M
  * Any K >= 1; rows whose arrays all start at 16-byte boundaries (K, strides)
  * are read and written in whole 16-byte pieces.
  * A row that holds an infinity or NaN, or whose sum of squares passes fp32,
- * gets s = NaN and codes 0 (so a linear's output row is NaN); other rows are
- * unaffected.  g must be finite.
+ * gets s = NaN and codes 0 (so a linear's output row is NaN) and a y of NaNs and
+ * zeros; other rows are unaffected.  g must be finite.
  * Errors: rows < 0, rows > 2^31 - 1, K <= 0, K > 2^26, a stride below K, bad
  * dtype, eps not positive and finite, NULL X / g / Xq / s, X / g / residual /
  * sum / y not aligned to their elements, s not 4-byte aligned.
