@@ -1,4 +1,4 @@
-"""Norm, routing, experts and adapters where byte offsets pass 32 bits: the last rows (experts, adapters) of arrays that are the first
+"""Norm, routing and experts where byte offsets pass 32 bits: the last rows (or experts) of arrays that are the first
 ones over and over give what the first ones give."""
 import pytest
 import torch
@@ -69,6 +69,7 @@ def test_experts(T):
     assert torch.equal(got, want) and float(want.abs().max()) > 0
 
 
+# Adapters: the last of many against a call that has it alone, and tokens that repeat.
 @pytest.mark.parametrize("M,K,N,r,L", [(5, 32768, 64, 256, 280), (100, 32768, 64, 256, 280),       # A past 4 GiB
                                        (5, 16, 12288, 256, 720), (100, 16, 32768, 256, 270)])      # B
 def test_last_adapter(M, K, N, r, L):
