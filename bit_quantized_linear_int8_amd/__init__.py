@@ -21,6 +21,7 @@ QA_F32, QA_F16, QA_BF16 = 0, 1, 2
 QA_SCALE_PER_ROW, QA_SCALE_PER_GROUP, QA_SCALE_PER_TENSOR = 0, 1, 2
 QA_SMOOTH_DIVIDE, QA_SMOOTH_MULTIPLY = 0, 1
 QA_SCORE_SOFTMAX, QA_SCORE_SIGMOID = 0, 1
+QA_ACT_NONE, QA_ACT_RELU, QA_ACT_GELU, QA_ACT_GELU_TANH, QA_ACT_SILU = 0, 1, 2, 3, 4
 
 EXPORTS = (
     "qa_status_string", "qa_last_error",
@@ -40,6 +41,7 @@ EXPORTS = (
     "qa_gemm_i8_i32", "qa_gemm_w4a4_group_acc", "qa_gemm_w4a8_group_acc",
     "qa_rmsnorm_int8", "qa_route_experts_workspace", "qa_route_experts", "qa_experts_int8_workspace",
     "qa_experts_int8", "qa_qlinear_int8_lora_workspace", "qa_qlinear_int8_lora",
+    "qa_kv_write", "qa_kv_read", "qa_attn_decode_workspace", "qa_attn_decode", "qa_qlinear_int8_act",
     "qa_probe_stream_read",
 )
 
@@ -113,6 +115,12 @@ def lib() -> ctypes.CDLL:
             "qa_qlinear_int8_lora_workspace": (SZ, [I64, I64, I32]),
             "qa_qlinear_int8_lora": (S, [P, P, P, S, I64, I64, P, P, I64, P, P, P, I32, I64, P, P, I64, P, S, P, SZ,
                                          P]),
+            "qa_kv_write": (S, [P, I64, P, I64, S, I64, P, I32, I64, I32, I32, I32, P, P, P, P, P]),
+            "qa_kv_read": (S, [P, I64, I32, I64, I32, I32, I32, P, P, P, P, P, P, S, P]),
+            "qa_attn_decode_workspace": (SZ, [I64, I32, I32, I32, I64, I32]),
+            "qa_attn_decode": (S, [P, I64, S, I64, I32, I32, I64, I32, I32, I32, P, P, P, P, P, I64, I64, P, I64, I32, F,
+                                   P, S, P, P, SZ, P]),
+            "qa_qlinear_int8_act": (S, [P, P, I64, I64, P, P, I64, P, S, P, I64, P, I64, S, P]),
             "qa_probe_stream_read": (S, [P, SZ, I32, I32, I32, P, P]),
         }
         for name, (res, args) in sig.items():
@@ -801,6 +809,156 @@ def qa_qlinear_int8_lora(Xq, s_x, X, Wq, s_w, A, B, alpha, seg, which, out_dtype
            lib().qa_qlinear_int8_lora(_a(Xq), _a(s_x), _a(X), _DTYPE_CODE[X.dtype], M, K, _a(Wq), _a(s_w), N, _a(A),
                                       _a(B), _a(alpha), r, L, _a(seg), _a(which), R, _a(out), _DTYPE_CODE[out.dtype],
                                       _a(workspace), workspace.numel(), _s(stream)))
+    return out
+
+
+def _cache(cache):
+    """The four tensors of a cache -> (bits, pages, heads, page, D): see qa_kv_write."""
+    kc, ks, vc, vs = cache
+    if kc.dtype not in (torch.int8, torch.int32):
+        raise TypeError("cache codes must be int8 (8 bits) or int32 (4 bits, packed), got %s" % kc.dtype)
+    _dev(kc, "k_codes", kc.dtype)
+    if kc.dim() != 4:
+        raise ValueError("k_codes must be [pages x heads x page x D (or D / 8 words)], got %s" % list(kc.shape))
+    _dev(ks, "k_scales", torch.float32)
+    _dev(vc, "v_codes", kc.dtype)
+    _dev(vs, "v_scales", torch.float32)
+    pages, heads, page, width = kc.shape
+    _shape(vc, "v_codes", kc.shape)
+    _shape(ks, "k_scales", kc.shape[:3])
+    _shape(vs, "v_scales", kc.shape[:3])
+    return (8, pages, heads, page, width) if kc.dtype == torch.int8 else (4, pages, heads, page, 8 * width)
+
+
+def _tokens(t, name, heads, D):
+    """A [tokens x heads x D] tensor whose tokens are contiguous -> its token stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    if t.dtype not in _DTYPE_CODE:
+        raise TypeError("%s must be fp32, fp16 or bf16, got %s" % (name, t.dtype))
+    if t.dim() != 3 or t.shape[1:] != (heads, D):
+        raise ValueError("%s must be [tokens x %d x %d], got %s" % (name, heads, D, list(t.shape)))
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+        raise ValueError("%s must have contiguous heads of contiguous values" % name)
+    return t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+def qa_kv_write(K, V, slots, cache, stream=None):
+    """Keys and values of new tokens into a paged cache of int8 or int4 codes, one scale per token and head.
+
+    K, V [T x heads x D] fp32 / fp16 / bf16 (tokens may be strided: columns of a projection's output); slots i64 [T]
+    the tokens' places, page index * page + place in the page (-1: not written); cache = (k_codes, k_scales, v_codes,
+    v_scales): codes int8 [pages x heads x page x D], or int32 [pages x heads x page x D / 8] for 4 bits, scales f32
+    [pages x heads x page]."""
+    bits, pages, heads, page, D = _cache(cache)
+    ldk, ldv = _tokens(K, "K", heads, D), _tokens(V, "V", heads, D)
+    if V.dtype != K.dtype:
+        raise TypeError("V must be %s, got %s" % (K.dtype, V.dtype))
+    T = K.shape[0]
+    _shape(V, "V", K.shape)
+    _dev(slots, "slots", torch.int64)
+    _shape(slots, "slots", (T,))
+    kc, ks, vc, vs = cache
+    _check("qa_kv_write",
+           lib().qa_kv_write(_a(K), ldk, _a(V), ldv, _DTYPE_CODE[K.dtype], T, _a(slots), bits, pages, heads, page, D,
+                             _a(kc), _a(ks), _a(vc), _a(vs), _s(stream)))
+
+
+def qa_kv_read(slots, cache, out_dtype=torch.float16, stream=None):
+    """The keys and values at places of a cache (see qa_kv_write) -> (K, V) [T x heads x D] of out_dtype; zeros for a
+    slot outside it."""
+    bits, pages, heads, page, D = _cache(cache)
+    _dev(slots, "slots", torch.int64)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T], got %s" % list(slots.shape))
+    if out_dtype not in _DTYPE_CODE:
+        raise TypeError("out_dtype must be fp32, fp16 or bf16, got %s" % out_dtype)
+    T = slots.numel()
+    K = _empty(stream, (T, heads, D), dtype=out_dtype, device=slots.device)
+    V = _empty(stream, (T, heads, D), dtype=out_dtype, device=slots.device)
+    kc, ks, vc, vs = cache
+    _check("qa_kv_read",
+           lib().qa_kv_read(_a(slots), T, bits, pages, heads, page, D, _a(kc), _a(ks), _a(vc), _a(vs), _a(K), _a(V),
+                            _DTYPE_CODE[out_dtype], _s(stream)))
+    return K, V
+
+
+def qa_attn_decode_workspace(B: int, H: int, heads: int, D: int, max_len: int, window: int = 0) -> int:
+    return int(lib().qa_attn_decode_workspace(B, H, heads, D, max_len, window))
+
+
+def qa_attn_decode(q, cache, table, lengths, scale=None, window=0, max_len=None, out_dtype=None, want_lse=False,
+                   out=None, workspace=None, stream=None):
+    """Attention of one new token per sequence over a paged cache (see qa_kv_write) -> out [B x H x D], or (out, lse
+    f32 [B x H]) if wanted.
+
+    q [B x H x D] fp32 / fp16 / bf16 (rows may be strided), H a multiple of the cache's heads; table i32 [B x width]
+    the pages of each sequence (rows may be strided), lengths i32 [B] its tokens; scale: 1 / sqrt(D) if not given;
+    window: the last tokens that are seen (0: all); max_len: an upper bound of the lengths (the table's places if not
+    given), by which the work is split over the card -- lengths past it count as it; out_dtype: q's if not given."""
+    bits, pages, heads, page, D = _cache(cache)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [B x H x D]")
+    B, H = q.shape[0], q.shape[1]
+    ldq = _tokens(q, "q", H, D)
+    ldt = _rows(table, "table", torch.int32)
+    _dev(lengths, "lengths", torch.int32)
+    _shape(lengths, "lengths", (B,))
+    width = table.shape[1]
+    _shape(table, "table", (B, width))
+    if max_len is None:
+        max_len = width * page
+    if out is None:
+        out = _empty(stream, (B, H, D), dtype=out_dtype or q.dtype, device=q.device)
+    _dev(out, "out")
+    _shape(out, "out", (B, H, D))
+    if out.dtype not in _DTYPE_CODE or (out_dtype is not None and out.dtype != out_dtype):
+        raise TypeError("out must be fp32, fp16 or bf16 (out_dtype), got %s" % out.dtype)
+    lse = _empty(stream, (B, H), dtype=torch.float32, device=q.device) if want_lse else None
+    need = qa_attn_decode_workspace(B, H, heads, D, int(max_len), int(window))
+    if workspace is None and need:
+        workspace = _workspace(stream, need, q.device, None)
+    kc, ks, vc, vs = cache
+    _check("qa_attn_decode",
+           lib().qa_attn_decode(_a(q), ldq, _DTYPE_CODE[q.dtype], B, H, bits, pages, heads, page, D, _a(kc), _a(ks),
+                                _a(vc), _a(vs), _a(table), ldt, width, _a(lengths), int(max_len), int(window),
+                                float(D ** -0.5 if scale is None else scale), _a(out), _DTYPE_CODE[out.dtype], _a(lse),
+                                _a(workspace), workspace.numel() if workspace is not None else 0, _s(stream)))
+    return (out, lse) if want_lse else out
+
+
+def qa_qlinear_int8_act(Xq, s_x, Wq, s_w, bias=None, act=QA_ACT_NONE, residual=None, out_dtype=torch.float16, out=None,
+                        stream=None):
+    """int8 linear on codes with bias, activation and residual: act(X W^T + bias) + residual -> out [M x N].
+
+    Xq i8 [M x K], s_x f32 [M]; Wq i8 [N x K], s_w f32 [N]; bias f32 [N]; act one of QA_ACT_*; residual [M x N] of the
+    output's type (rows may be strided); out: the given tensor (rows may be strided, it may be the residual itself) or
+    a new one of out_dtype (of the residual's type if there is one)."""
+    _dev(Xq, "Xq", torch.int8)
+    _dev(s_x, "s_x", torch.float32)
+    _dev(Wq, "Wq", torch.int8)
+    _dev(s_w, "s_w", torch.float32)
+    M, K = Xq.shape
+    N = Wq.shape[0]
+    _shape(s_x, "s_x", (M,))
+    _shape(Wq, "Wq", (N, K))
+    _shape(s_w, "s_w", (N,))
+    if bias is not None:
+        _dev(bias, "bias", torch.float32)
+        _shape(bias, "bias", (N,))
+    if out is None:
+        out = _empty(stream, (M, N), dtype=out_dtype if residual is None else residual.dtype, device=Xq.device)
+    if out.dtype not in _DTYPE_CODE:
+        raise TypeError("out must be fp32, fp16 or bf16, got %s" % out.dtype)
+    ldo = _rows(out, "out", out.dtype)
+    _shape(out, "out", (M, N))
+    ldr = N
+    if residual is not None:
+        ldr = _rows(residual, "residual", out.dtype)
+        _shape(residual, "residual", (M, N))
+    _check("qa_qlinear_int8_act",
+           lib().qa_qlinear_int8_act(_a(Xq), _a(s_x), M, K, _a(Wq), _a(s_w), N, _a(bias), int(act), _a(residual), ldr,
+                                     _a(out), ldo, _DTYPE_CODE[out.dtype], _s(stream)))
     return out
 
 

@@ -19,7 +19,8 @@ LIB = os.path.join(PKG, "libqa.so")
 
 ARCH = "gfx950"
 SOURCES = ["qa_api.cpp", "qa_noalloc.hip", "k_quant.hip", "k_smooth.hip", "k_kron.hip", "k_gemm.hip",
-           "k_decode.hip", "k_probe.hip", "k_norm.hip", "k_route.hip", "k_experts.hip", "k_lora.hip"]
+           "k_decode.hip", "k_probe.hip", "k_norm.hip", "k_route.hip", "k_experts.hip", "k_lora.hip",
+           "k_kv.hip", "k_attn.hip", "k_linear.hip"]
 
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

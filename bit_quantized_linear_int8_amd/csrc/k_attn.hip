@@ -1,0 +1,578 @@
+// k_attn.hip -- attention of one new token per sequence over a paged cache of
+// int8 or int4 keys and values, on gfx950.
+//
+//   x_t = scale s_k[t] sum_d q_d k[t][d],   p_t = exp(x_t - m)
+//   o_d = sum_t p_t s_v[t] v[t][d] / sum_t p_t,   lse = m + log sum_t p_t
+//
+// over the tokens t of a sequence (inside its window, on a page that the cache
+// has).  The heads that share a key head are the 16 columns of one MFMA tile.
+//
+// A wave takes 32 tokens at a time, from memory straight into MFMA operands:
+//   - keys are the rows of A: lane (m, c) holds 16-byte pieces c, c + 4, ... of
+//     token m (and 16 + m); the order of d that this makes is the queries' too;
+//   - x comes out with four consecutive tokens of column g = lane % 16 in each
+//     lane, which is where p has to be as the operand B of the second product;
+//   - values are A of the second product, transposed: lane (m, c) holds the
+//     16th part m of the D values of tokens 4 c + j and 16 + 4 c + j, and
+//     the bytes of two tokens are put side by side in registers.
+// So nothing passes through LDS, and lanes exchange nothing inside the loop.
+//
+// Codes become fp16 exactly: the byte (or nibble) with its sign bit flipped under
+// the exponent of 1024, less 1024 and the flip.  Queries enter as fp16 times a
+// power of two per head (exact for fp16 and bf16; fp32 as two numbers, 2^-22 of
+// the head's largest).  p s_v enters as two fp16 numbers with a power of two per
+// head, 2^-22 of the value, so that neither the scales' range nor a softmax over
+// long contexts costs digits: one fp16 number would add an error as large as the
+// rounding of an fp16 output.  Sums are fp32.
+//
+// The reference m of the exponentials and the power of two of p s_v follow their
+// running maxima lazily: only when a tile passes one by 2^16 (or 2^14) are
+// they taken anew, with the lanes' exchange that this needs; 2^16 leaves the sums
+// far inside fp32's range.
+//
+// The four waves of a block take tiles in turn and are joined through LDS; a
+// sequence is split over blocks in equal chunks, joined by k_attn_join.
+#include "qa_device.hpp"
+#include "qa_launch.hpp"
+
+namespace qa {
+
+namespace {
+
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+
+struct AttnArgs {
+    const void* q;             // [B][H][D], token stride ldq
+    int64_t ldq;
+    const uint8_t* kc;
+    const float* ks;
+    const uint8_t* vc;
+    const float* vs;
+    const int32_t* table;      // [B][width], row stride ldt: pages of a sequence
+    int64_t ldt;
+    const int32_t* lengths;    // [B]
+    int32_t H, heads, group, gtiles, D, shift, pages, qdt;
+    int32_t max_len;           // lengths past it (or past the table) count as it
+    int32_t window;            // 0: none
+    int32_t chunk, splits;
+    float scale2;              // scale log2(e)
+    void* out;                 // [B][H][D]
+    int32_t dt;
+    float* lse;                // [B][H] or nullptr
+    float* part;               // [B][H][splits][D] (splits > 1)
+    float* plse;               // [B][H][splits], base 2
+};
+
+constexpr float kLow = -3.0e38f;           // the reference before any token
+constexpr float kLn2 = 0.693147180559945309f;
+
+__device__ __forceinline__ v2h pk(uint32_t u) { return __builtin_bit_cast(v2h, u); }
+__device__ __forceinline__ uint32_t up(v2h h) { return __builtin_bit_cast(uint32_t, h); }
+
+// Pairs of bytes u (in the low bytes of each half, biased by 128) less the bias.
+__device__ __forceinline__ uint32_t byte_pair(uint32_t u) {
+    return up(pk(u | 0x64006400u) - v2h{(_Float16)1152, (_Float16)1152});
+}
+// Pairs of nibbles (biased by 8) in bits 0..3 or 4..7 of each half of y.
+__device__ __forceinline__ uint32_t nib_pair0(uint32_t y) {
+    return up(pk((y & 0x000f000fu) | 0x64006400u) - v2h{(_Float16)1032, (_Float16)1032});
+}
+__device__ __forceinline__ uint32_t nib_pair1(uint32_t y) {
+    return up(__builtin_elementwise_fma(pk((y & 0x00f000f0u) | 0x64006400u), v2h{(_Float16)0.0625, (_Float16)0.0625},
+                                        v2h{(_Float16)-72, (_Float16)-72}));
+}
+
+// Eight codes of one row as fp16: bytes of two words in order, or nibbles of one
+// word in the order 0 4 1 5 2 6 3 7.
+template <int BITS>
+__device__ __forceinline__ v8h row8(uint32_t a, uint32_t b) {
+    u32x4 o;
+    if constexpr (BITS == 8) {
+        a ^= 0x80808080u;
+        b ^= 0x80808080u;
+        o[0] = byte_pair(__builtin_amdgcn_perm(0u, a, 0x0c010c00u));
+        o[1] = byte_pair(__builtin_amdgcn_perm(0u, a, 0x0c030c02u));
+        o[2] = byte_pair(__builtin_amdgcn_perm(0u, b, 0x0c010c00u));
+        o[3] = byte_pair(__builtin_amdgcn_perm(0u, b, 0x0c030c02u));
+    } else {
+        a ^= 0x88888888u;
+        o[0] = nib_pair0(a);
+        o[1] = nib_pair1(a);
+        o[2] = nib_pair0(a >> 8);
+        o[3] = nib_pair1(a >> 8);
+    }
+    return __builtin_bit_cast(v8h, o);
+}
+template <int BITS>
+__device__ __forceinline__ constexpr int row8_order(int j) {
+    return BITS == 8 ? j : (j >> 1) + 4 * (j & 1);
+}
+
+__device__ __forceinline__ float wide(const void* p, int64_t at, int dt) {
+    if (dt == 0) return static_cast<const float*>(p)[at];
+    const uint16_t u = static_cast<const uint16_t*>(p)[at];
+    return dt == 1 ? h2f(u) : __builtin_bit_cast(float, (uint32_t)u << 16);
+}
+
+// N consecutive outputs of type dt at p[at] (8-byte aligned at least).
+template <int N>
+__device__ __forceinline__ void store_row(void* p, int64_t at, int dt, const float* v) {
+    if (dt == 0) {
+        float* o = static_cast<float*>(p) + at;
+#pragma unroll
+        for (int j = 0; j < N; j += 4) *reinterpret_cast<v4f*>(o + j) = v4f{v[j], v[j + 1], v[j + 2], v[j + 3]};
+        return;
+    }
+    uint16_t* o = static_cast<uint16_t*>(p) + at;
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+        uint16_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = dt == 1 ? f2h(v[j + e]) : f2bf(v[j + e]);
+        *reinterpret_cast<u32x2*>(o + j) = u32x2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
+    }
+}
+
+// First and last tokens that a sequence's query sees, and the place that its
+// chunks are counted from.
+__device__ __forceinline__ void span_of(const AttnArgs& a, int b, int& first, int& end, int& from) {
+    int n = a.lengths[b];
+    end = n < 0 ? 0 : (n > a.max_len ? a.max_len : n);
+    first = a.window > 0 && end > a.window ? end - a.window : 0;
+    from = first & ~31;
+}
+
+__device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
+
+}  // namespace
+
+// DP: D rounded up to 64, 128 or 256 (what lies behind D meets queries of 0, or is
+// not stored).  QT: fp16 numbers that a query value is made of.
+template <int BITS, int DP, int QT>
+__global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
+    constexpr int CC = BITS == 8 || DP == 64 ? 16 : 32;      // codes of a lane's piece of a key
+    constexpr int NS = DP / (4 * CC);                        // pieces of a lane
+    constexpr int PB = CC * BITS / 8;                        // bytes of a piece
+    constexpr int FP = CC / 8, NF = NS * FP;                 // MFMA steps of a piece, of a key
+    constexpr int VN = DP / 16;                              // values of a lane per token
+    constexpr int VB = VN * BITS / 8;                        // their bytes
+    constexpr int VW = VB < 4 ? 1 : VB / 4;                  // their words
+    __shared__ v4f red[2][16][DP / 4];
+    __shared__ float st_m[4][16], st_l[4][16], st_e[4][16];
+
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int m16 = lane & 15, c4 = lane >> 4;
+    uint32_t id = blockIdx.x;
+    const int gt = id % (uint32_t)a.gtiles;
+    id /= (uint32_t)a.gtiles;
+    const int h = id % (uint32_t)a.heads;
+    id /= (uint32_t)a.heads;
+    const int split = id % (uint32_t)a.splits;
+    const int b = id / (uint32_t)a.splits;
+    int first, end, from;
+    span_of(a, b, first, end, from);
+    const int64_t lo64 = (int64_t)from + (int64_t)split * a.chunk;
+    const int g = gt * 16 + m16;                             // the lane's head within the group
+    const bool head = g < a.group;
+    const int64_t row = (int64_t)b * a.H + h * a.group + g;  // its row of the output
+    if (lo64 >= end) {                                       // nothing in this chunk
+        if (a.splits > 1) {
+            if (wave == 0 && c4 == 0 && head) a.plse[row * a.splits + split] = -__builtin_inff();
+        } else if (wave == 0 && head) {
+            const float z[VN] = {};
+            for (int e = 0; e < 4; ++e) {
+                const int d = VN * (4 * c4 + e);
+                if (d < a.D) store_row<VN>(a.out, row * a.D + d, a.dt, z);
+            }
+            if (c4 == 0 && a.lse) a.lse[row] = -__builtin_inff();
+        }
+        return;
+    }
+    const int lo = (int)lo64;
+    const int hi = end - lo < a.chunk ? end : lo + a.chunk;
+    const int ntiles = (hi - lo + 31) >> 5;
+
+    const int32_t* tab = a.table + (int64_t)b * a.ldt;
+    const int page = 1 << a.shift;
+    const uint32_t RB = (uint32_t)a.D * BITS / 8;            // bytes of a row
+    // the page of the 16 tokens from t: its index, or -1 (past the end, or not one of the cache's)
+    auto page_of = [&](int t) __attribute__((always_inline)) {
+        const int p = __builtin_amdgcn_readfirstlane(tab[(t < hi ? t : hi - 1) >> a.shift]);
+        return t < hi && (uint32_t)p < (uint32_t)a.pages ? p : -1;
+    };
+    struct Stage {
+        u32x4 k[2][NS];
+        uint32_t v[8][VW];
+        v4f ks[2], vs[2];
+    };
+    auto load = [&](Stage& s, int t0, int p0, int p1) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int p = u ? p1 : p0;
+            const int64_t base = ((int64_t)(p < 0 ? 0 : p) * a.heads + h) << a.shift;    // row of the page's first token
+            const uint32_t t = (uint32_t)(t0 + 16 * u) & (uint32_t)(page - 1);
+            const rsrc_t rk = make_rsrc(a.kc + base * RB, p < 0 ? 0 : (int64_t)page * RB);
+            const rsrc_t rv = make_rsrc(a.vc + base * RB, p < 0 ? 0 : (int64_t)page * RB);
+            const rsrc_t rks = make_rsrc(a.ks + base, p < 0 ? 0 : (int64_t)page * 4);
+            const rsrc_t rvs = make_rsrc(a.vs + base, p < 0 ? 0 : (int64_t)page * 4);
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const uint32_t off = (t + m16) * RB + (c4 + 4 * i) * PB;
+                if constexpr (PB == 16) s.k[u][i] = bload16(rk, off);
+                else {
+                    const u32x2 w = bload8(rk, off);
+                    s.k[u][i] = u32x4{w[0], w[1], 0u, 0u};
+                }
+            }
+            s.ks[u] = __builtin_bit_cast(v4f, bload16(rks, (t + 4 * c4) * 4));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t off = (t + 4 * c4 + j) * RB + m16 * VB;
+                uint32_t* o = s.v[4 * u + j];
+                if constexpr (VB == 2) o[0] = bload2(rv, off);
+                else if constexpr (VB == 4) o[0] = bload4(rv, off);
+                else if constexpr (VB == 8) {
+                    const u32x2 w = bload8(rv, off);
+                    o[0] = w[0], o[1] = w[1];
+                } else {
+                    const u32x4 w = bload16(rv, off);
+                    o[0] = w[0], o[1] = w[1], o[2] = w[2], o[3] = w[3];
+                }
+            }
+            s.vs[u] = __builtin_bit_cast(v4f, bload16(rvs, (t + 4 * c4) * 4));
+        }
+    };
+
+    // this wave's first tile, and the queries while it comes
+    int tile = wave;
+    int t0 = lo + 32 * tile, p0 = page_of(t0), p1 = page_of(t0 + 16);
+    int np0 = page_of(t0 + 128), np1 = page_of(t0 + 144);    // of its next one
+    Stage cur;
+    load(cur, t0, p0, p1);
+    v8h qf[QT][NF];
+    float qscale;
+    {
+        float x[NF][8], top = 0.0f;
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int d = (c4 + 4 * (f / FP)) * CC + 8 * (f % FP) + row8_order<BITS>(j);
+                x[f][j] = head && d < a.D ? wide(a.q, (int64_t)b * a.ldq + (int64_t)(h * a.group + g) * a.D + d, a.qdt) : 0.0f;
+                top = fmaxf(top, __builtin_fabsf(x[f][j]));
+            }
+        top = fmaxf(top, __shfl_xor(top, 16, QA_WAVE));
+        top = fmaxf(top, __shfl_xor(top, 32, QA_WAVE));
+        // times 2^up the head's largest is in [2^13, 2^14)
+        const int e = top > 0.0f && top < __builtin_inff() ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
+        qscale = __builtin_ldexpf(a.scale2, -e);
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float y = __builtin_ldexpf(x[f][j], e);
+                qf[0][f][j] = (_Float16)y;
+                if constexpr (QT == 2) qf[1][f][j] = (_Float16)(y - (float)qf[0][f][j]);
+            }
+    }
+
+    v4f acc[VN];
+#pragma unroll
+    for (int i = 0; i < VN; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    float m = kLow, l = 0.0f, ex = -120.0f, r = 0.0f;        // r = 2^-ex, the factor of p s_v
+
+    while (tile < ntiles) {
+        const int nt = tile + 4;
+        const int n0 = lo + 32 * nt;
+        Stage nxt;
+        load(nxt, n0, np0, np1);
+        const int nnp0 = page_of(n0 + 128), nnp1 = page_of(n0 + 144);
+
+        v4f x[2], sv[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            v4f s = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                const u32x4 w = cur.k[u][f / FP];
+                const v8h kf = BITS == 8 ? row8<BITS>(w[2 * (f % FP)], w[2 * (f % FP) + 1]) : row8<BITS>(w[f % FP], 0u);
+                s = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[0][f], s, 0, 0, 0);
+                if constexpr (QT == 2) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[QT - 1][f], s, 0, 0, 0);
+            }
+            sv[u] = cur.vs[u];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[u][e] = s[e] * cur.ks[u][e] * qscale;
+        }
+        if (t0 < first || t0 + 32 > hi || p0 < 0 || p1 < 0) {    // tokens that are not seen
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = t0 + 16 * u + 4 * c4 + e;
+                    const bool live = t >= first && t < hi && (u ? p1 : p0) >= 0;
+                    x[u][e] = live ? x[u][e] : -__builtin_inff();
+                    sv[u][e] = live ? sv[u][e] : 0.0f;
+                }
+        }
+        v4f p[2], w[2];
+        auto weigh = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[u][e] = __builtin_amdgcn_exp2f(x[u][e] - m);
+                    w[u][e] = p[u][e] * sv[u][e] * r;
+                }
+        };
+        weigh();
+        const float xm = fmaxf(max4(x[0]), max4(x[1]));
+        if (__any(xm > m + 16.0f || fmaxf(max4(w[0]), max4(w[1])) > 16384.0f)) {
+            // new references from this tile's maxima and the old ones
+            float tm = fmaxf(xm, __shfl_xor(xm, 16, QA_WAVE));
+            tm = fmaxf(tm, __shfl_xor(tm, 32, QA_WAVE));
+            const float mn = fmaxf(m, tm);
+            float wm = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) wm = fmaxf(wm, __builtin_amdgcn_exp2f(x[u][e] - mn) * sv[u][e]);
+            wm = fmaxf(wm, __shfl_xor(wm, 16, QA_WAVE));
+            wm = fmaxf(wm, __shfl_xor(wm, 32, QA_WAVE));
+            const float down = m - mn;
+            const float en = fmaxf(-120.0f, fmaxf(__builtin_ceilf(ex + down), (float)__builtin_amdgcn_frexp_expf(wm)));
+            l *= __builtin_amdgcn_exp2f(down);
+            const float f = __builtin_ldexpf(__builtin_amdgcn_exp2f(down), (int)fmaxf(ex - en, -300.0f));
+#pragma unroll
+            for (int i = 0; i < VN; ++i) acc[i] *= f;
+            m = mn;
+            ex = en;
+            r = __builtin_amdgcn_exp2f(-en);
+            weigh();
+        }
+        v8h ph, pl;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                l += p[u][e];
+                ph[4 * u + e] = (_Float16)w[u][e];
+                pl[4 * u + e] = (_Float16)(w[u][e] - (float)ph[4 * u + e]);
+            }
+        auto pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) __attribute__((always_inline)) {
+            const v8h vf = __builtin_bit_cast(v8h, u32x4{a0, a1, a2, a3});
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, ph, acc[i], 0, 0, 0);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl, acc[i], 0, 0, 0);
+        };
+        if constexpr (BITS == 8) {
+#pragma unroll
+            for (int q = 0; q < VW; ++q) {
+                uint32_t y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = cur.v[j][q] ^ 0x80808080u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t sel = 0x0c000c00u | (uint32_t)i | ((uint32_t)(4 + i) << 16);
+                    pv(4 * q + i, byte_pair(__builtin_amdgcn_perm(y[1], y[0], sel)),
+                       byte_pair(__builtin_amdgcn_perm(y[3], y[2], sel)), byte_pair(__builtin_amdgcn_perm(y[5], y[4], sel)),
+                       byte_pair(__builtin_amdgcn_perm(y[7], y[6], sel)));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < VN / 4; ++q) {               // halves of words: four nibbles of two tokens
+                const uint32_t sel = q & 1 ? 0x07060302u : 0x05040100u;
+                uint32_t y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    y[j] = __builtin_amdgcn_perm(cur.v[2 * j + 1][q / 2], cur.v[2 * j][q / 2], sel) ^ 0x88888888u;
+                pv(4 * q, nib_pair0(y[0]), nib_pair0(y[1]), nib_pair0(y[2]), nib_pair0(y[3]));
+                pv(4 * q + 1, nib_pair1(y[0]), nib_pair1(y[1]), nib_pair1(y[2]), nib_pair1(y[3]));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] >>= 8;
+                pv(4 * q + 2, nib_pair0(y[0]), nib_pair0(y[1]), nib_pair0(y[2]), nib_pair0(y[3]));
+                pv(4 * q + 3, nib_pair1(y[0]), nib_pair1(y[1]), nib_pair1(y[2]), nib_pair1(y[3]));
+            }
+        }
+        tile = nt;
+        t0 = n0;
+        p0 = np0;
+        p1 = np1;
+        np0 = nnp0;
+        np1 = nnp1;
+        cur = nxt;
+    }
+
+    // the block's waves: common references, then the sums of the accumulators
+    l += __shfl_xor(l, 16, QA_WAVE);
+    l += __shfl_xor(l, 32, QA_WAVE);
+    if (c4 == 0) {
+        st_m[wave][m16] = m;
+        st_l[wave][m16] = l;
+        st_e[wave][m16] = ex;
+    }
+    __syncthreads();
+    float mg = kLow, lg = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mg = fmaxf(mg, st_m[w][m16]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) lg += st_l[w][m16] * __builtin_amdgcn_exp2f(st_m[w][m16] - mg);
+    const float f = __builtin_ldexpf(__builtin_amdgcn_exp2f(m - mg), (int)ex);
+    float o[4][VN];                                          // head m16, values VN (4 c4 + e) + i
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int i = 0; i < VN; ++i) o[e][i] = acc[i][e] * f;
+    auto give = [&](int to) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < VN / 4; ++i)
+                red[to][m16][VN / 4 * (4 * c4 + e) + i] = v4f{o[e][4 * i], o[e][4 * i + 1], o[e][4 * i + 2], o[e][4 * i + 3]};
+    };
+    auto take = [&](int at) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < VN / 4; ++i) {
+                const v4f v = red[at][m16][VN / 4 * (4 * c4 + e) + i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[e][4 * i + j] += v[j];
+            }
+    };
+    if (wave >= 2) give(wave - 2);
+    __syncthreads();
+    if (wave < 2) take(wave);
+    __syncthreads();
+    if (wave == 1) give(0);
+    __syncthreads();
+    if (wave != 0 || !head) return;
+    take(0);
+    const float inv = lg == 0.0f ? 0.0f : 1.0f / lg;
+    const float lse = lg == 0.0f ? -__builtin_inff() : mg + __builtin_log2f(lg);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int d = VN * (4 * c4 + e);
+        if (d >= a.D) continue;
+#pragma unroll
+        for (int i = 0; i < VN; ++i) o[e][i] *= inv;
+        if (a.splits > 1) store_row<VN>(a.part, (row * a.splits + split) * a.D + d, 0, o[e]);
+        else store_row<VN>(a.out, row * a.D + d, a.dt, o[e]);
+    }
+    if (c4 == 0) {
+        if (a.splits > 1) a.plse[row * a.splits + split] = lse;
+        else if (a.lse) a.lse[row] = lse * kLn2;
+    }
+}
+
+// The parts of one row (sequence and head): weights 2^(lse_i - max), four values to
+// a lane, the parts over groups of D / 4 lanes.
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+    __shared__ float wt[1024];
+    __shared__ v4f sum[256];
+    __shared__ float red[8];
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+    const int64_t row = blockIdx.x;
+    const int b = (int)(row / a.H);
+    int first, end, from;
+    span_of(a, b, first, end, from);
+    int n = (int)(((int64_t)end - from + a.chunk - 1) / a.chunk);
+    n = end <= first ? 0 : (n < a.splits ? n : a.splits);
+    float top = -__builtin_inff();
+    for (int i = tid; i < n; i += 256) top = fmaxf(top, a.plse[row * a.splits + i]);
+    top = wave_max(top);
+    if (lane == 0) red[wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    float total = 0.0f;
+    for (int i = tid; i < n; i += 256) {
+        const float v = a.plse[row * a.splits + i];
+        // a part without a token weighs nothing, and a NaN stays one
+        const float w = v == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(v - top);
+        wt[i] = w;
+        total += w;
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o, QA_WAVE);
+    if (lane == 0) red[4 + wave] = total;
+    __syncthreads();
+    total = red[4] + red[5] + red[6] + red[7];
+    const int L = a.D / 4, groups = 256 / L, grp = tid / L, j = tid - grp * L;
+    v4f s = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (grp < groups)
+        for (int i = grp; i < n; i += groups) {
+            const float w = wt[i];
+            if (w != 0.0f) s += w * *reinterpret_cast<const v4f*>(a.part + (row * a.splits + i) * a.D + 4 * j);
+        }
+    sum[tid] = s;
+    __syncthreads();
+    if (tid >= L) return;
+    for (int i = 1; i < groups; ++i) s += sum[i * L + tid];
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    const float o[4] = {s[0] * inv, s[1] * inv, s[2] * inv, s[3] * inv};
+    store_row<4>(a.out, row * a.D + 4 * tid, a.dt, o);
+    if (tid == 0 && a.lse) a.lse[row] = total == 0.0f ? -__builtin_inff() : (top + __builtin_log2f(total)) * kLn2;
+}
+
+namespace {
+
+struct Plan {
+    int32_t chunk, splits;
+};
+
+// Chunks of a sequence: about 1024 blocks of four waves (four on each CU), at
+// least one tile of 32 tokens for every wave of a block.
+Plan plan_of(int64_t B, int32_t H, int32_t heads, int64_t max_len, int32_t window) {
+    const int64_t group = H / heads, pairs = B * heads * ((group + 15) / 16);
+    int64_t span = window > 0 && (int64_t)window + 31 < max_len ? (int64_t)window + 31 : max_len;
+    if (span < 1) span = 1;
+    const int64_t want = pairs >= 1024 ? 1 : 1024 / pairs;
+    const int64_t chunk = ((span + want - 1) / want + 127) / 128 * 128;
+    return Plan{(int32_t)chunk, (int32_t)((span + chunk - 1) / chunk)};
+}
+
+template <int BITS, int DP>
+hipError_t run_attn(const AttnArgs& a, int64_t blocks, hipStream_t st) {
+    if (a.qdt == 0) hipLaunchKernelGGL((k_attn_decode<BITS, DP, 2>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_attn_decode<BITS, DP, 1>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+template <int BITS>
+hipError_t run_attn(const AttnArgs& a, int64_t blocks, hipStream_t st) {
+    if (a.D <= 64) return run_attn<BITS, 64>(a, blocks, st);
+    return a.D <= 128 ? run_attn<BITS, 128>(a, blocks, st) : run_attn<BITS, 256>(a, blocks, st);
+}
+
+}  // namespace
+
+size_t attn_scratch_bytes(int64_t B, int32_t H, int32_t heads, int32_t D, int64_t max_len, int32_t window) {
+    const Plan p = plan_of(B, H, heads, max_len, window);
+    return p.splits > 1 ? (size_t)B * H * p.splits * (D + 1) * 4 : 0;
+}
+
+hipError_t launch_attn_decode(const void* q, int64_t ldq, int q_dtype, int64_t B, int32_t H, const KvCache& c,
+                              const int32_t* table, int64_t ldt, int64_t width, const int32_t* lengths, int64_t max_len,
+                              int32_t window, float scale, void* out, int out_dtype, float* lse, void* scratch,
+                              hipStream_t st) {
+    AttnArgs a{};
+    a.q = q; a.ldq = ldq; a.qdt = q_dtype;
+    a.kc = static_cast<const uint8_t*>(c.k_codes); a.ks = c.k_scales;
+    a.vc = static_cast<const uint8_t*>(c.v_codes); a.vs = c.v_scales;
+    a.table = table; a.ldt = ldt; a.lengths = lengths;
+    a.H = H; a.heads = c.heads; a.group = H / c.heads; a.gtiles = (a.group + 15) / 16;
+    a.D = c.D; a.shift = c.shift; a.pages = (int32_t)c.pages;
+    const int64_t most = width << c.shift;
+    const Plan p = plan_of(B, H, c.heads, max_len, window);
+    a.max_len = (int32_t)(max_len < most ? max_len : most);
+    a.window = window; a.chunk = p.chunk; a.splits = p.splits;
+    a.scale2 = scale * 1.44269504088896340736f;
+    a.out = out; a.dt = out_dtype; a.lse = lse;
+    a.part = static_cast<float*>(scratch);
+    a.plse = a.part + (p.splits > 1 ? (size_t)B * H * p.splits * c.D : 0);
+    const int64_t blocks = B * c.heads * a.gtiles * p.splits;
+    hipError_t e = c.bits == 8 ? run_attn<8>(a, blocks, st) : run_attn<4>(a, blocks, st);
+    if (e != hipSuccess || p.splits == 1) return e;
+    hipLaunchKernelGGL(k_attn_join, dim3((unsigned)(B * H)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+}  // namespace qa

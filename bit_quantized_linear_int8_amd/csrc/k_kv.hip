@@ -1,0 +1,205 @@
+// k_kv.hip -- a paged cache of keys and values in int8 or int4 codes: written
+// from new tokens and read back, on gfx950.
+//
+//   s = max_d |x_d| / q_max (1 where that is 0),  q = rint(x / s)      (write)
+//   x = fl32(q s), rounded to the type                                  (read)
+//
+// per token and head, q_max 127 or 7.  A page holds `page` tokens of every head,
+// head by head: codes [pages][heads][page][D], scales [pages][heads][page]; four-bit
+// codes are packed eight to a word like every int4 row of this library.
+//
+// A row of D values is eight values to a lane and 8, 16 or 32 lanes; the maximum
+// over them is the only exchange (DPP).  The lanes of a token do its key and its
+// value, so a place is looked up once and two rows are in flight.  Consecutive
+// rows of a block are consecutive tokens of one head: prompts then write whole
+// pieces of a page, codes and scales.
+#include "qa_device.hpp"
+#include "qa_launch.hpp"
+
+namespace qa {
+
+namespace {
+
+struct KvArgs {
+    const void* x[2];          // write: keys and values, rows of heads x D
+    int64_t ld[2];             // their token strides in elements
+    void* y[2];                // read: outputs [T][heads][D]
+    uint8_t* codes[2];
+    float* scales[2];
+    const int64_t* slots;      // [T] page * page_size + place in the page
+    int64_t T, places;         // places: pages * page_size
+    int32_t heads, D, shift;   // shift: log2 of the page's tokens
+};
+
+__device__ __forceinline__ float bf2f(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
+
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, int64_t at, float* x) {
+    if constexpr (DT == 0) {
+        const v4f* q = reinterpret_cast<const v4f*>(static_cast<const float*>(p) + at);
+        const v4f a = q[0], b = q[1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
+    } else {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint16_t u = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+            x[j] = DT == 1 ? h2f(u) : bf2f(u);
+        }
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void* p, int64_t at, const float* x) {
+    if constexpr (DT == 0) {
+        v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(p) + at);
+        o[0] = v4f{x[0], x[1], x[2], x[3]};
+        o[1] = v4f{x[4], x[5], x[6], x[7]};
+    } else {
+        u32x4 w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = DT == 1 ? f2h(x[2 * j]) : f2bf(x[2 * j]);
+            const uint32_t hi = DT == 1 ? f2h(x[2 * j + 1]) : f2bf(x[2 * j + 1]);
+            w[j] = lo | (hi << 16);
+        }
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + at) = w;
+    }
+}
+
+// Row of a place in codes and scales.
+__device__ __forceinline__ int64_t row_of(const KvArgs& a, int64_t slot, int h) {
+    return (((slot >> a.shift) * a.heads + h) << a.shift) + (slot & ((1 << a.shift) - 1));
+}
+
+// LPR lanes to a row, 256 / LPR tokens of head blockIdx.y to a block.
+template <int DT, int BITS, int LPR>
+__global__ __launch_bounds__(256) void k_kv_write(KvArgs a) {
+    const int j = threadIdx.x % LPR;
+    const int64_t t = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const int h = blockIdx.y;
+    const int64_t slot = t < a.T ? a.slots[t] : -1;
+    const bool row = slot >= 0 && slot < a.places;           // the same for a row's lanes
+    const bool live = row && j * 8 < a.D;
+    float x[2][8];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[w][e] = 0.0f;
+        if (live) load8<DT>(a.x[w], t * a.ld[w] + (int64_t)h * a.D + j * 8, x[w]);
+    }
+    const int64_t at = row ? row_of(a, slot, h) : 0;
+    constexpr float QM = BITS == 8 ? 127.0f : 7.0f;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        // magnitudes as bit patterns: they order like the values, infinities and NaNs above all
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, __builtin_bit_cast(uint32_t, x[w][e]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = LPR / 2; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, QA_WAVE));
+        const bool fine = m < 0x7f800000u;
+        float s = __builtin_bit_cast(float, m) / QM;
+        if (s == 0.0f) s = 1.0f;
+        if (!fine) s = __builtin_nanf("");
+        u32x2 c = u32x2{0u, 0u};
+        if (fine) {
+            if (s >= 0x1p-120f) {
+                c = codes8_dyn(x[w], s, 1.0f / s);
+            } else {                                         // the reciprocal overflows or loses digits
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    c[e >> 2] |= ((uint32_t)(int)__builtin_rintf(x[w][e] / s) & 0xffu) << (8 * (e & 3));
+            }
+        }
+        if (live) {
+            if constexpr (BITS == 8) *reinterpret_cast<u32x2*>(a.codes[w] + at * a.D + j * 8) = c;
+            else *reinterpret_cast<uint32_t*>(a.codes[w] + at * (a.D / 2) + j * 4) = pack_nibbles(c);
+        }
+        if (row && j == 0) a.scales[w][at] = s;
+    }
+}
+
+template <int DT, int BITS, int LPR>
+__global__ __launch_bounds__(256) void k_kv_read(KvArgs a) {
+    const int j = threadIdx.x % LPR;
+    const int64_t t = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const int h = blockIdx.y;
+    if (t >= a.T || j * 8 >= a.D) return;
+    const int64_t slot = a.slots[t];
+    const bool row = slot >= 0 && slot < a.places;
+    const int64_t at = row ? row_of(a, slot, h) : 0;
+    u32x2 c[2] = {u32x2{0u, 0u}, u32x2{0u, 0u}};
+    float s[2] = {0.0f, 0.0f};
+    if (row) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            if constexpr (BITS == 8) c[w] = *reinterpret_cast<const u32x2*>(a.codes[w] + at * a.D + j * 8);
+            else c[w][0] = *reinterpret_cast<const uint32_t*>(a.codes[w] + at * (a.D / 2) + j * 4);
+            s[w] = a.scales[w][at];
+        }
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int q = BITS == 8 ? (int)(int8_t)(c[w][e >> 2] >> (8 * (e & 3))) : (int)(c[w][0] << (28 - 4 * e)) >> 28;
+            x[e] = (float)q * s[w];
+            asm("" : "+v"(x[e]));                            // (or product and rounding fuse for fp16, and for it alone)
+        }
+        store8<DT>(a.y[w], (t * a.heads + h) * a.D + j * 8, x);
+    }
+}
+
+template <bool WRITE, int DT, int BITS>
+hipError_t run_kv(const KvArgs& a, hipStream_t st) {
+    const int lpr = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32;
+    const dim3 g((unsigned)((a.T + 256 / lpr - 1) / (256 / lpr)), (unsigned)a.heads);
+#define QA_KV(L)                                                                             \
+    if constexpr (WRITE) hipLaunchKernelGGL((k_kv_write<DT, BITS, L>), g, dim3(256), 0, st, a); \
+    else hipLaunchKernelGGL((k_kv_read<DT, BITS, L>), g, dim3(256), 0, st, a);
+    if (lpr == 8) { QA_KV(8) }
+    else if (lpr == 16) { QA_KV(16) }
+    else { QA_KV(32) }
+#undef QA_KV
+    return hipGetLastError();
+}
+
+template <bool WRITE>
+hipError_t run_kv(const KvArgs& a, int dtype, int bits, hipStream_t st) {
+    if (bits == 8) {
+        if (dtype == 0) return run_kv<WRITE, 0, 8>(a, st);
+        return dtype == 1 ? run_kv<WRITE, 1, 8>(a, st) : run_kv<WRITE, 2, 8>(a, st);
+    }
+    if (dtype == 0) return run_kv<WRITE, 0, 4>(a, st);
+    return dtype == 1 ? run_kv<WRITE, 1, 4>(a, st) : run_kv<WRITE, 2, 4>(a, st);
+}
+
+KvArgs kv_args(const int64_t* slots, int64_t T, const KvCache& c) {
+    KvArgs a{};
+    a.slots = slots; a.T = T;
+    a.codes[0] = static_cast<uint8_t*>(c.k_codes); a.codes[1] = static_cast<uint8_t*>(c.v_codes);
+    a.scales[0] = c.k_scales; a.scales[1] = c.v_scales;
+    a.places = c.pages << c.shift; a.heads = c.heads; a.D = c.D; a.shift = c.shift;
+    return a;
+}
+
+}  // namespace
+
+hipError_t launch_kv_write(const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype, int64_t T,
+                           const int64_t* slots, const KvCache& c, hipStream_t st) {
+    KvArgs a = kv_args(slots, T, c);
+    a.x[0] = k; a.x[1] = v; a.ld[0] = ldk; a.ld[1] = ldv;
+    return run_kv<true>(a, dtype, c.bits, st);
+}
+
+hipError_t launch_kv_read(const int64_t* slots, int64_t T, const KvCache& c, void* k, void* v, int dtype,
+                          hipStream_t st) {
+    KvArgs a = kv_args(slots, T, c);
+    a.y[0] = k; a.y[1] = v;
+    return run_kv<false>(a, dtype, c.bits, st);
+}
+
+}  // namespace qa

@@ -964,6 +964,136 @@ qa_status qa_qlinear_int8_lora(const int8_t* Xq, const float* s_x, const void* X
                          "qa_qlinear_int8_lora");
 }
 
+// ----------------------------------------------------------------- quantized cache
+namespace {
+
+constexpr int64_t kMaxHeads = 65535;        // a grid's second dimension
+constexpr int64_t kMaxPlaces = (int64_t)1 << 30;    // a sequence's tokens count in 32 bits
+
+bool cache_shape_ok(int64_t pages, int32_t heads, int32_t page, int32_t D) {
+    return pages >= 0 && pages <= kMaxI32 && heads >= 1 && heads <= kMaxHeads && page >= 16 && page <= 1024 &&
+           (page & (page - 1)) == 0 && D >= 16 && D <= 256 && D % 16 == 0;
+}
+bool cache_aligned(const void* kc, const float* ks, const void* vc, const float* vs) {
+    return aligned(kc, 16) && aligned(ks, 16) && aligned(vc, 16) && aligned(vs, 16);
+}
+qa::KvCache cache_of(const void* kc, const float* ks, const void* vc, const float* vs, int64_t pages, int32_t heads,
+                     int32_t page, int32_t D, int32_t bits) {
+    int32_t shift = 4;
+    while ((1 << shift) < page) ++shift;
+    return qa::KvCache{const_cast<void*>(kc), const_cast<float*>(ks), const_cast<void*>(vc), const_cast<float*>(vs),
+                       pages, heads, D, shift, bits};
+}
+int64_t bytes_of(qa_dtype d) { return d == QA_F32 ? 4 : 2; }
+
+}  // namespace
+
+qa_status qa_kv_write(const void* K, int64_t ldk, const void* V, int64_t ldv, qa_dtype dtype, int64_t T,
+                      const int64_t* slots, int32_t bits, int64_t pages, int32_t heads, int32_t page, int32_t D,
+                      void* k_codes, float* k_scales, void* v_codes, float* v_scales, void* stream) {
+    if (!valid_dtype(dtype) || (bits != 8 && bits != 4))
+        return fail(QA_ERR_VALUE, "qa_kv_write: bad dtype %d or bits %d (8 or 4)", (int)dtype, bits);
+    const int64_t el = bytes_of(dtype);
+    if (T < 0 || T > kMaxTokens || !cache_shape_ok(pages, heads, page, D) || ldk < (int64_t)heads * D ||
+        ldv < (int64_t)heads * D || ldk * el % 16 != 0 || ldv * el % 16 != 0)
+        return fail(QA_ERR_SHAPE, "qa_kv_write: need 0 <= T <= 2^23, 1 <= heads <= 65535, D %% 16 == 0 in 16..256, page "
+                                  "a power of two in 16..1024, token strides >= heads D in whole 16 bytes");
+    if (T == 0) return ok();
+    if (!K || !V || !slots || !k_codes || !k_scales || !v_codes || !v_scales)
+        return fail(QA_ERR_NULL, "qa_kv_write: NULL pointer");
+    if (!aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 8) || !cache_aligned(k_codes, k_scales, v_codes, v_scales))
+        return fail(QA_ERR_ALIGN, "qa_kv_write: K, V, codes, scales 16-byte, slots 8-byte aligned");
+    return device_status(qa::launch_kv_write(K, ldk, V, ldv, (int)dtype, T, slots,
+                                             cache_of(k_codes, k_scales, v_codes, v_scales, pages, heads, page, D, bits),
+                                             as_stream(stream)),
+                         "qa_kv_write");
+}
+
+qa_status qa_kv_read(const int64_t* slots, int64_t T, int32_t bits, int64_t pages, int32_t heads, int32_t page,
+                     int32_t D, const void* k_codes, const float* k_scales, const void* v_codes, const float* v_scales,
+                     void* K, void* V, qa_dtype dtype, void* stream) {
+    if (!valid_dtype(dtype) || (bits != 8 && bits != 4))
+        return fail(QA_ERR_VALUE, "qa_kv_read: bad dtype %d or bits %d (8 or 4)", (int)dtype, bits);
+    if (T < 0 || T > kMaxTokens || !cache_shape_ok(pages, heads, page, D))
+        return fail(QA_ERR_SHAPE, "qa_kv_read: need 0 <= T <= 2^23, 1 <= heads <= 65535, D %% 16 == 0 in 16..256, page "
+                                  "a power of two in 16..1024");
+    if (T == 0) return ok();
+    if (!K || !V || !slots || !k_codes || !k_scales || !v_codes || !v_scales)
+        return fail(QA_ERR_NULL, "qa_kv_read: NULL pointer");
+    if (!aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 8) || !cache_aligned(k_codes, k_scales, v_codes, v_scales))
+        return fail(QA_ERR_ALIGN, "qa_kv_read: K, V, codes, scales 16-byte, slots 8-byte aligned");
+    return device_status(qa::launch_kv_read(slots, T,
+                                            cache_of(k_codes, k_scales, v_codes, v_scales, pages, heads, page, D, bits),
+                                            K, V, (int)dtype, as_stream(stream)),
+                         "qa_kv_read");
+}
+
+// ----------------------------------------------------------------- attention over it
+static bool attn_shape_ok(int64_t B, int32_t H, int32_t heads, int32_t D, int64_t max_len, int32_t window) {
+    return B >= 0 && B <= ((int64_t)1 << 20) && heads >= 1 && heads <= kMaxHeads && H >= heads && H <= kMaxHeads &&
+           H % heads == 0 && B * H <= kMaxTokens && D >= 16 && D <= 256 && D % 16 == 0 && max_len >= 0 &&
+           max_len <= kMaxPlaces && window >= 0;
+}
+
+size_t qa_attn_decode_workspace(int64_t B, int32_t H, int32_t heads, int32_t D, int64_t max_len, int32_t window) {
+    if (!attn_shape_ok(B, H, heads, D, max_len, window) || B == 0) return 0;
+    return up(qa::attn_scratch_bytes(B, H, heads, D, max_len, window));
+}
+
+qa_status qa_attn_decode(const void* q, int64_t ldq, qa_dtype q_dtype, int64_t B, int32_t H, int32_t bits,
+                         int64_t pages, int32_t heads, int32_t page, int32_t D, const void* k_codes,
+                         const float* k_scales, const void* v_codes, const float* v_scales, const int32_t* table,
+                         int64_t ldt, int64_t width, const int32_t* lengths, int64_t max_len, int32_t window,
+                         float scale, void* out, qa_dtype out_dtype, float* lse_or_null, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    if (!valid_dtype(q_dtype) || !valid_dtype(out_dtype) || (bits != 8 && bits != 4) || !std::isfinite(scale))
+        return fail(QA_ERR_VALUE, "qa_attn_decode: bad dtype, bits (8 or 4) or scale");
+    if (!attn_shape_ok(B, H, heads, D, max_len, window) || !cache_shape_ok(pages, heads, page, D) || width < 0 ||
+        width > kMaxPlaces / page || max_len > width * page || ldt < width || ldq < (int64_t)H * D ||
+        ldq * bytes_of(q_dtype) % 16 != 0)
+        return fail(QA_ERR_SHAPE, "qa_attn_decode: need 0 <= B <= 2^20, H a multiple of heads up to 65535, B H <= 2^23, "
+                                  "D %% 16 == 0 in 16..256, page a power of two in 16..1024, 0 <= max_len <= width page "
+                                  "<= 2^30, ldt >= width, ldq >= H D in whole 16 bytes, window >= 0");
+    if (B == 0) return ok();
+    const size_t need = qa_attn_decode_workspace(B, H, heads, D, max_len, window);
+    if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !lengths || !out || (width > 0 && !table) ||
+        (need > 0 && !workspace))
+        return fail(QA_ERR_NULL, "qa_attn_decode: NULL pointer");
+    if (!aligned(q, 16) || !cache_aligned(k_codes, k_scales, v_codes, v_scales) || !aligned(table, 4) ||
+        !aligned(lengths, 4) || !aligned(out, 16) || !aligned(lse_or_null, 4) || (need > 0 && !aligned(workspace, kAlign)))
+        return fail(QA_ERR_ALIGN, "qa_attn_decode: q, codes, scales, out 16-byte, workspace 256-byte, others 4-byte aligned");
+    if (workspace_bytes < need)
+        return fail(QA_ERR_WORKSPACE, "qa_attn_decode: workspace %zu < %zu bytes", workspace_bytes, need);
+    return device_status(qa::launch_attn_decode(q, ldq, (int)q_dtype, B, H,
+                                                cache_of(k_codes, k_scales, v_codes, v_scales, pages, heads, page, D, bits),
+                                                table, ldt, width, lengths, max_len, window, scale, out, (int)out_dtype,
+                                                lse_or_null, workspace, as_stream(stream)),
+                         "qa_attn_decode");
+}
+
+// ----------------------------------------------------------------- linear with an epilogue
+qa_status qa_qlinear_int8_act(const int8_t* Xq, const float* s_x, int64_t M, int64_t K, const int8_t* Wq,
+                              const float* s_w, int64_t N, const float* bias_or_null, qa_act act,
+                              const void* residual_or_null, int64_t ldr, void* out, int64_t ldo, qa_dtype dtype,
+                              void* stream) {
+    if (M < 0 || M > kMaxTokens || N < 0 || N > kMaxI32 || K <= 0 || K % 16 != 0 || K > kMaxK_i8 ||
+        (M + 63) / 64 * ((N + 63) / 64) >= kMaxTiles || ldo < N || (residual_or_null && ldr < N))
+        return fail(QA_ERR_SHAPE, "qa_qlinear_int8_act: need 0 <= M <= 2^23, N >= 0, (M / 64) (N / 64) < 2^23, "
+                                  "K %% 16 == 0, 0 < K <= %lld, row strides >= N", (long long)kMaxK_i8);
+    if (!valid_dtype(dtype) || (int)act < (int)QA_ACT_NONE || (int)act > (int)QA_ACT_SILU)
+        return fail(QA_ERR_VALUE, "qa_qlinear_int8_act: bad dtype %d or act %d", (int)dtype, (int)act);
+    if (M == 0 || N == 0) return ok();
+    if (!Xq || !s_x || !Wq || !s_w || !out) return fail(QA_ERR_NULL, "qa_qlinear_int8_act: NULL pointer");
+    const size_t el = (size_t)bytes_of(dtype);
+    if (!aligned(Xq, 16) || !aligned(Wq, 16) || !aligned(s_x, 4) || !aligned(s_w, 4) || !aligned(bias_or_null, 4) ||
+        !aligned(residual_or_null, el) || !aligned(out, el))
+        return fail(QA_ERR_ALIGN, "qa_qlinear_int8_act: Xq, Wq 16-byte, scales and bias 4-byte, out and residual aligned "
+                                  "to their elements");
+    return device_status(qa::launch_linear_i8_act(Xq, s_x, M, K, Wq, s_w, N, bias_or_null, (int)act, residual_or_null,
+                                                  ldr, out, ldo, (int)dtype, as_stream(stream)),
+                         "qa_qlinear_int8_act");
+}
+
 qa_status qa_probe_stream_read(const void* src, size_t bytes, int32_t wgs, int32_t lane_bytes, int32_t unroll,
                                uint32_t* sink, void* stream) {
     if (wgs < 1 || wgs > 65536) return fail(QA_ERR_SHAPE, "qa_probe_stream_read: need wgs in [1, 65536]");

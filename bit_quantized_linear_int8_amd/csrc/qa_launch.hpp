@@ -229,4 +229,32 @@ hipError_t launch_lora_i8(const int8_t* Xq, const float* s_x, const void* X, boo
                           const float* alpha, int r, int L, const int32_t* seg, const int32_t* which, int R, void* out,
                           int out_dtype, void* scratch, hipStream_t st);
 
+// A paged cache of keys and values in int8 or int4 codes, one scale per token and
+// head: codes [pages][heads][2^shift][D], scales [pages][heads][2^shift].
+struct KvCache {
+    void* k_codes;
+    float* k_scales;
+    void* v_codes;
+    float* v_scales;
+    int64_t pages;
+    int32_t heads, D, shift, bits;
+};
+hipError_t launch_kv_write(const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype, int64_t T,
+                           const int64_t* slots, const KvCache& c, hipStream_t st);
+hipError_t launch_kv_read(const int64_t* slots, int64_t T, const KvCache& c, void* k, void* v, int dtype,
+                          hipStream_t st);
+
+// Attention of one token per sequence over such a cache; splits of a sequence are
+// joined by a second launch through scratch.
+size_t attn_scratch_bytes(int64_t B, int32_t H, int32_t heads, int32_t D, int64_t max_len, int32_t window);
+hipError_t launch_attn_decode(const void* q, int64_t ldq, int q_dtype, int64_t B, int32_t H, const KvCache& c,
+                              const int32_t* table, int64_t ldt, int64_t width, const int32_t* lengths, int64_t max_len,
+                              int32_t window, float scale, void* out, int out_dtype, float* lse, void* scratch,
+                              hipStream_t st);
+
+// The int8 linear with bias, activation (qa_act) and residual in its epilogue.
+hipError_t launch_linear_i8_act(const int8_t* Xq, const float* s_x, int64_t M, int64_t K, const int8_t* Wq,
+                                const float* s_w, int64_t N, const float* bias, int act, const void* res, int64_t ldr,
+                                void* out, int64_t ldo, int dtype, hipStream_t st);
+
 }  // namespace qa

@@ -19,8 +19,10 @@
  *     so both quantize to int8 with plain absmax scales (per token or per
  *     tensor for X, per output channel for W) and no fp16 branch.
  *   - Around them: the norm that makes a linear's codes, routing to experts,
- *     the experts' gated feed-forward on int8 codes, and an int8 projection
- *     with the low-rank adapters of many requests.
+ *     the experts' gated feed-forward on int8 codes, an int8 projection
+ *     with the low-rank adapters of many requests, an int8 linear with bias,
+ *     activation and residual, and a paged cache of keys and values in int8 or
+ *     int4 codes with the attention of single tokens over it.
  *
  * Sources, cited by page title and section:
  *   [AIInfra-Q01]  Infrasys-AI "AIInfra" notes, page 05Quantization01 (模型量化):
@@ -724,6 +726,108 @@ qa_status qa_qlinear_int8_lora(const int8_t* Xq, const float* s_x, const void* X
                                const float* alpha, int32_t r, int64_t L, const int32_t* seg, const int32_t* which,
                                int64_t R, void* out, qa_dtype out_dtype, void* workspace, size_t workspace_bytes,
                                void* stream);
+
+/* ---------------------------------------------------------------------------
+ * A paged cache of keys and values in int8 or int4 codes
+ *
+ * The cache is four arrays: for keys and for values, codes and scales.
+ *   codes   bits 8: i8 [pages x heads x page x D]
+ *           bits 4: u32 [pages x heads x page x D/8], element 8w+i of a row in
+ *           bits [4i+3:4i] of its word w, two's complement
+ *   scales  f32 [pages x heads x page]
+ * A row (one token, one head) x is stored as
+ *   s = fl32(max_d |x_d| / q_max) (1.0 where that is 0), q_max = 127 or 7
+ *   q_d = clip(rint(fl32(x_d / s)), -q_max, q_max)
+ * A row that holds an infinity or NaN gets s = NaN and codes 0; other rows are
+ * unaffected.  slots name tokens' places: slot = page index * page + place in
+ * the page.
+ *
+ * qa_kv_write: K, V [T x heads x D] of dtype (fp32, fp16 or bf16), token strides
+ *   ldk, ldv in elements (a token's heads are contiguous), into the places
+ *   slots i64 [T].  A slot outside 0 .. pages page - 1 (-1 for padding) writes
+ *   nothing; places that no slot names are left as they were.  A place named
+ *   twice holds unspecified codes and scales (no access leaves the arrays).
+ * qa_kv_read: x_d = fl32(q_d s), rounded to dtype, for the places slots i64 [T]
+ *   in any order, into K, V [T x heads x D] contiguous of dtype; a slot outside the
+ *   cache gives a row of zeros.
+ * Errors: (QA_ERR_SHAPE) T outside 0..2^23, heads outside 1..65535, D not a
+ * multiple of 16 in 16..256, page not a power of two in 16..1024, pages < 0 or
+ * pages > 2^31 - 1, a token stride below heads D or not a multiple of 16
+ * bytes; (QA_ERR_VALUE) bad dtype, bits not 8 or 4; NULL pointers; K, V, codes
+ * and scales not 16-byte, slots not 8-byte aligned.  T == 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+qa_status qa_kv_write(const void* K, int64_t ldk, const void* V, int64_t ldv, qa_dtype dtype, int64_t T,
+                      const int64_t* slots, int32_t bits, int64_t pages, int32_t heads, int32_t page, int32_t D,
+                      void* k_codes, float* k_scales, void* v_codes, float* v_scales, void* stream);
+qa_status qa_kv_read(const int64_t* slots, int64_t T, int32_t bits, int64_t pages, int32_t heads, int32_t page,
+                     int32_t D, const void* k_codes, const float* k_scales, const void* v_codes, const float* v_scales,
+                     void* K, void* V, qa_dtype dtype, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of one new token per sequence over such a cache
+ *
+ *   n = min(max(lengths[b], 0), max_len);  t runs over max(0, n - window) .. n - 1
+ *   (window 0: over 0 .. n - 1), token t at place t % page of page
+ *   table[b][t / page]; an entry outside 0 .. pages - 1 masks its tokens
+ *   x_t = scale sum_d q[b][h][d] k_t[d]        (k, v of key head h heads / H)
+ *   out[b][h][d] = sum_t exp(x_t) v_t[d] / sum_t exp(x_t)
+ *   lse[b][h] = log sum_t exp(x_t)
+ * A sequence without a token to see (length 0, every page masked) gets a row of
+ * zeros and lse = -infinity.  Scales and sums are fp32; scores and weights keep
+ * about 2^-21 of their head's largest, and the output is rounded once.  A NaN
+ * scale among the tokens that are seen makes the head's outputs NaN.
+ *   q        [B x H x D] of q_dtype (fp32, fp16 or bf16), token stride ldq
+ *            elements, finite
+ *   table    i32 [B x width], row stride ldt: the pages of each sequence.  Entries
+ *            past the last token's are not read
+ *   lengths  i32 [B]: tokens in the cache, the new one's included
+ *   max_len  an upper bound of the lengths that the host knows: sequences are
+ *            split over the card by it.  Longer ones count as max_len
+ *   out      [B x H x D] contiguous of out_dtype; lse f32 [B x H] or NULL
+ *   workspace  qa_attn_decode_workspace(...) bytes (any content; 0 where a
+ *            sequence is not split, workspace may then be NULL)
+ * Errors: (QA_ERR_SHAPE) B outside 0..2^20, heads outside 1..65535, H not a
+ * multiple of heads, H > 65535, B H > 2^23, D, page, pages as qa_kv_write, width
+ * or max_len negative, width page > 2^30, max_len > width page, ldt < width,
+ * ldq < H D or not a multiple of 16 bytes, window < 0; (QA_ERR_VALUE) bad dtypes
+ * or bits, scale not finite; NULL pointers; q, codes, scales and out not 16-byte,
+ * table, lengths and lse not 4-byte, workspace not 256-byte aligned; small
+ * workspace.  B == 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+size_t qa_attn_decode_workspace(int64_t B, int32_t H, int32_t heads, int32_t D, int64_t max_len, int32_t window);
+qa_status qa_attn_decode(const void* q, int64_t ldq, qa_dtype q_dtype, int64_t B, int32_t H, int32_t bits,
+                         int64_t pages, int32_t heads, int32_t page, int32_t D, const void* k_codes,
+                         const float* k_scales, const void* v_codes, const float* v_scales, const int32_t* table,
+                         int64_t ldt, int64_t width, const int32_t* lengths, int64_t max_len, int32_t window,
+                         float scale, void* out, qa_dtype out_dtype, float* lse_or_null, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * int8 linear on codes with bias, activation and residual
+ *
+ *   out[m][n] = act(s_x[m] s_w[n] sum_k Xq[m][k] Wq[n][k] + bias[n]) + residual[m][n]
+ * formed in fp32 from the exact integer sum and rounded once.
+ *   QA_ACT_NONE x; QA_ACT_RELU max(x, 0); QA_ACT_GELU x Phi(x);
+ *   QA_ACT_GELU_TANH x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2;
+ *   QA_ACT_SILU x / (1 + exp(-x))
+ *   Xq, s_x  i8 [M x K], f32 [M] (qa_rmsnorm_int8 or qa_quantize_rowwise_int8)
+ *   Wq, s_w  i8 [N x K], f32 [N]
+ *   bias     f32 [N] or NULL
+ *   residual [M x N] of dtype, row stride ldr elements, or NULL
+ *   out      [M x N] of dtype, row stride ldo; may be residual itself (same
+ *            pointer and stride), no other overlap with the inputs is allowed
+ * A row whose scale is NaN (of a token without a finite norm) gives NaNs.
+ * Errors: (QA_ERR_SHAPE) M outside 0..2^23, N outside 0..2^31 - 1,
+ * ceil(M / 64) ceil(N / 64) >= 2^23, K not a positive multiple of 16 up to
+ * 131072, ldo or ldr below N; (QA_ERR_VALUE) bad dtype or act; NULL pointers;
+ * Xq and Wq not 16-byte, scales and bias not 4-byte, out and residual not
+ * aligned to their elements.  M == 0 or N == 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+typedef enum { QA_ACT_NONE = 0, QA_ACT_RELU = 1, QA_ACT_GELU = 2, QA_ACT_GELU_TANH = 3, QA_ACT_SILU = 4 } qa_act;
+qa_status qa_qlinear_int8_act(const int8_t* Xq, const float* s_x, int64_t M, int64_t K, const int8_t* Wq,
+                              const float* s_w, int64_t N, const float* bias_or_null, qa_act act,
+                              const void* residual_or_null, int64_t ldr, void* out, int64_t ldo, qa_dtype dtype,
+                              void* stream);
 
 /* ---------------------------------------------------------------------------
  * Measurement helper, not part of the method: the single-launch HBM read
