@@ -108,29 +108,19 @@ __device__ __forceinline__ constexpr int row8_order(int j) {
     return BITS == 8 ? j : (j >> 1) + 4 * (j & 1);
 }
 
-__device__ __forceinline__ float wide(const void* p, int64_t at, int dt) {
-    if (dt == 0) return static_cast<const float*>(p)[at];
-    const uint16_t u = static_cast<const uint16_t*>(p)[at];
-    return dt == 1 ? h2f(u) : __builtin_bit_cast(float, (uint32_t)u << 16);
-}
-
-// N consecutive outputs of type dt at p[at] (8-byte aligned at least).
-template <int N>
-__device__ __forceinline__ void store_row(void* p, int64_t at, int dt, const float* v) {
+// Four consecutive outputs of type dt at p[at].
+__device__ __forceinline__ void store_quad(void* p, int64_t at, int dt, v4f v) {
     if (dt == 0) {
-        float* o = static_cast<float*>(p) + at;
-#pragma unroll
-        for (int j = 0; j < N; j += 4) *reinterpret_cast<v4f*>(o + j) = v4f{v[j], v[j + 1], v[j + 2], v[j + 3]};
+        *reinterpret_cast<v4f*>(static_cast<float*>(p) + at) = v;
         return;
     }
-    uint16_t* o = static_cast<uint16_t*>(p) + at;
+    uint32_t w[2];
 #pragma unroll
-    for (int j = 0; j < N; j += 4) {
-        uint16_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = dt == 1 ? f2h(v[j + e]) : f2bf(v[j + e]);
-        *reinterpret_cast<u32x2*>(o + j) = u32x2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t lo = dt == 1 ? f2h(v[2 * j]) : f2bf(v[2 * j]), hi = dt == 1 ? f2h(v[2 * j + 1]) : f2bf(v[2 * j + 1]);
+        w[j] = lo | (hi << 16);
     }
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p) + at) = u32x2{w[0], w[1]};
 }
 
 // First and last tokens that a sequence's query sees, and the place that its
@@ -157,8 +147,8 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
     constexpr int VN = DP / 16;                              // values of a lane per token
     constexpr int VB = VN * BITS / 8;                        // their bytes
     constexpr int VW = VB < 4 ? 1 : VB / 4;                  // their words
-    __shared__ v4f red[2][16][DP / 4];
-    __shared__ float st_m[4][16], st_l[4][16], st_e[4][16];
+    __shared__ v4f red[4][16][DP / 4 + 1];                // (one more: the 16 rows start at different banks)
+    __shared__ float st_m[4][16], st_l[4][16], st_e[4][16], inv_l[16];
 
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int m16 = lane & 15, c4 = lane >> 4;
@@ -173,19 +163,16 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
     span_of(a, b, first, end, from);
     const int64_t lo64 = (int64_t)from + (int64_t)split * a.chunk;
     const int g = gt * 16 + m16;                             // the lane's head within the group
-    const bool head = g < a.group;
-    const int64_t row = (int64_t)b * a.H + h * a.group + g;  // its row of the output
+    const int heads_here = a.group - gt * 16 < 16 ? a.group - gt * 16 : 16;
+    const int64_t row0 = (int64_t)b * a.H + h * a.group + gt * 16;    // the block's first row of the output
     if (lo64 >= end) {                                       // nothing in this chunk
-        if (a.splits > 1) {
-            if (wave == 0 && c4 == 0 && head) a.plse[row * a.splits + split] = -__builtin_inff();
-        } else if (wave == 0 && head) {
-            const float z[VN] = {};
-            for (int e = 0; e < 4; ++e) {
-                const int d = VN * (4 * c4 + e);
-                if (d < a.D) store_row<VN>(a.out, row * a.D + d, a.dt, z);
-            }
-            if (c4 == 0 && a.lse) a.lse[row] = -__builtin_inff();
+        if ((int)threadIdx.x < heads_here) {
+            if (a.splits > 1) a.plse[(row0 + threadIdx.x) * a.splits + split] = -__builtin_inff();
+            else if (a.lse) a.lse[row0 + threadIdx.x] = -__builtin_inff();
         }
+        if (a.splits == 1)
+            for (int i = threadIdx.x; i < heads_here * a.D / 4; i += 256)
+                store_quad(a.out, row0 * a.D + 4 * i, a.dt, v4f{0.0f, 0.0f, 0.0f, 0.0f});
         return;
     }
     const int lo = (int)lo64;
@@ -197,7 +184,7 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
     const uint32_t RB = (uint32_t)a.D * BITS / 8;            // bytes of a row
     // the page of the 16 tokens from t: its index, or -1 (past the end, or not one of the cache's)
     auto page_of = [&](int t) __attribute__((always_inline)) {
-        const int p = __builtin_amdgcn_readfirstlane(tab[(t < hi ? t : hi - 1) >> a.shift]);
+        const int p = __builtin_amdgcn_readfirstlane(tab[(t < a.max_len ? t : a.max_len - 1) >> a.shift]);
         return t < hi && (uint32_t)p < (uint32_t)a.pages ? p : -1;
     };
     struct Stage {
@@ -252,18 +239,36 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
     v8h qf[QT][NF];
     float qscale;
     {
+        constexpr uint32_t EL = QT == 2 ? 4 : 2;             // bytes of a query value
+        const rsrc_t rq = make_rsrc(static_cast<const uint8_t*>(a.q) + ((int64_t)b * a.ldq + (int64_t)h * a.group * a.D) * EL,
+                                    (int64_t)a.group * a.D * EL);
         float x[NF][8], top = 0.0f;
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
+        for (int f = 0; f < NF; ++f) {
+            const int d = (c4 + 4 * (f / FP)) * CC + 8 * (f % FP);
+            const uint32_t off = d < a.D ? (uint32_t)(g * a.D + d) * EL : kOOB;    // (heads past the group: zeros)
+            const u32x4 u = bload16(rq, off);
+            float y[8];
+            if constexpr (QT == 2) {
+                const v4f lo = __builtin_bit_cast(v4f, u), hi = __builtin_bit_cast(v4f, bload16(rq, off + 16));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = lo[j], y[4 + j] = hi[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t v = u[j >> 1] >> (16 * (j & 1));
+                    y[j] = a.qdt == 1 ? h2f((uint16_t)v) : __builtin_bit_cast(float, v << 16);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int d = (c4 + 4 * (f / FP)) * CC + 8 * (f % FP) + row8_order<BITS>(j);
-                x[f][j] = head && d < a.D ? wide(a.q, (int64_t)b * a.ldq + (int64_t)(h * a.group + g) * a.D + d, a.qdt) : 0.0f;
-                top = fmaxf(top, __builtin_fabsf(x[f][j]));
+                x[f][j] = y[row8_order<BITS>(j)];
+                top = fmaxf(top, __builtin_fabsf(y[j]));
             }
+        }
         top = fmaxf(top, __shfl_xor(top, 16, QA_WAVE));
         top = fmaxf(top, __shfl_xor(top, 32, QA_WAVE));
-        // times 2^up the head's largest is in [2^13, 2^14)
+        // times 2^e the head's largest is in [2^13, 2^14)
         const int e = top > 0.0f && top < __builtin_inff() ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
         qscale = __builtin_ldexpf(a.scale2, -e);
 #pragma unroll
@@ -410,57 +415,40 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
         st_l[wave][m16] = l;
         st_e[wave][m16] = ex;
     }
-    __syncthreads();
-    float mg = kLow, lg = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) mg = fmaxf(mg, st_m[w][m16]);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) lg += st_l[w][m16] * __builtin_amdgcn_exp2f(st_m[w][m16] - mg);
-    const float f = __builtin_ldexpf(__builtin_amdgcn_exp2f(m - mg), (int)ex);
-    float o[4][VN];                                          // head m16, values VN (4 c4 + e) + i
+    // head m16, values VN (4 c4 + e) + i
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int i = 0; i < VN; ++i) o[e][i] = acc[i][e] * f;
-    auto give = [&](int to) __attribute__((always_inline)) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int i = 0; i < VN / 4; ++i)
-                red[to][m16][VN / 4 * (4 * c4 + e) + i] = v4f{o[e][4 * i], o[e][4 * i + 1], o[e][4 * i + 2], o[e][4 * i + 3]};
-    };
-    auto take = [&](int at) __attribute__((always_inline)) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int i = 0; i < VN / 4; ++i) {
-                const v4f v = red[at][m16][VN / 4 * (4 * c4 + e) + i];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[e][4 * i + j] += v[j];
-            }
-    };
-    if (wave >= 2) give(wave - 2);
+        for (int i = 0; i < VN / 4; ++i)
+            red[wave][m16][VN / 4 * (4 * c4 + e) + i] = v4f{acc[4 * i][e], acc[4 * i + 1][e], acc[4 * i + 2][e], acc[4 * i + 3][e]};
     __syncthreads();
-    if (wave < 2) take(wave);
-    __syncthreads();
-    if (wave == 1) give(0);
-    __syncthreads();
-    if (wave != 0 || !head) return;
-    take(0);
-    const float inv = lg == 0.0f ? 0.0f : 1.0f / lg;
-    const float lse = lg == 0.0f ? -__builtin_inff() : mg + __builtin_log2f(lg);
+    if (threadIdx.x < 16) {
+        float mg = kLow, lg = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int d = VN * (4 * c4 + e);
-        if (d >= a.D) continue;
+        for (int w = 0; w < 4; ++w) mg = fmaxf(mg, st_m[w][threadIdx.x]);
 #pragma unroll
-        for (int i = 0; i < VN; ++i) o[e][i] *= inv;
-        if (a.splits > 1) store_row<VN>(a.part, (row * a.splits + split) * a.D + d, 0, o[e]);
-        else store_row<VN>(a.out, row * a.D + d, a.dt, o[e]);
+        for (int w = 0; w < 4; ++w) {
+            const float f = __builtin_amdgcn_exp2f(st_m[w][threadIdx.x] - mg);
+            lg += st_l[w][threadIdx.x] * f;
+            st_e[w][threadIdx.x] = __builtin_ldexpf(f, (int)st_e[w][threadIdx.x]);
+        }
+        inv_l[threadIdx.x] = lg == 0.0f ? 0.0f : 1.0f / lg;
+        if ((int)threadIdx.x < heads_here) {
+            const float lse = lg == 0.0f ? -__builtin_inff() : mg + __builtin_log2f(lg);
+            if (a.splits > 1) a.plse[(row0 + threadIdx.x) * a.splits + split] = lse;
+            else if (a.lse) a.lse[row0 + threadIdx.x] = lse * kLn2;
+        }
     }
-    if (c4 == 0) {
-        if (a.splits > 1) a.plse[row * a.splits + split] = lse;
-        else if (a.lse) a.lse[row] = lse * kLn2;
+    __syncthreads();
+    const int L = a.D / 4;
+    for (int i = threadIdx.x; i < heads_here * L; i += 256) {
+        const int r = i / L, d = i - r * L;
+        v4f o = red[0][r][d] * st_e[0][r];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) o += red[w][r][d] * st_e[w][r];
+        o *= inv_l[r];
+        if (a.splits > 1) *reinterpret_cast<v4f*>(a.part + ((row0 + r) * a.splits + split) * a.D + 4 * d) = o;
+        else store_quad(a.out, (row0 + r) * a.D + 4 * d, a.dt, o);
     }
 }
 
@@ -472,11 +460,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     __shared__ float red[8];
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
     const int64_t row = blockIdx.x;
-    const int b = (int)(row / a.H);
-    int first, end, from;
-    span_of(a, b, first, end, from);
-    int n = (int)(((int64_t)end - from + a.chunk - 1) / a.chunk);
-    n = end <= first ? 0 : (n < a.splits ? n : a.splits);
+    const int n = a.splits;
     float top = -__builtin_inff();
     for (int i = tid; i < n; i += 256) top = fmaxf(top, a.plse[row * a.splits + i]);
     top = wave_max(top);
@@ -508,8 +492,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     if (tid >= L) return;
     for (int i = 1; i < groups; ++i) s += sum[i * L + tid];
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    const float o[4] = {s[0] * inv, s[1] * inv, s[2] * inv, s[3] * inv};
-    store_row<4>(a.out, row * a.D + 4 * tid, a.dt, o);
+    store_quad(a.out, row * a.D + 4 * tid, a.dt, s * inv);
     if (tid == 0 && a.lse) a.lse[row] = total == 0.0f ? -__builtin_inff() : (top + __builtin_log2f(total)) * kLn2;
 }
 

@@ -779,7 +779,7 @@ qa_status qa_kv_read(const int64_t* slots, int64_t T, int32_t bits, int64_t page
  *   q        [B x H x D] of q_dtype (fp32, fp16 or bf16), token stride ldq
  *            elements, finite
  *   table    i32 [B x width], row stride ldt: the pages of each sequence.  Entries
- *            past the last token's are not read
+ *            past the last token's may hold anything
  *   lengths  i32 [B]: tokens in the cache, the new one's included
  *   max_len  an upper bound of the lengths that the host knows: sequences are
  *            split over the card by it.  Longer ones count as max_len
