@@ -8,22 +8,26 @@
 // has).  The heads that share a key head are the 16 columns of one MFMA tile.
 //
 // A wave takes 32 tokens at a time, from memory straight into MFMA operands:
-//   - keys are the rows of A: lane (m, c) holds 16-byte pieces c, c + 4, ... of
-//     token m (and 16 + m); the order of d that this makes is the queries' too;
+//   - keys are the rows of A of an int8 product: lane (m, c) holds 16-byte pieces
+//     c, c + 4, ... of token m (and 16 + m), as they are (int4: the nibbles in the
+//     upper halves of bytes, 16 times the codes);
 //   - x comes out with four consecutive tokens of column g = lane % 16 in each
 //     lane, which is where p has to be as the operand B of the second product;
 //   - values are A of the second product, transposed: lane (m, c) holds the
 //     16th part m of the D values of tokens 4 c + j and 16 + 4 c + j, and
-//     the bytes of two tokens are put side by side in registers.
+//     the codes of two tokens are put side by side in registers.
 // So nothing passes through LDS, and lanes exchange nothing inside the loop.
 //
-// Codes become fp16 exactly: the byte (or nibble) with its sign bit flipped under
-// the exponent of 1024, less 1024 and the flip.  Queries enter as fp16 times a
-// power of two per head (exact for fp16 and bf16; fp32 as two numbers, 2^-22 of
-// the head's largest).  p s_v enters as two fp16 numbers with a power of two per
-// head, 2^-22 of the value, so that neither the scales' range nor a softmax over
-// long contexts costs digits: one fp16 number would add an error as large as the
-// rounding of an fp16 output.  Sums are fp32.
+// Queries enter as whole numbers of 22 bits and a sign next to the head's largest
+// (what fp16 and bf16 hold of values down to 2^-11 and 2^-14 of it), in three
+// balanced digits of base 256, so that the scores of integers are exact: three
+// int8 products cost less than to convert every key's codes to fp16.  Values'
+// codes become fp16 (times 2^-10) exactly: the byte or nibble with its sign bit
+// flipped is an fp16 number below the normal ones, and a fused multiply-add
+// scales it and takes the flip away.  p s_v enters as two fp16 numbers with a power
+// of two per head, 2^-22 of the value, so that neither the scales' range nor a
+// softmax over long contexts costs digits: one fp16 number would add an error as
+// large as the rounding of an fp16 output.  Sums are fp32.
 //
 // The reference m of the exponentials and the power of two of p s_v follow their
 // running maxima lazily: only when a tile passes one by 2^16 (or 2^14) are
@@ -69,43 +73,20 @@ constexpr float kLn2 = 0.693147180559945309f;
 __device__ __forceinline__ v2h pk(uint32_t u) { return __builtin_bit_cast(v2h, u); }
 __device__ __forceinline__ uint32_t up(v2h h) { return __builtin_bit_cast(uint32_t, h); }
 
-// Pairs of bytes u (in the low bytes of each half, biased by 128) less the bias.
+// Pairs of codes as fp16 times 2^-10, from their bytes plus 128 in the low bytes of
+// each half: u 2^-24 as it stands, times 2^14, less 128 2^-10.
 __device__ __forceinline__ uint32_t byte_pair(uint32_t u) {
-    return up(pk(u | 0x64006400u) - v2h{(_Float16)1152, (_Float16)1152});
+    return up(__builtin_elementwise_fma(pk(u), v2h{(_Float16)16384, (_Float16)16384},
+                                        v2h{(_Float16)-0.125, (_Float16)-0.125}));
 }
-// Pairs of nibbles (biased by 8) in bits 0..3 or 4..7 of each half of y.
+// The same from nibbles plus 8 in bits 0..3, or 4..7, of each half of y.
 __device__ __forceinline__ uint32_t nib_pair0(uint32_t y) {
-    return up(pk((y & 0x000f000fu) | 0x64006400u) - v2h{(_Float16)1032, (_Float16)1032});
+    return up(__builtin_elementwise_fma(pk(y & 0x000f000fu), v2h{(_Float16)16384, (_Float16)16384},
+                                        v2h{(_Float16)-0.0078125, (_Float16)-0.0078125}));
 }
 __device__ __forceinline__ uint32_t nib_pair1(uint32_t y) {
-    return up(__builtin_elementwise_fma(pk((y & 0x00f000f0u) | 0x64006400u), v2h{(_Float16)0.0625, (_Float16)0.0625},
-                                        v2h{(_Float16)-72, (_Float16)-72}));
-}
-
-// Eight codes of one row as fp16: bytes of two words in order, or nibbles of one
-// word in the order 0 4 1 5 2 6 3 7.
-template <int BITS>
-__device__ __forceinline__ v8h row8(uint32_t a, uint32_t b) {
-    u32x4 o;
-    if constexpr (BITS == 8) {
-        a ^= 0x80808080u;
-        b ^= 0x80808080u;
-        o[0] = byte_pair(__builtin_amdgcn_perm(0u, a, 0x0c010c00u));
-        o[1] = byte_pair(__builtin_amdgcn_perm(0u, a, 0x0c030c02u));
-        o[2] = byte_pair(__builtin_amdgcn_perm(0u, b, 0x0c010c00u));
-        o[3] = byte_pair(__builtin_amdgcn_perm(0u, b, 0x0c030c02u));
-    } else {
-        a ^= 0x88888888u;
-        o[0] = nib_pair0(a);
-        o[1] = nib_pair1(a);
-        o[2] = nib_pair0(a >> 8);
-        o[3] = nib_pair1(a >> 8);
-    }
-    return __builtin_bit_cast(v8h, o);
-}
-template <int BITS>
-__device__ __forceinline__ constexpr int row8_order(int j) {
-    return BITS == 8 ? j : (j >> 1) + 4 * (j & 1);
+    return up(__builtin_elementwise_fma(pk(y & 0x00f000f0u), v2h{(_Float16)1024, (_Float16)1024},
+                                        v2h{(_Float16)-0.0078125, (_Float16)-0.0078125}));
 }
 
 // Four consecutive outputs of type dt at p[at].
@@ -137,17 +118,17 @@ __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), f
 }  // namespace
 
 // DP: D rounded up to 64, 128 or 256 (what lies behind D meets queries of 0, or is
-// not stored).  QT: fp16 numbers that a query value is made of.
-template <int BITS, int DP, int QT>
-__global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
+// not stored).  F32: fp32 queries.
+template <int BITS, int DP, bool F32>
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 3) void k_attn_decode(AttnArgs a) {
     constexpr int CC = BITS == 8 || DP == 64 ? 16 : 32;      // codes of a lane's piece of a key
     constexpr int NS = DP / (4 * CC);                        // pieces of a lane
     constexpr int PB = CC * BITS / 8;                        // bytes of a piece
-    constexpr int FP = CC / 8, NF = NS * FP;                 // MFMA steps of a piece, of a key
+    constexpr int NM = DP / 64;                              // MFMA steps of a key
     constexpr int VN = DP / 16;                              // values of a lane per token
     constexpr int VB = VN * BITS / 8;                        // their bytes
     constexpr int VW = VB < 4 ? 1 : VB / 4;                  // their words
-    __shared__ v4f red[4][16][DP / 4 + 1];                // (one more: the 16 rows start at different banks)
+    __shared__ v4f red[4][16][DP / 4 + 1];                   // (one more: the 16 rows start at different banks)
     __shared__ float st_m[4][16], st_l[4][16], st_e[4][16], inv_l[16];
 
     const int lane = threadIdx.x & 63, wave = wave_id();
@@ -177,107 +158,132 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
     }
     const int lo = (int)lo64;
     const int hi = end - lo < a.chunk ? end : lo + a.chunk;
-    const int ntiles = (hi - lo + 31) >> 5;
 
     const int32_t* tab = a.table + (int64_t)b * a.ldt;
     const int page = 1 << a.shift;
     const uint32_t RB = (uint32_t)a.D * BITS / 8;            // bytes of a row
     // the page of the 16 tokens from t: its index, or -1 (past the end, or not one of the cache's)
-    auto page_of = [&](int t) __attribute__((always_inline)) {
-        const int p = __builtin_amdgcn_readfirstlane(tab[(t < a.max_len ? t : a.max_len - 1) >> a.shift]);
+    auto entry = [&](int t) __attribute__((always_inline)) {
+        return tab[(t < a.max_len ? t : a.max_len - 1) >> a.shift];
+    };
+    auto page_of = [&](int t, int e) __attribute__((always_inline)) {
+        const int p = __builtin_amdgcn_readfirstlane(e);
         return t < hi && (uint32_t)p < (uint32_t)a.pages ? p : -1;
     };
-    struct Stage {
-        u32x4 k[2][NS];
-        uint32_t v[8][VW];
-        v4f ks[2], vs[2];
-    };
-    auto load = [&](Stage& s, int t0, int p0, int p1) __attribute__((always_inline)) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int p = u ? p1 : p0;
-            const int64_t base = ((int64_t)(p < 0 ? 0 : p) * a.heads + h) << a.shift;    // row of the page's first token
-            const uint32_t t = (uint32_t)(t0 + 16 * u) & (uint32_t)(page - 1);
-            const rsrc_t rk = make_rsrc(a.kc + base * RB, p < 0 ? 0 : (int64_t)page * RB);
-            const rsrc_t rv = make_rsrc(a.vc + base * RB, p < 0 ? 0 : (int64_t)page * RB);
-            const rsrc_t rks = make_rsrc(a.ks + base, p < 0 ? 0 : (int64_t)page * 4);
-            const rsrc_t rvs = make_rsrc(a.vs + base, p < 0 ? 0 : (int64_t)page * 4);
-#pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                const uint32_t off = (t + m16) * RB + (c4 + 4 * i) * PB;
-                if constexpr (PB == 16) s.k[u][i] = bload16(rk, off);
-                else {
-                    const u32x2 w = bload8(rk, off);
-                    s.k[u][i] = u32x4{w[0], w[1], 0u, 0u};
-                }
-            }
-            s.ks[u] = __builtin_bit_cast(v4f, bload16(rks, (t + 4 * c4) * 4));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t off = (t + 4 * c4 + j) * RB + m16 * VB;
-                uint32_t* o = s.v[4 * u + j];
-                if constexpr (VB == 2) o[0] = bload2(rv, off);
-                else if constexpr (VB == 4) o[0] = bload4(rv, off);
-                else if constexpr (VB == 8) {
-                    const u32x2 w = bload8(rv, off);
-                    o[0] = w[0], o[1] = w[1];
-                } else {
-                    const u32x4 w = bload16(rv, off);
-                    o[0] = w[0], o[1] = w[1], o[2] = w[2], o[3] = w[3];
-                }
-            }
-            s.vs[u] = __builtin_bit_cast(v4f, bload16(rvs, (t + 4 * c4) * 4));
-        }
+    // the rows of this head from token t on in page p: a descriptor that ends with the page (p < 0: of nothing).
+    // The token's place is in its base: an offset beside the lane's would pass the range check.
+    auto rows_of = [&](const void* x, int t, int p, uint32_t row_bytes) __attribute__((always_inline)) {
+        const uint32_t at = (uint32_t)t & (uint32_t)(page - 1);
+        const int64_t row = (((int64_t)(p < 0 ? 0 : p) * a.heads + h) << a.shift) + at;
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(static_cast<const uint8_t*>(x) + row * row_bytes), (short)0,
+                                                 p < 0 ? 0 : (int)(((uint32_t)page - at) * row_bytes), 0x00020000);
     };
 
-    // this wave's first tile, and the queries while it comes
-    int tile = wave;
-    int t0 = lo + 32 * tile, p0 = page_of(t0), p1 = page_of(t0 + 16);
-    int np0 = page_of(t0 + 128), np1 = page_of(t0 + 144);    // of its next one
-    Stage cur;
-    load(cur, t0, p0, p1);
-    v8h qf[QT][NF];
-    float qscale;
-    {
-        constexpr uint32_t EL = QT == 2 ? 4 : 2;             // bytes of a query value
-        const rsrc_t rq = make_rsrc(static_cast<const uint8_t*>(a.q) + ((int64_t)b * a.ldq + (int64_t)h * a.group * a.D) * EL,
-                                    (int64_t)a.group * a.D * EL);
-        float x[NF][8], top = 0.0f;
+    // offsets of a lane in 16 tokens
+    const uint32_t ok = m16 * RB + c4 * PB, os = 16 * c4;
+    uint32_t ov[4];
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            const int d = (c4 + 4 * (f / FP)) * CC + 8 * (f % FP);
-            const uint32_t off = d < a.D ? (uint32_t)(g * a.D + d) * EL : kOOB;    // (heads past the group: zeros)
-            const u32x4 u = bload16(rq, off);
-            float y[8];
-            if constexpr (QT == 2) {
-                const v4f lo = __builtin_bit_cast(v4f, u), hi = __builtin_bit_cast(v4f, bload16(rq, off + 16));
+    for (int j = 0; j < 4; ++j) ov[j] = (4 * c4 + j) * RB + m16 * VB;
+    u32x4 kq[2][NS];
+    uint32_t vq[8][VW];
+    v4f ks[2], vs[2];
+    auto load_k = [&](int u, int t, int p) __attribute__((always_inline)) {
+        const rsrc_t rk = rows_of(a.kc, t, p, RB), rs = rows_of(a.ks, t, p, 4);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = lo[j], y[4 + j] = hi[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t v = u[j >> 1] >> (16 * (j & 1));
-                    y[j] = a.qdt == 1 ? h2f((uint16_t)v) : __builtin_bit_cast(float, v << 16);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[f][j] = y[row8_order<BITS>(j)];
-                top = fmaxf(top, __builtin_fabsf(y[j]));
+        for (int i = 0; i < NS; ++i) {
+            if constexpr (PB == 16) kq[u][i] = bload16(rk, ok + 4 * i * PB);
+            else {
+                const u32x2 w = bload8(rk, ok + 4 * i * PB);
+                kq[u][i] = u32x4{w[0], w[1], 0u, 0u};
             }
         }
+        ks[u] = __builtin_bit_cast(v4f, bload16(rs, os));
+    };
+    auto load_v = [&](int u, int t, int p) __attribute__((always_inline)) {
+        const rsrc_t rv = rows_of(a.vc, t, p, RB), rs = rows_of(a.vs, t, p, 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t* o = vq[4 * u + j];
+            if constexpr (VB == 2) o[0] = bload2(rv, ov[j]);
+            else if constexpr (VB == 4) o[0] = bload4(rv, ov[j]);
+            else if constexpr (VB == 8) {
+                const u32x2 w = bload8(rv, ov[j]);
+                o[0] = w[0], o[1] = w[1];
+            } else {
+                const u32x4 w = bload16(rv, ov[j]);
+                o[0] = w[0], o[1] = w[1], o[2] = w[2], o[3] = w[3];
+            }
+        }
+        vs[u] = __builtin_bit_cast(v4f, bload16(rs, os));
+    };
+
+    // this wave's first tile and the entries of its next one, and the queries while they come
+    int t0 = lo + 32 * wave;
+    int e0 = entry(t0), e1 = entry(t0 + 16), n0 = entry(t0 + 128), n1 = entry(t0 + 144);
+    int p0 = page_of(t0, e0), p1 = page_of(t0 + 16, e1);
+    load_k(0, t0, p0);
+    load_k(1, t0 + 16, p1);
+    load_v(0, t0, p0);
+    load_v(1, t0 + 16, p1);
+    v4i qd[3][NM];                                           // digits of 1, 256, 65536
+    float qscale;
+    {
+        constexpr uint32_t EL = F32 ? 4 : 2;                 // bytes of a query value
+        const rsrc_t rq = make_rsrc(static_cast<const uint8_t*>(a.q) + ((int64_t)b * a.ldq + (int64_t)h * a.group * a.D) * EL,
+                                    (int64_t)a.group * a.D * EL);
+        // 16 values to an MFMA step: int8 piece s is step s; an int4 piece of 32 codes is two,
+        // its even and its odd codes, one of 16 is its even and then its odd codes
+        constexpr int FP = CC / 8;
+        float x[NS][CC], top = 0.0f;
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int f = 0; f < FP; ++f) {
+                const int d = (c4 + 4 * s) * CC + 8 * f;
+                const uint32_t off = d < a.D ? (uint32_t)(g * a.D + d) * EL : kOOB;    // (heads past the group: zeros)
+                const u32x4 u = bload16(rq, off);
+                float* y = x[s] + 8 * f;
+                if constexpr (F32) {
+                    const v4f lo4 = __builtin_bit_cast(v4f, u), hi4 = __builtin_bit_cast(v4f, bload16(rq, off + 16));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] = lo4[j], y[4 + j] = hi4[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t v = u[j >> 1] >> (16 * (j & 1));
+                        y[j] = a.qdt == 1 ? h2f((uint16_t)v) : __builtin_bit_cast(float, v << 16);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(y[j]));
+            }
         top = fmaxf(top, __shfl_xor(top, 16, QA_WAVE));
         top = fmaxf(top, __shfl_xor(top, 32, QA_WAVE));
-        // times 2^e the head's largest is in [2^13, 2^14)
-        const int e = top > 0.0f && top < __builtin_inff() ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
-        qscale = __builtin_ldexpf(a.scale2, -e);
+        // times 2^e the head's largest is in [2^21, 2^22)
+        const int e = top > 0.0f && top < __builtin_inff() ? 22 - __builtin_amdgcn_frexp_expf(top) : 0;
+        qscale = __builtin_ldexpf(a.scale2, -e - (BITS == 8 ? 0 : 4));
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
+        for (int i = 0; i < NM; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float y = __builtin_ldexpf(x[f][j], e);
-                qf[0][f][j] = (_Float16)y;
-                if constexpr (QT == 2) qf[1][f][j] = (_Float16)(y - (float)qf[0][f][j]);
+            for (int w = 0; w < 4; ++w) {
+                uint32_t d0 = 0, d1 = 0, d2 = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // value at byte k of step i
+                    const int k = 4 * w + j;
+                    float y;
+                    if constexpr (BITS == 8) y = x[i][k];
+                    else if constexpr (CC == 32) y = x[i / 2][2 * k + (i & 1)];
+                    else y = x[i][k < 8 ? 2 * k : 2 * (k - 8) + 1];
+                    const int n = (int)__builtin_rintf(__builtin_ldexpf(y, e));
+                    const int m1 = (n + 128) >> 8, m2 = (m1 + 128) >> 8;    // what is left above each digit
+                    d0 |= ((uint32_t)n & 0xffu) << (8 * j);
+                    d1 |= ((uint32_t)m1 & 0xffu) << (8 * j);
+                    d2 |= ((uint32_t)m2 & 0xffu) << (8 * j);
+                }
+                qd[0][i][w] = (int)d0;
+                qd[1][i][w] = (int)d1;
+                qd[2][i][w] = (int)d2;
             }
     }
 
@@ -286,28 +292,44 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
     for (int i = 0; i < VN; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     float m = kLow, l = 0.0f, ex = -120.0f, r = 0.0f;        // r = 2^-ex, the factor of p s_v
 
-    while (tile < ntiles) {
-        const int nt = tile + 4;
-        const int n0 = lo + 32 * nt;
-        Stage nxt;
-        load(nxt, n0, np0, np1);
-        const int nnp0 = page_of(n0 + 128), nnp1 = page_of(n0 + 144);
+    while (t0 < hi) {
+        // the next tile's pages, the entries of the one after it
+        const int tn = t0 + 128;
+        const int np0 = page_of(tn, n0), np1 = page_of(tn + 16, n1);
+        n0 = entry(tn + 128);
+        n1 = entry(tn + 144);
 
-        v4f x[2], sv[2];
+        // scores as exact integers / 2^k, with their factors
+        v4f f[2], fs[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            v4f s = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            v4i s0 = v4i{0, 0, 0, 0}, s1 = s0, s2 = s0;
 #pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                const u32x4 w = cur.k[u][f / FP];
-                const v8h kf = BITS == 8 ? row8<BITS>(w[2 * (f % FP)], w[2 * (f % FP) + 1]) : row8<BITS>(w[f % FP], 0u);
-                s = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[0][f], s, 0, 0, 0);
-                if constexpr (QT == 2) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[QT - 1][f], s, 0, 0, 0);
+            for (int i = 0; i < NM; ++i) {
+                v4i kf;
+                if constexpr (BITS == 8) kf = __builtin_bit_cast(v4i, kq[u][i]);
+                else if constexpr (CC == 32) {
+                    const u32x4 w = kq[u][i / 2];
+                    kf = __builtin_bit_cast(v4i, (i & 1 ? w : w << 4) & 0xf0f0f0f0u);
+                } else {
+                    const u32x4 w = kq[u][i];
+                    kf = __builtin_bit_cast(v4i, u32x4{w[0] << 4, w[1] << 4, w[0], w[1]} & 0xf0f0f0f0u);
+                }
+                s0 = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf, qd[0][i], s0, 0, 0, 0);
+                s1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf, qd[1][i], s1, 0, 0, 0);
+                s2 = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf, qd[2][i], s2, 0, 0, 0);
             }
-            sv[u] = cur.vs[u];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[u][e] = s[e] * cur.ks[u][e] * qscale;
+            for (int e = 0; e < 4; ++e) {
+                // |s1| <= 256 * 128 * 127: 256 s1 + s0 fits
+                f[u][e] = __builtin_fmaf((float)s2[e], 65536.0f, (float)(s1[e] * 256 + s0[e]));
+                fs[u][e] = ks[u][e] * qscale;
+            }
         }
+        load_k(0, tn, np0);
+        load_k(1, tn + 16, np1);
+
+        v4f sv[2] = {vs[0], vs[1]};
         if (t0 < first || t0 + 32 > hi || p0 < 0 || p1 < 0) {    // tokens that are not seen
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -315,7 +337,8 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
                 for (int e = 0; e < 4; ++e) {
                     const int t = t0 + 16 * u + 4 * c4 + e;
                     const bool live = t >= first && t < hi && (u ? p1 : p0) >= 0;
-                    x[u][e] = live ? x[u][e] : -__builtin_inff();
+                    f[u][e] = live ? f[u][e] : -__builtin_inff();
+                    fs[u][e] = live ? fs[u][e] : 1.0f;
                     sv[u][e] = live ? sv[u][e] : 0.0f;
                 }
         }
@@ -325,30 +348,34 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    p[u][e] = __builtin_amdgcn_exp2f(x[u][e] - m);
+                    p[u][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(f[u][e], fs[u][e], -m));
                     w[u][e] = p[u][e] * sv[u][e] * r;
                 }
         };
         weigh();
-        const float xm = fmaxf(max4(x[0]), max4(x[1]));
-        if (__any(xm > m + 16.0f || fmaxf(max4(w[0]), max4(w[1])) > 16384.0f)) {
+        if (__any(fmaxf(max4(p[0]), max4(p[1])) > 65536.0f || fmaxf(max4(w[0]), max4(w[1])) > 16384.0f)) {
             // new references from this tile's maxima and the old ones
-            float tm = fmaxf(xm, __shfl_xor(xm, 16, QA_WAVE));
-            tm = fmaxf(tm, __shfl_xor(tm, 32, QA_WAVE));
-            const float mn = fmaxf(m, tm);
-            float wm = 0.0f;
+            float tm = -__builtin_inff(), wm = 0.0f;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) wm = fmaxf(wm, __builtin_amdgcn_exp2f(x[u][e] - mn) * sv[u][e]);
+                for (int e = 0; e < 4; ++e) tm = fmaxf(tm, f[u][e] * fs[u][e]);
+            tm = fmaxf(tm, __shfl_xor(tm, 16, QA_WAVE));
+            tm = fmaxf(tm, __shfl_xor(tm, 32, QA_WAVE));
+            const float mn = fmaxf(m, tm);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    wm = fmaxf(wm, __builtin_amdgcn_exp2f(__builtin_fmaf(f[u][e], fs[u][e], -mn)) * sv[u][e]);
             wm = fmaxf(wm, __shfl_xor(wm, 16, QA_WAVE));
             wm = fmaxf(wm, __shfl_xor(wm, 32, QA_WAVE));
             const float down = m - mn;
             const float en = fmaxf(-120.0f, fmaxf(__builtin_ceilf(ex + down), (float)__builtin_amdgcn_frexp_expf(wm)));
             l *= __builtin_amdgcn_exp2f(down);
-            const float f = __builtin_ldexpf(__builtin_amdgcn_exp2f(down), (int)fmaxf(ex - en, -300.0f));
+            const float z = __builtin_ldexpf(__builtin_amdgcn_exp2f(down), (int)fmaxf(ex - en, -300.0f));
 #pragma unroll
-            for (int i = 0; i < VN; ++i) acc[i] *= f;
+            for (int i = 0; i < VN; ++i) acc[i] *= z;
             m = mn;
             ex = en;
             r = __builtin_amdgcn_exp2f(-en);
@@ -373,7 +400,7 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
             for (int q = 0; q < VW; ++q) {
                 uint32_t y[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = cur.v[j][q] ^ 0x80808080u;
+                for (int j = 0; j < 8; ++j) y[j] = vq[j][q] ^ 0x80808080u;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t sel = 0x0c000c00u | (uint32_t)i | ((uint32_t)(4 + i) << 16);
@@ -389,7 +416,7 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
                 uint32_t y[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    y[j] = __builtin_amdgcn_perm(cur.v[2 * j + 1][q / 2], cur.v[2 * j][q / 2], sel) ^ 0x88888888u;
+                    y[j] = __builtin_amdgcn_perm(vq[2 * j + 1][q / 2], vq[2 * j][q / 2], sel) ^ 0x88888888u;
                 pv(4 * q, nib_pair0(y[0]), nib_pair0(y[1]), nib_pair0(y[2]), nib_pair0(y[3]));
                 pv(4 * q + 1, nib_pair1(y[0]), nib_pair1(y[1]), nib_pair1(y[2]), nib_pair1(y[3]));
 #pragma unroll
@@ -398,13 +425,11 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
                 pv(4 * q + 3, nib_pair1(y[0]), nib_pair1(y[1]), nib_pair1(y[2]), nib_pair1(y[3]));
             }
         }
-        tile = nt;
-        t0 = n0;
+        load_v(0, tn, np0);
+        load_v(1, tn + 16, np1);
+        t0 = tn;
         p0 = np0;
         p1 = np1;
-        np0 = nnp0;
-        np1 = nnp1;
-        cur = nxt;
     }
 
     // the block's waves: common references, then the sums of the accumulators
@@ -430,7 +455,7 @@ __global__ __launch_bounds__(256) void k_attn_decode(AttnArgs a) {
         for (int w = 0; w < 4; ++w) {
             const float f = __builtin_amdgcn_exp2f(st_m[w][threadIdx.x] - mg);
             lg += st_l[w][threadIdx.x] * f;
-            st_e[w][threadIdx.x] = __builtin_ldexpf(f, (int)st_e[w][threadIdx.x]);
+            st_e[w][threadIdx.x] = __builtin_ldexpf(f, (int)st_e[w][threadIdx.x] + 10);    // (values' codes came times 2^-10)
         }
         inv_l[threadIdx.x] = lg == 0.0f ? 0.0f : 1.0f / lg;
         if ((int)threadIdx.x < heads_here) {
@@ -515,8 +540,8 @@ Plan plan_of(int64_t B, int32_t H, int32_t heads, int64_t max_len, int32_t windo
 
 template <int BITS, int DP>
 hipError_t run_attn(const AttnArgs& a, int64_t blocks, hipStream_t st) {
-    if (a.qdt == 0) hipLaunchKernelGGL((k_attn_decode<BITS, DP, 2>), dim3((unsigned)blocks), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_attn_decode<BITS, DP, 1>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+    if (a.qdt == 0) hipLaunchKernelGGL((k_attn_decode<BITS, DP, true>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_attn_decode<BITS, DP, false>), dim3((unsigned)blocks), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 template <int BITS>
