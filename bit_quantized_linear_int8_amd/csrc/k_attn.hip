@@ -7,16 +7,19 @@
 // over the tokens t of a sequence (inside its window, on a page that the cache
 // has).  The heads that share a key head are the 16 columns of one MFMA tile.
 //
-// A wave takes 32 tokens at a time, from memory straight into MFMA operands:
-//   - keys are the rows of A of an int8 product: lane (m, c) holds 16-byte pieces
+// A wave takes 32 tokens at a time through stages of LDS of its own (no barrier in
+// the loop), filled by direct global -> LDS loads of whole lines, NST tiles ahead:
+//   - keys are the rows of A of an int8 product: lane (m, c) takes 16-byte pieces
 //     c, c + 4, ... of token m (and 16 + m), as they are (int4: the nibbles in the
 //     upper halves of bytes, 16 times the codes);
 //   - x comes out with four consecutive tokens of column g = lane % 16 in each
 //     lane, which is where p has to be as the operand B of the second product;
-//   - values are A of the second product, transposed: lane (m, c) holds the
+//   - values are A of the second product, transposed: lane (m, c) takes the
 //     16th part m of the D values of tokens 4 c + j and 16 + 4 c + j, and
 //     the codes of two tokens are put side by side in registers.
-// So nothing passes through LDS, and lanes exchange nothing inside the loop.
+// Lanes exchange nothing inside the loop.  (Keys straight into the operand's
+// registers have every lane of a load in a line of its own: 460 accesses of the L1
+// for a tile's 68 lines, which bounded the kernel at 4.4 TB/s.)
 //
 // Queries enter as whole numbers of 22 bits and a sign next to the head's largest
 // (what fp16 and bf16 hold of values down to 2^-11 and 2^-14 of it), in three
@@ -89,6 +92,14 @@ __device__ __forceinline__ uint32_t nib_pair1(uint32_t y) {
                                         v2h{(_Float16)-0.0078125, (_Float16)-0.0078125}));
 }
 
+// Query j of a 16-byte piece: fp32, fp16 or bf16.
+template <bool F32, bool F16>
+__device__ __forceinline__ float query(const u32x4& u, int j) {
+    if constexpr (F32) return __builtin_bit_cast(v4f, u)[j];
+    const uint32_t v = u[j >> 1] >> (16 * (j & 1));
+    return F16 ? h2f((uint16_t)v) : __builtin_bit_cast(float, v << 16);
+}
+
 // Four consecutive outputs of type dt at p[at].
 __device__ __forceinline__ void store_quad(void* p, int64_t at, int dt, v4f v) {
     if (dt == 0) {
@@ -113,6 +124,23 @@ __device__ __forceinline__ void span_of(const AttnArgs& a, int b, int& first, in
     from = first & ~31;
 }
 
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void glb_void;
+
+// Sixteen bytes from each lane's offset, and four from each lane's address, to LDS, lane after lane.
+__device__ __forceinline__ void load_lds16(rsrc_t r, uint32_t off, void* lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, 0, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(const void* p, void* lds) {
+    __builtin_amdgcn_global_load_lds((glb_void*)p, (lds_void*)lds, 4, 0, 0);
+}
+
+// s_waitcnt immediate waiting for vmcnt <= n only (gfx9 encoding)
+constexpr int vmcnt_only(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
+
+// Stages of LDS for a wave, by the bits of a row.
+constexpr int stages(int bits) { return bits >= 1024 ? 2 : 3; }
+
 __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
 
 }  // namespace
@@ -120,7 +148,7 @@ __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), f
 // DP: D rounded up to 64, 128 or 256 (what lies behind D meets queries of 0, or is
 // not stored).  F32: fp32 queries.
 template <int BITS, int DP, bool F32>
-__global__ __launch_bounds__(256, DP == 256 ? 1 : 3) void k_attn_decode(AttnArgs a) {
+__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs a) {
     constexpr int CC = BITS == 8 || DP == 64 ? 16 : 32;      // codes of a lane's piece of a key
     constexpr int NS = DP / (4 * CC);                        // pieces of a lane
     constexpr int PB = CC * BITS / 8;                        // bytes of a piece
@@ -128,7 +156,13 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 3) void k_attn_decode(AttnArgs
     constexpr int VN = DP / 16;                              // values of a lane per token
     constexpr int VB = VN * BITS / 8;                        // their bytes
     constexpr int VW = VB < 4 ? 1 : VB / 4;                  // their words
-    __shared__ v4f red[4][16][DP / 4 + 1];                   // (one more: the 16 rows start at different banks)
+    constexpr int DPB = DP * BITS / 8, NCH = DPB / 16;       // a row in LDS, its chunks
+    constexpr int INS = 16 * DPB < 1024 ? 1 : 16 * DPB / 1024;    // loads of 16 rows
+    constexpr int HALF = INS * 1024;
+    constexpr int SB = 4 * HALF + 256, NST = stages(BITS * DP);
+    constexpr int RED = 4 * 16 * (DP / 4 + 1) * 16;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[4 * NST * SB > RED ? 4 * NST * SB : RED];
+    auto swz = [](int r) { return (NCH <= 8 ? r / (8 / (NCH <= 8 ? NCH : 8)) : r) & (NCH - 1); };
     __shared__ float st_m[4][16], st_l[4][16], st_e[4][16], inv_l[16];
 
     const int lane = threadIdx.x & 63, wave = wave_id();
@@ -162,69 +196,61 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 3) void k_attn_decode(AttnArgs
     const int32_t* tab = a.table + (int64_t)b * a.ldt;
     const int page = 1 << a.shift;
     const uint32_t RB = (uint32_t)a.D * BITS / 8;            // bytes of a row
-    // the page of the 16 tokens from t: its index, or -1 (past the end, or not one of the cache's)
-    auto entry = [&](int t) __attribute__((always_inline)) {
-        return tab[(t < a.max_len ? t : a.max_len - 1) >> a.shift];
+    // Pages of the wave's tiles: lane 2 i + u of `ent` holds the table's entry for 16 tokens u of tile i of 32.
+    auto entries = [&](int t) __attribute__((always_inline)) {
+        const int64_t at = (int64_t)t + 128 * (lane >> 1) + 16 * (lane & 1);
+        return tab[(int)(at < a.max_len ? at : a.max_len - 1) >> a.shift];
     };
-    auto page_of = [&](int t, int e) __attribute__((always_inline)) {
-        const int p = __builtin_amdgcn_readfirstlane(e);
+    // the page of the 16 tokens from t, or -1 (past the end, or not one of the cache's)
+    auto page_of = [&](int t, int p) __attribute__((always_inline)) {
         return t < hi && (uint32_t)p < (uint32_t)a.pages ? p : -1;
     };
-    // the rows of this head from token t on in page p: a descriptor that ends with the page (p < 0: of nothing).
-    // The token's place is in its base: an offset beside the lane's would pass the range check.
-    auto rows_of = [&](const void* x, int t, int p, uint32_t row_bytes) __attribute__((always_inline)) {
+    // the rows of this head from token t on in page p: a descriptor that ends with the page (p < 0: of nothing)
+    auto rows_of = [&](const uint8_t* x, int t, int p) __attribute__((always_inline)) {
         const uint32_t at = (uint32_t)t & (uint32_t)(page - 1);
         const int64_t row = (((int64_t)(p < 0 ? 0 : p) * a.heads + h) << a.shift) + at;
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(static_cast<const uint8_t*>(x) + row * row_bytes), (short)0,
-                                                 p < 0 ? 0 : (int)(((uint32_t)page - at) * row_bytes), 0x00020000);
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(x + row * RB), (short)0,
+                                                 p < 0 ? 0 : (int)(((uint32_t)page - at) * RB), 0x00020000);
     };
 
-    // offsets of a lane in 16 tokens
-    const uint32_t ok = m16 * RB + c4 * PB, os = 16 * c4;
-    uint32_t ov[4];
+    // A stage: keys and values of two times 16 tokens, rows of DPB bytes whose 16-byte chunk c is at c ^ swz(row), so
+    // that reads of 16 rows meet all banks; behind them 32 scales of keys and 32 of values.
+    uint8_t* const mine = smem + wave * NST * SB;
+    uint32_t src[INS];                                       // a lane's part of a load of 16 rows
 #pragma unroll
-    for (int j = 0; j < 4; ++j) ov[j] = (4 * c4 + j) * RB + m16 * VB;
-    u32x4 kq[2][NS];
-    uint32_t vq[8][VW];
-    v4f ks[2], vs[2];
-    auto load_k = [&](int u, int t, int p) __attribute__((always_inline)) {
-        const rsrc_t rk = rows_of(a.kc, t, p, RB), rs = rows_of(a.ks, t, p, 4);
+    for (int n = 0; n < INS; ++n) {
+        const int P = n * 64 + lane, rr = P / NCH, c = (P % NCH) ^ swz(rr);
+        src[n] = rr < 16 && (uint32_t)(16 * c) < RB ? (uint32_t)rr * RB + 16 * c : kOOB;
+    }
+    auto fill = [&](int st, int t, int q0, int q1) __attribute__((always_inline)) {
+        uint8_t* const to = mine + st * SB;
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            if constexpr (PB == 16) kq[u][i] = bload16(rk, ok + 4 * i * PB);
-            else {
-                const u32x2 w = bload8(rk, ok + 4 * i * PB);
-                kq[u][i] = u32x4{w[0], w[1], 0u, 0u};
+        for (int u = 0; u < 2; ++u) {
+            const rsrc_t rk = rows_of(a.kc, t + 16 * u, u ? q1 : q0), rv = rows_of(a.vc, t + 16 * u, u ? q1 : q0);
+#pragma unroll
+            for (int n = 0; n < INS; ++n) {
+                load_lds16(rk, src[n], to + u * HALF + n * 1024);
+                load_lds16(rv, src[n], to + (2 + u) * HALF + n * 1024);
             }
         }
-        ks[u] = __builtin_bit_cast(v4f, bload16(rs, os));
+        // scales: 16 tokens of u to 16 lanes, keys' and then values' (of page 0 where there is none: not looked at)
+        const int u = (lane >> 4) & 1, p = u ? q1 : q0;
+        const uint32_t at = (uint32_t)(t + 16 * u) & (uint32_t)(page - 1);
+        const float* sc = (lane < 32 ? a.ks : a.vs) + ((((int64_t)(p < 0 ? 0 : p) * a.heads + h) << a.shift) + at + m16);
+        load_lds4(sc, to + 4 * HALF);
     };
-    auto load_v = [&](int u, int t, int p) __attribute__((always_inline)) {
-        const rsrc_t rv = rows_of(a.vc, t, p, RB), rs = rows_of(a.vs, t, p, 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t* o = vq[4 * u + j];
-            if constexpr (VB == 2) o[0] = bload2(rv, ov[j]);
-            else if constexpr (VB == 4) o[0] = bload4(rv, ov[j]);
-            else if constexpr (VB == 8) {
-                const u32x2 w = bload8(rv, ov[j]);
-                o[0] = w[0], o[1] = w[1];
-            } else {
-                const u32x4 w = bload16(rv, ov[j]);
-                o[0] = w[0], o[1] = w[1], o[2] = w[2], o[3] = w[3];
-            }
-        }
-        vs[u] = __builtin_bit_cast(v4f, bload16(rs, os));
-    };
+    constexpr int PER = 4 * INS + 1;                         // loads of a stage, always as many
 
-    // this wave's first tile and the entries of its next one, and the queries while they come
-    int t0 = lo + 32 * wave;
-    int e0 = entry(t0), e1 = entry(t0 + 16), n0 = entry(t0 + 128), n1 = entry(t0 + 144);
-    int p0 = page_of(t0, e0), p1 = page_of(t0 + 16, e1);
-    load_k(0, t0, p0);
-    load_k(1, t0 + 16, p1);
-    load_v(0, t0, p0);
-    load_v(1, t0 + 16, p1);
+    // the wave's first tiles, and the queries while they come
+    int t0 = lo + 32 * wave, it = 0;
+    int ent = entries(t0), ent2 = entries(t0 + 32 * 128);
+    int p0[NST], p1[NST];
+#pragma unroll
+    for (int s = 0; s < NST; ++s) {
+        p0[s] = page_of(t0 + 128 * s, __builtin_amdgcn_readlane(ent, 2 * s));
+        p1[s] = page_of(t0 + 128 * s + 16, __builtin_amdgcn_readlane(ent, 2 * s + 1));
+        fill(s, t0 + 128 * s, p0[s], p1[s]);
+    }
     v4i qd[3][NM];                                           // digits of 1, 256, 65536
     float qscale;
     {
@@ -233,30 +259,31 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 3) void k_attn_decode(AttnArgs
                                     (int64_t)a.group * a.D * EL);
         // 16 values to an MFMA step: int8 piece s is step s; an int4 piece of 32 codes is two,
         // its even and its odd codes, one of 16 is its even and then its odd codes
-        constexpr int FP = CC / 8;
         float x[NS][CC], top = 0.0f;
+        constexpr int V = 16 / EL;                           // values of a load
+        u32x4 raw[NS][CC / V];
 #pragma unroll
         for (int s = 0; s < NS; ++s)
 #pragma unroll
-            for (int f = 0; f < FP; ++f) {
-                const int d = (c4 + 4 * s) * CC + 8 * f;
-                const uint32_t off = d < a.D ? (uint32_t)(g * a.D + d) * EL : kOOB;    // (heads past the group: zeros)
-                const u32x4 u = bload16(rq, off);
-                float* y = x[s] + 8 * f;
-                if constexpr (F32) {
-                    const v4f lo4 = __builtin_bit_cast(v4f, u), hi4 = __builtin_bit_cast(v4f, bload16(rq, off + 16));
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] = lo4[j], y[4 + j] = hi4[j];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t v = u[j >> 1] >> (16 * (j & 1));
-                        y[j] = a.qdt == 1 ? h2f((uint16_t)v) : __builtin_bit_cast(float, v << 16);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(y[j]));
+            for (int f = 0; f < CC / V; ++f) {
+                const int d = (c4 + 4 * s) * CC + V * f;
+                raw[s][f] = bload16(rq, d < a.D ? (uint32_t)(g * a.D + d) * EL : kOOB);    // (heads past the group: zeros)
             }
+        if (a.qdt == 1) {
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int k = 0; k < CC; ++k) x[s][k] = query<F32, true>(raw[s][k / V], k % V);
+        } else {
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int k = 0; k < CC; ++k) x[s][k] = query<F32, false>(raw[s][k / V], k % V);
+        }
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int k = 0; k < CC; ++k) top = fmaxf(top, __builtin_fabsf(x[s][k]));
         top = fmaxf(top, __shfl_xor(top, 16, QA_WAVE));
         top = fmaxf(top, __shfl_xor(top, 32, QA_WAVE));
         // times 2^e the head's largest is in [2^21, 2^22)
@@ -292,12 +319,71 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 3) void k_attn_decode(AttnArgs
     for (int i = 0; i < VN; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     float m = kLow, l = 0.0f, ex = -120.0f, r = 0.0f;        // r = 2^-ex, the factor of p s_v
 
+    // a lane's places in a stage
+    uint32_t ak[NS], av[4];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int byte = (c4 + 4 * i) * PB;
+        ak[i] = m16 * DPB + (((byte >> 4) ^ swz(m16)) << 4) + (byte & 15);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int rr = 4 * c4 + j, byte = m16 * VB;
+        av[j] = 2 * HALF + rr * DPB + (((byte >> 4) ^ swz(rr)) << 4) + (byte & 15);
+    }
+    int st = 0;
     while (t0 < hi) {
-        // the next tile's pages, the entries of the one after it
-        const int tn = t0 + 128;
-        const int np0 = page_of(tn, n0), np1 = page_of(tn + 16, n1);
-        n0 = entry(tn + 128);
-        n1 = entry(tn + 144);
+        // this tile's stage into registers
+        __builtin_amdgcn_s_waitcnt(vmcnt_only(PER * (NST - 1)));
+        asm volatile("" ::: "memory");
+        const uint8_t* const from_ = mine + st * SB;
+        u32x4 kq[2][NS];
+        uint32_t vq[8][VW];
+        v4f ks[2], vs[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const uint8_t* q = from_ + u * HALF + ak[i];
+                if constexpr (PB == 16) kq[u][i] = *reinterpret_cast<const u32x4*>(q);
+                else {
+                    const u32x2 w = *reinterpret_cast<const u32x2*>(q);
+                    kq[u][i] = u32x4{w[0], w[1], 0u, 0u};
+                }
+            }
+            ks[u] = *reinterpret_cast<const v4f*>(from_ + 4 * HALF + 64 * u + 16 * c4);
+            vs[u] = *reinterpret_cast<const v4f*>(from_ + 4 * HALF + 128 + 64 * u + 16 * c4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint8_t* q = from_ + u * HALF + av[j];
+                uint32_t* o = vq[4 * u + j];
+                if constexpr (VB == 2) o[0] = *reinterpret_cast<const uint16_t*>(q);
+                else if constexpr (VB == 4) o[0] = *reinterpret_cast<const uint32_t*>(q);
+                else if constexpr (VB == 8) {
+                    const u32x2 w = *reinterpret_cast<const u32x2*>(q);
+                    o[0] = w[0], o[1] = w[1];
+                } else {
+                    const u32x4 w = *reinterpret_cast<const u32x4*>(q);
+                    o[0] = w[0], o[1] = w[1], o[2] = w[2], o[3] = w[3];
+                }
+            }
+        }
+        // and the stage, once it is read, for the tile NST further on
+        __builtin_amdgcn_s_waitcnt(0xC07F);                  // lgkmcnt(0)
+        asm volatile("" ::: "memory");
+        const int q0 = p0[0], q1 = p1[0];                    // this tile's pages
+        {
+            const int at = it + NST, tn = t0 + 128 * NST;
+            if ((at & 31) == 0) {                            // the next 32 tiles' entries
+                ent = ent2;
+                ent2 = entries(tn + 32 * 128);
+            }
+#pragma unroll
+            for (int s = 0; s + 1 < NST; ++s) p0[s] = p0[s + 1], p1[s] = p1[s + 1];
+            p0[NST - 1] = page_of(tn, __builtin_amdgcn_readlane(ent, 2 * (at & 31)));
+            p1[NST - 1] = page_of(tn + 16, __builtin_amdgcn_readlane(ent, 2 * (at & 31) + 1));
+            fill(st, tn, p0[NST - 1], p1[NST - 1]);
+        }
 
         // scores as exact integers / 2^k, with their factors
         v4f f[2], fs[2];
@@ -326,17 +412,15 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 3) void k_attn_decode(AttnArgs
                 fs[u][e] = ks[u][e] * qscale;
             }
         }
-        load_k(0, tn, np0);
-        load_k(1, tn + 16, np1);
 
         v4f sv[2] = {vs[0], vs[1]};
-        if (t0 < first || t0 + 32 > hi || p0 < 0 || p1 < 0) {    // tokens that are not seen
+        if (t0 < first || t0 + 32 > hi || q0 < 0 || q1 < 0) {    // tokens that are not seen
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = t0 + 16 * u + 4 * c4 + e;
-                    const bool live = t >= first && t < hi && (u ? p1 : p0) >= 0;
+                    const bool live = t >= first && t < hi && (u ? q1 : q0) >= 0;
                     f[u][e] = live ? f[u][e] : -__builtin_inff();
                     fs[u][e] = live ? fs[u][e] : 1.0f;
                     sv[u][e] = live ? sv[u][e] : 0.0f;
@@ -425,12 +509,12 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 3) void k_attn_decode(AttnArgs
                 pv(4 * q + 3, nib_pair1(y[0]), nib_pair1(y[1]), nib_pair1(y[2]), nib_pair1(y[3]));
             }
         }
-        load_v(0, tn, np0);
-        load_v(1, tn + 16, np1);
-        t0 = tn;
-        p0 = np0;
-        p1 = np1;
+        t0 += 128;
+        ++it;
+        st = st + 1 == NST ? 0 : st + 1;
     }
+    __builtin_amdgcn_s_waitcnt(vmcnt_only(0));               // no load may land in what the waves share below
+    __syncthreads();
 
     // the block's waves: common references, then the sums of the accumulators
     l += __shfl_xor(l, 16, QA_WAVE);
@@ -440,12 +524,13 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 3) void k_attn_decode(AttnArgs
         st_l[wave][m16] = l;
         st_e[wave][m16] = ex;
     }
-    // head m16, values VN (4 c4 + e) + i
+    // head m16, values VN (4 c4 + e) + i; rows one piece longer, so that 16 of them start at different banks
+    v4f* const red = reinterpret_cast<v4f*>(smem);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int i = 0; i < VN / 4; ++i)
-            red[wave][m16][VN / 4 * (4 * c4 + e) + i] = v4f{acc[4 * i][e], acc[4 * i + 1][e], acc[4 * i + 2][e], acc[4 * i + 3][e]};
+            red[(wave * 16 + m16) * (DP / 4 + 1) + VN / 4 * (4 * c4 + e) + i] = v4f{acc[4 * i][e], acc[4 * i + 1][e], acc[4 * i + 2][e], acc[4 * i + 3][e]};
     __syncthreads();
     if (threadIdx.x < 16) {
         float mg = kLow, lg = 0.0f;
@@ -468,9 +553,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 3) void k_attn_decode(AttnArgs
     const int L = a.D / 4;
     for (int i = threadIdx.x; i < heads_here * L; i += 256) {
         const int r = i / L, d = i - r * L;
-        v4f o = red[0][r][d] * st_e[0][r];
+        v4f o = red[r * (DP / 4 + 1) + d] * st_e[0][r];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) o += red[w][r][d] * st_e[w][r];
+        for (int w = 1; w < 4; ++w) o += red[(w * 16 + r) * (DP / 4 + 1) + d] * st_e[w][r];
         o *= inv_l[r];
         if (a.splits > 1) *reinterpret_cast<v4f*>(a.part + ((row0 + r) * a.splits + split) * a.D + 4 * d) = o;
         else store_quad(a.out, (row0 + r) * a.D + 4 * d, a.dt, o);
@@ -570,7 +655,7 @@ hipError_t launch_attn_decode(const void* q, int64_t ldq, int q_dtype, int64_t B
     a.D = c.D; a.shift = c.shift; a.pages = (int32_t)c.pages;
     const int64_t most = width << c.shift;
     const Plan p = plan_of(B, H, c.heads, max_len, window);
-    a.max_len = (int32_t)(max_len < most ? max_len : most);
+    a.max_len = (int32_t)(c.pages == 0 ? 0 : max_len < most ? max_len : most);
     a.window = window; a.chunk = p.chunk; a.splits = p.splits;
     a.scale2 = scale * 1.44269504088896340736f;
     a.out = out; a.dt = out_dtype; a.lse = lse;
