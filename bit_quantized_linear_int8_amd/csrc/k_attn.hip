@@ -37,8 +37,12 @@
 // they taken anew, with the lanes' exchange that this needs; 2^16 leaves the sums
 // far inside fp32's range.
 //
-// The four waves of a block take tiles in turn and are joined through LDS; a
-// sequence is split over blocks in equal chunks, joined by k_attn_join.
+// The four waves of a block take tiles in turn and are joined through LDS.  Where
+// there are few sequences and heads, the work of all of them, in units of 128 tokens
+// of a head, is one line that the blocks that fit the card share evenly, whatever the
+// lengths are (a block finds its place by a sum over them); a head that reaches over
+// several blocks is joined by k_attn_join.  (Equal chunks of each sequence leave
+// blocks of unequal size: half the card's waves were idle with ragged lengths.)
 #include "qa_device.hpp"
 #include "qa_launch.hpp"
 
@@ -61,13 +65,14 @@ struct AttnArgs {
     int32_t H, heads, group, gtiles, D, shift, pages, qdt;
     int32_t max_len;           // lengths past it (or past the table) count as it
     int32_t window;            // 0: none
-    int32_t chunk, splits;
+    int32_t B, share;          // parts that the work of a tile of heads is shared in; 0: a block to each sequence and tile
     float scale2;              // scale log2(e)
     void* out;                 // [B][H][D]
     int32_t dt;
     float* lse;                // [B][H] or nullptr
-    float* part;               // [B][H][splits][D] (splits > 1)
-    float* plse;               // [B][H][splits], base 2
+    float* part;               // parts of sequences, [(share + B) heads gtiles][16][D]
+    float* plse;               // and their log-sum-exp, base 2, [..][16]
+    int32_t* before;           // [B + 1] units of all the sequences before one
 };
 
 constexpr float kLow = -3.0e38f;           // the reference before any token
@@ -90,6 +95,25 @@ __device__ __forceinline__ uint32_t nib_pair0(uint32_t y) {
 __device__ __forceinline__ uint32_t nib_pair1(uint32_t y) {
     return up(__builtin_elementwise_fma(pk(y & 0x00f000f0u), v2h{(_Float16)1024, (_Float16)1024},
                                         v2h{(_Float16)-0.0078125, (_Float16)-0.0078125}));
+}
+
+// w less the fp16 number in the low (high) half of h, in one instruction (the compiler makes two).
+__device__ __forceinline__ float less_low(float w, uint32_t h) {
+    float r;
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r) : "v"(h), "v"(w));
+    return r;
+}
+__device__ __forceinline__ float less_high(float w, uint32_t h) {
+    float r;
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(h), "v"(w));
+    return r;
+}
+
+// Byte K of four words, side by side.
+template <int K>
+__device__ __forceinline__ uint32_t bytes4(const uint32_t (&n)[4]) {
+    constexpr uint32_t two = 0x0c0c0000u | (uint32_t)K | ((uint32_t)(4 + K) << 8);
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(n[3], n[2], two), __builtin_amdgcn_perm(n[1], n[0], two), 0x05040100u);
 }
 
 // Query j of a 16-byte piece: fp32, fp16 or bf16.
@@ -123,6 +147,9 @@ __device__ __forceinline__ void span_of(const AttnArgs& a, int b, int& first, in
     first = a.window > 0 && end > a.window ? end - a.window : 0;
     from = first & ~31;
 }
+constexpr int kUnit = 128;
+// Units of a sequence per head.
+__device__ __forceinline__ int units_of(int end, int from) { return (end - from + kUnit - 1) / kUnit; }
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef const __attribute__((address_space(1))) void glb_void;
@@ -148,7 +175,7 @@ __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), f
 // DP: D rounded up to 64, 128 or 256 (what lies behind D meets queries of 0, or is
 // not stored).  F32: fp32 queries.
 template <int BITS, int DP, bool F32>
-__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs a) {
+__global__ __launch_bounds__(256, DP == 256 ? 1 : stages(BITS * DP)) void k_attn_decode(AttnArgs a) {
     constexpr int CC = BITS == 8 || DP == 64 ? 16 : 32;      // codes of a lane's piece of a key
     constexpr int NS = DP / (4 * CC);                        // pieces of a lane
     constexpr int PB = CC * BITS / 8;                        // bytes of a piece
@@ -164,34 +191,96 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
     __shared__ __attribute__((aligned(16))) uint8_t smem[4 * NST * SB > RED ? 4 * NST * SB : RED];
     auto swz = [](int r) { return (NCH <= 8 ? r / (8 / (NCH <= 8 ? NCH : 8)) : r) & (NCH - 1); };
     __shared__ float st_m[4][16], st_l[4][16], st_e[4][16], inv_l[16];
+    __shared__ int plan[6];
 
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int m16 = lane & 15, c4 = lane >> 4;
-    uint32_t id = blockIdx.x;
-    const int gt = id % (uint32_t)a.gtiles;
-    id /= (uint32_t)a.gtiles;
-    const int h = id % (uint32_t)a.heads;
-    id /= (uint32_t)a.heads;
-    const int split = id % (uint32_t)a.splits;
-    const int b = id / (uint32_t)a.splits;
-    int first, end, from;
-    span_of(a, b, first, end, from);
-    const int64_t lo64 = (int64_t)from + (int64_t)split * a.chunk;
-    const int g = gt * 16 + m16;                             // the lane's head within the group
-    const int heads_here = a.group - gt * 16 < 16 ? a.group - gt * 16 : 16;
-    const int64_t row0 = (int64_t)b * a.H + h * a.group + gt * 16;    // the block's first row of the output
-    if (lo64 >= end) {                                       // nothing in this chunk
-        if ((int)threadIdx.x < heads_here) {
-            if (a.splits > 1) a.plse[(row0 + threadIdx.x) * a.splits + split] = -__builtin_inff();
-            else if (a.lse) a.lse[row0 + threadIdx.x] = -__builtin_inff();
+    const int HG = a.heads * a.gtiles;                       // tiles of heads of a sequence
+    int b = 0, hg = 0, k0 = 0, left = 0;                     // the next unit's sequence, tile, place; units to do
+    if (a.share) {
+        // sums of the units over the sequences, four to a thread, and where the block's share begins
+        int n[4], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = 4 * threadIdx.x + j;
+            int first, end, from;
+            n[j] = 0;
+            if (i < a.B) {
+                span_of(a, i, first, end, from);
+                n[j] = units_of(end, from);
+            }
+            sum += n[j];
         }
-        if (a.splits == 1)
+        int upto = sum;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(upto, o, QA_WAVE);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 63) plan[wave] = upto;
+        __syncthreads();
+        int total = 0, pre = upto - sum;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w < wave) pre += plan[w];
+            total += plan[w];
+        }
+        const int share = total < a.share ? total : a.share;
+        const int part = blockIdx.x / (uint32_t)HG;
+        hg = blockIdx.x - (uint32_t)part * HG;
+        if (blockIdx.x == 0)
+#pragma unroll
+            for (int j = 0, at = pre; j < 4; ++j) {
+                const int i = 4 * threadIdx.x + j;
+                if (i < a.B) a.before[i] = at;
+                at += n[j];
+                if (i == a.B - 1) a.before[a.B] = at;
+            }
+        if (part >= share) return;
+        const int u0 = (int)((int64_t)part * total / share), u1 = (int)((int64_t)(part + 1) * total / share);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (pre <= u0 && u0 < pre + n[j]) plan[4] = 4 * threadIdx.x + j, plan[5] = u0 - pre;
+            pre += n[j];
+        }
+        __syncthreads();
+        b = __builtin_amdgcn_readfirstlane(plan[4]);
+        k0 = __builtin_amdgcn_readfirstlane(plan[5]);
+        left = u1 - u0;
+    } else {
+        b = blockIdx.x / (uint32_t)HG;
+        hg = blockIdx.x - (uint32_t)b * HG;
+        int first, end, from;
+        span_of(a, b, first, end, from);
+        left = units_of(end, from);
+        if (left == 0) {                                     // no token to see
+            const int h = hg / a.gtiles, gt = hg - h * a.gtiles;
+            const int heads_here = a.group - gt * 16 < 16 ? a.group - gt * 16 : 16;
+            const int64_t row0 = (int64_t)b * a.H + h * a.group + gt * 16;
+            if ((int)threadIdx.x < heads_here && a.lse) a.lse[row0 + threadIdx.x] = -__builtin_inff();
             for (int i = threadIdx.x; i < heads_here * a.D / 4; i += 256)
                 store_quad(a.out, row0 * a.D + 4 * i, a.dt, v4f{0.0f, 0.0f, 0.0f, 0.0f});
-        return;
+            return;
+        }
     }
-    const int lo = (int)lo64;
-    const int hi = end - lo < a.chunk ? end : lo + a.chunk;
+
+    while (left > 0) {
+    int first, end, from;
+    span_of(a, b, first, end, from);
+    const int n1 = units_of(end, from);
+    if (n1 == 0) {                                           // (its rows are written by the join)
+        ++b;
+        continue;
+    }
+    const int k1 = n1 - k0 < left ? n1 : k0 + left;
+    const bool whole = k0 == 0 && k1 == n1;
+    const int64_t slot = (int64_t)b * HG + blockIdx.x;       // of a part: grows with the sequence and with the block's share
+    const int h = hg / a.gtiles, gt = hg - h * a.gtiles;
+    const int g = gt * 16 + m16;                             // the lane's head within the group
+    const int heads_here = a.group - gt * 16 < 16 ? a.group - gt * 16 : 16;
+    const int64_t row0 = (int64_t)b * a.H + h * a.group + gt * 16;    // the first row of the output
+    const int lo = from + k0 * kUnit;
+    const int hi = end - from <= k1 * kUnit ? end : from + k1 * kUnit;
 
     const int32_t* tab = a.table + (int64_t)b * a.ldt;
     const int page = 1 << a.shift;
@@ -222,6 +311,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
         const int P = n * 64 + lane, rr = P / NCH, c = (P % NCH) ^ swz(rr);
         src[n] = rr < 16 && (uint32_t)(16 * c) < RB ? (uint32_t)rr * RB + 16 * c : kOOB;
     }
+    const float* const scales_at = (lane < 32 ? a.ks : a.vs) + (((int64_t)h << a.shift) + m16);
     auto fill = [&](int st, int t, int q0, int q1) __attribute__((always_inline)) {
         uint8_t* const to = mine + st * SB;
 #pragma unroll
@@ -234,10 +324,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
             }
         }
         // scales: 16 tokens of u to 16 lanes, keys' and then values' (of page 0 where there is none: not looked at)
-        const int u = (lane >> 4) & 1, p = u ? q1 : q0;
-        const uint32_t at = (uint32_t)(t + 16 * u) & (uint32_t)(page - 1);
-        const float* sc = (lane < 32 ? a.ks : a.vs) + ((((int64_t)(p < 0 ? 0 : p) * a.heads + h) << a.shift) + at + m16);
-        load_lds4(sc, to + 4 * HALF);
+        const int64_t r0 = (((int64_t)(q0 < 0 ? 0 : q0) * a.heads) << a.shift) + ((uint32_t)t & (uint32_t)(page - 1));
+        const int64_t r1 = (((int64_t)(q1 < 0 ? 0 : q1) * a.heads) << a.shift) + ((uint32_t)(t + 16) & (uint32_t)(page - 1));
+        load_lds4(scales_at + (lane & 16 ? r1 : r0), to + 4 * HALF);
     };
     constexpr int PER = 4 * INS + 1;                         // loads of a stage, always as many
 
@@ -289,11 +378,14 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
         // times 2^e the head's largest is in [2^21, 2^22)
         const int e = top > 0.0f && top < __builtin_inff() ? 22 - __builtin_amdgcn_frexp_expf(top) : 0;
         qscale = __builtin_ldexpf(a.scale2, -e - (BITS == 8 ? 0 : 4));
+        const float f1 = __builtin_ldexpf(1.0f, e / 2), f2 = __builtin_ldexpf(1.0f, e - e / 2);
 #pragma unroll
         for (int i = 0; i < NM; ++i)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                uint32_t d0 = 0, d1 = 0, d2 = 0;
+                // Beside 3 2^22 the whole number is in the low bits of the sum; a digit is a byte of it, or of
+                // it with what carries into the next digit: n, n + 128, n + 128 + 2^15.
+                uint32_t n[4], n1[4], n2[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     // value at byte k of step i
@@ -302,15 +394,13 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
                     if constexpr (BITS == 8) y = x[i][k];
                     else if constexpr (CC == 32) y = x[i / 2][2 * k + (i & 1)];
                     else y = x[i][k < 8 ? 2 * k : 2 * (k - 8) + 1];
-                    const int n = (int)__builtin_rintf(__builtin_ldexpf(y, e));
-                    const int m1 = (n + 128) >> 8, m2 = (m1 + 128) >> 8;    // what is left above each digit
-                    d0 |= ((uint32_t)n & 0xffu) << (8 * j);
-                    d1 |= ((uint32_t)m1 & 0xffu) << (8 * j);
-                    d2 |= ((uint32_t)m2 & 0xffu) << (8 * j);
+                    n[j] = __builtin_bit_cast(uint32_t, __builtin_fmaf(y * f1, f2, 12582912.0f));
+                    n1[j] = n[j] + (128u - 0x4b400000u);
+                    n2[j] = n1[j] + 0x8000u;
                 }
-                qd[0][i][w] = (int)d0;
-                qd[1][i][w] = (int)d1;
-                qd[2][i][w] = (int)d2;
+                qd[0][i][w] = (int)bytes4<0>(n);
+                qd[1][i][w] = (int)bytes4<1>(n1);
+                qd[2][i][w] = (int)bytes4<2>(n2);
             }
     }
 
@@ -465,15 +555,18 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
             r = __builtin_amdgcn_exp2f(-en);
             weigh();
         }
-        v8h ph, pl;
+        u32x4 hi4, lo4;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                l += p[u][e];
-                ph[4 * u + e] = (_Float16)w[u][e];
-                pl[4 * u + e] = (_Float16)(w[u][e] - (float)ph[4 * u + e]);
+            for (int e = 0; e < 2; ++e) {
+                const float w0 = w[u][2 * e], w1 = w[u][2 * e + 1];
+                l += p[u][2 * e] + p[u][2 * e + 1];
+                const uint32_t both = up(v2h{(_Float16)w0, (_Float16)w1});
+                hi4[2 * u + e] = both;
+                lo4[2 * u + e] = up(v2h{(_Float16)less_low(w0, both), (_Float16)less_high(w1, both)});
             }
+        const v8h ph = __builtin_bit_cast(v8h, hi4), pl = __builtin_bit_cast(v8h, lo4);
         auto pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) __attribute__((always_inline)) {
             const v8h vf = __builtin_bit_cast(v8h, u32x4{a0, a1, a2, a3});
             acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, ph, acc[i], 0, 0, 0);
@@ -545,7 +638,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
         inv_l[threadIdx.x] = lg == 0.0f ? 0.0f : 1.0f / lg;
         if ((int)threadIdx.x < heads_here) {
             const float lse = lg == 0.0f ? -__builtin_inff() : mg + __builtin_log2f(lg);
-            if (a.splits > 1) a.plse[(row0 + threadIdx.x) * a.splits + split] = lse;
+            if (!whole) a.plse[slot * 16 + threadIdx.x] = lse;
             else if (a.lse) a.lse[row0 + threadIdx.x] = lse * kLn2;
         }
     }
@@ -557,8 +650,13 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
 #pragma unroll
         for (int w = 1; w < 4; ++w) o += red[(w * 16 + r) * (DP / 4 + 1) + d] * st_e[w][r];
         o *= inv_l[r];
-        if (a.splits > 1) *reinterpret_cast<v4f*>(a.part + ((row0 + r) * a.splits + split) * a.D + 4 * d) = o;
+        if (!whole) *reinterpret_cast<v4f*>(a.part + (slot * 16 + r) * a.D + 4 * d) = o;
         else store_quad(a.out, (row0 + r) * a.D + 4 * d, a.dt, o);
+    }
+    left -= k1 - k0;
+    k0 = 0;
+    ++b;
+    if (left > 0) __syncthreads();                           // the stages' LDS is free again
     }
 }
 
@@ -570,16 +668,38 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     __shared__ float red[8];
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
     const int64_t row = blockIdx.x;
-    const int n = a.splits;
+    const int b = (int)(row / a.H), hq = (int)(row - (int64_t)b * a.H), h = hq / a.group, g = hq - h * a.group;
+    const int HG = a.heads * a.gtiles, hg = h * a.gtiles + (g >> 4);
+    const int u0 = a.before[b], all = a.before[a.B], share = all < a.share ? all : a.share;
+    const int n1 = a.before[b + 1] - u0, L = a.D / 4;
+    if (n1 == 0) {                                           // no token to see
+        if (tid < L) store_quad(a.out, row * a.D + 4 * tid, a.dt, v4f{0.0f, 0.0f, 0.0f, 0.0f});
+        if (tid == 0 && a.lse) a.lse[row] = -__builtin_inff();
+        return;
+    }
+    // share i has the units from i all / share on: the shares of the sequence's first and last unit
+    const int i0 = (int)(((int64_t)(u0 + 1) * share - 1) / all);
+    const int n = (int)(((int64_t)(u0 + n1) * share - 1) / all) - i0 + 1;
+    if (n == 1) return;                                      // a single block has written it
+    const int64_t slot = (int64_t)(b + i0) * HG + hg;        // of the first part; the next ones HG further on each
+    const float* plse = a.plse + slot * 16 + (g & 15);
+    const float* part = a.part + (slot * 16 + (g & 15)) * a.D;
+    const int groups = 256 / L, grp = tid / L, j = tid - grp * L;
+    const bool mine = grp < groups && grp < n;
+    auto part_at = [&](int i) __attribute__((always_inline)) {
+        return *reinterpret_cast<const v4f*>(part + (int64_t)i * HG * 16 * a.D + 4 * j);
+    };
+    v4f s = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (mine) s = part_at(grp);                              // requested before the weights are known
     float top = -__builtin_inff();
-    for (int i = tid; i < n; i += 256) top = fmaxf(top, a.plse[row * a.splits + i]);
+    for (int i = tid; i < n; i += 256) top = fmaxf(top, plse[(int64_t)i * HG * 16]);
     top = wave_max(top);
     if (lane == 0) red[wave] = top;
     __syncthreads();
     top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
     float total = 0.0f;
     for (int i = tid; i < n; i += 256) {
-        const float v = a.plse[row * a.splits + i];
+        const float v = plse[(int64_t)i * HG * 16];
         // a part without a token weighs nothing, and a NaN stays one
         const float w = v == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(v - top);
         wt[i] = w;
@@ -590,13 +710,11 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     if (lane == 0) red[4 + wave] = total;
     __syncthreads();
     total = red[4] + red[5] + red[6] + red[7];
-    const int L = a.D / 4, groups = 256 / L, grp = tid / L, j = tid - grp * L;
-    v4f s = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    if (grp < groups)
-        for (int i = grp; i < n; i += groups) {
-            const float w = wt[i];
-            if (w != 0.0f) s += w * *reinterpret_cast<const v4f*>(a.part + (row * a.splits + i) * a.D + 4 * j);
-        }
+    if (mine) {
+        // (a part without a token holds zeros)
+        s *= wt[grp];
+        for (int i = grp + groups; i < n; i += groups) s += wt[i] * part_at(i);
+    }
     sum[tid] = s;
     __syncthreads();
     if (tid >= L) return;
@@ -608,19 +726,15 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 
 namespace {
 
-struct Plan {
-    int32_t chunk, splits;
-};
+constexpr int64_t kMaxShare = 768;         // blocks that share the work: at most three on each CU
 
-// Chunks of a sequence: about 1024 blocks of four waves (four on each CU), at
-// least one tile of 32 tokens for every wave of a block.
-Plan plan_of(int64_t B, int32_t H, int32_t heads, int64_t max_len, int32_t window) {
+// Whether the blocks share the work: where a block to each sequence and tile of heads
+// would not fill the card (and sequences are longer than a unit), as far as the sums
+// over sequences fit a block and 31 bits.
+bool shared_work(int64_t B, int32_t H, int32_t heads, int64_t max_len, int32_t window) {
     const int64_t group = H / heads, pairs = B * heads * ((group + 15) / 16);
-    int64_t span = window > 0 && (int64_t)window + 31 < max_len ? (int64_t)window + 31 : max_len;
-    if (span < 1) span = 1;
-    const int64_t want = pairs >= 1024 ? 1 : 1024 / pairs;
-    const int64_t chunk = ((span + want - 1) / want + 127) / 128 * 128;
-    return Plan{(int32_t)chunk, (int32_t)((span + chunk - 1) / chunk)};
+    const int64_t span = window > 0 && (int64_t)window + 31 < max_len ? (int64_t)window + 31 : max_len;
+    return span > kUnit && B <= 1024 && pairs < kMaxShare && pairs * ((span + kUnit - 1) / kUnit) < ((int64_t)1 << 30);
 }
 
 template <int BITS, int DP>
@@ -638,8 +752,10 @@ hipError_t run_attn(const AttnArgs& a, int64_t blocks, hipStream_t st) {
 }  // namespace
 
 size_t attn_scratch_bytes(int64_t B, int32_t H, int32_t heads, int32_t D, int64_t max_len, int32_t window) {
-    const Plan p = plan_of(B, H, heads, max_len, window);
-    return p.splits > 1 ? (size_t)B * H * p.splits * (D + 1) * 4 : 0;
+    if (!shared_work(B, H, heads, max_len, window)) return 0;
+    const int64_t HG = (int64_t)heads * ((H / heads + 15) / 16);
+    const size_t slots = (size_t)((kMaxShare > HG ? kMaxShare / HG : 1) + B) * HG;
+    return slots * 16 * (D + 1) * 4 + (size_t)(B + 1) * 4;
 }
 
 hipError_t launch_attn_decode(const void* q, int64_t ldq, int q_dtype, int64_t B, int32_t H, const KvCache& c,
@@ -651,19 +767,27 @@ hipError_t launch_attn_decode(const void* q, int64_t ldq, int q_dtype, int64_t B
     a.kc = static_cast<const uint8_t*>(c.k_codes); a.ks = c.k_scales;
     a.vc = static_cast<const uint8_t*>(c.v_codes); a.vs = c.v_scales;
     a.table = table; a.ldt = ldt; a.lengths = lengths;
-    a.H = H; a.heads = c.heads; a.group = H / c.heads; a.gtiles = (a.group + 15) / 16;
+    a.B = (int32_t)B; a.H = H; a.heads = c.heads; a.group = H / c.heads; a.gtiles = (a.group + 15) / 16;
     a.D = c.D; a.shift = c.shift; a.pages = (int32_t)c.pages;
-    const int64_t most = width << c.shift;
-    const Plan p = plan_of(B, H, c.heads, max_len, window);
+    const int64_t most = width << c.shift, pairs = B * c.heads * a.gtiles;
     a.max_len = (int32_t)(c.pages == 0 ? 0 : max_len < most ? max_len : most);
-    a.window = window; a.chunk = p.chunk; a.splits = p.splits;
+    a.window = window;
     a.scale2 = scale * 1.44269504088896340736f;
     a.out = out; a.dt = out_dtype; a.lse = lse;
-    a.part = static_cast<float*>(scratch);
-    a.plse = a.part + (p.splits > 1 ? (size_t)B * H * p.splits * c.D : 0);
-    const int64_t blocks = B * c.heads * a.gtiles * p.splits;
+    const bool shared = shared_work(B, H, c.heads, max_len, window);
+    if (shared) {
+        // what fits: by the stages' LDS, and the registers at D above 128
+        const int bits = c.bits * (c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256);
+        const int64_t fit = c.D > 128 ? 256 : bits >= 1024 ? 512 : 768, HG = (int64_t)c.heads * a.gtiles;
+        a.share = (int32_t)(fit > HG ? fit / HG : 1);
+        const int64_t slots = (a.share + B) * HG;
+        a.part = static_cast<float*>(scratch);
+        a.plse = a.part + slots * 16 * c.D;
+        a.before = reinterpret_cast<int32_t*>(a.plse + slots * 16);
+    }
+    const int64_t blocks = shared ? (int64_t)a.share * c.heads * a.gtiles : pairs;
     hipError_t e = c.bits == 8 ? run_attn<8>(a, blocks, st) : run_attn<4>(a, blocks, st);
-    if (e != hipSuccess || p.splits == 1) return e;
+    if (e != hipSuccess || !shared) return e;
     hipLaunchKernelGGL(k_attn_join, dim3((unsigned)(B * H)), dim3(256), 0, st, a);
     return hipGetLastError();
 }

@@ -87,7 +87,7 @@ def test_attn_workspace():
     assert L.qa_attn_decode_workspace(2000, 32, 8, 128, 1 << 20, 0) == 0    # enough sequences for the card
     n = L.qa_attn_decode_workspace(1, 32, 8, 128, 4096, 0)
     assert n >= 2 * 32 * 129 * 4 and n % 256 == 0
-    assert 0 < L.qa_attn_decode_workspace(1, 32, 8, 128, 1 << 30, 600) < n  # the window bounds the work
+    assert L.qa_attn_decode_workspace(1, 32, 8, 128, 1 << 30, 90) == 0       # the window bounds the work
 
 
 LINEAR = dict(Xq=A, sx=A, M=6, K=64, Wq=A, sw=A, N=48, bias=A, act=0, res=A, ldr=48, out=A, ldo=48, dt=1, st=None)
