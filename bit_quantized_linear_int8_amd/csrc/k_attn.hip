@@ -165,8 +165,14 @@ __device__ __forceinline__ void load_lds4(const void* p, void* lds) {
 // s_waitcnt immediate waiting for vmcnt <= n only (gfx9 encoding)
 constexpr int vmcnt_only(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 
-// Stages of LDS for a wave, by the bits of a row.
-constexpr int stages(int bits) { return bits >= 1024 ? 2 : 3; }
+// Stages of LDS for a wave and blocks on a CU, by D rounded up: at 64 four blocks hide
+// each other's waits better than stages do (33 sequences of 1000 tokens, 32 heads:
+// 26.2 us against 27.7 with two stages and 30.7 with three of three blocks); from 128
+// on two stages (4 sequences of up to 131072 in int4: 95 us of the call against
+// 96 with one stage and three blocks, 102 with three of each); at 256 the registers
+// leave one block.
+constexpr int stages(int DP) { return DP == 64 ? 1 : 2; }
+constexpr int blocks_on_cu(int DP) { return DP == 64 ? 4 : DP == 128 ? 2 : 1; }
 
 __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
 
@@ -175,7 +181,7 @@ __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), f
 // DP: D rounded up to 64, 128 or 256 (what lies behind D meets queries of 0, or is
 // not stored).  F32: fp32 queries.
 template <int BITS, int DP, bool F32>
-__global__ __launch_bounds__(256, DP == 256 ? 1 : stages(BITS * DP)) void k_attn_decode(AttnArgs a) {
+__global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs a) {
     constexpr int CC = BITS == 8 || DP == 64 ? 16 : 32;      // codes of a lane's piece of a key
     constexpr int NS = DP / (4 * CC);                        // pieces of a lane
     constexpr int PB = CC * BITS / 8;                        // bytes of a piece
@@ -186,7 +192,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : stages(BITS * DP)) void k_attn
     constexpr int DPB = DP * BITS / 8, NCH = DPB / 16;       // a row in LDS, its chunks
     constexpr int INS = 16 * DPB < 1024 ? 1 : 16 * DPB / 1024;    // loads of 16 rows
     constexpr int HALF = INS * 1024;
-    constexpr int SB = 4 * HALF + 256, NST = stages(BITS * DP);
+    constexpr int SB = 4 * HALF + 256, NST = stages(DP);
     constexpr int RED = 4 * 16 * (DP / 4 + 1) * 16;
     __shared__ __attribute__((aligned(16))) uint8_t smem[4 * NST * SB > RED ? 4 * NST * SB : RED];
     auto swz = [](int r) { return (NCH <= 8 ? r / (8 / (NCH <= 8 ? NCH : 8)) : r) & (NCH - 1); };
@@ -726,15 +732,16 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 
 namespace {
 
-constexpr int64_t kMaxShare = 768;         // blocks that share the work: at most three on each CU
+constexpr int64_t kMaxShare = 1024;        // blocks that share the work: at most four on each CU
 
 // Whether the blocks share the work: where a block to each sequence and tile of heads
-// would not fill the card (and sequences are longer than a unit), as far as the sums
+// would not fill the card (768: with 1056 of 1000 tokens, 40 us shared and 31 not; and
+// sequences are longer than a unit), as far as the sums
 // over sequences fit a block and 31 bits.
 bool shared_work(int64_t B, int32_t H, int32_t heads, int64_t max_len, int32_t window) {
     const int64_t group = H / heads, pairs = B * heads * ((group + 15) / 16);
     const int64_t span = window > 0 && (int64_t)window + 31 < max_len ? (int64_t)window + 31 : max_len;
-    return span > kUnit && B <= 1024 && pairs < kMaxShare && pairs * ((span + kUnit - 1) / kUnit) < ((int64_t)1 << 30);
+    return span > kUnit && B <= 1024 && pairs < 768 && pairs * ((span + kUnit - 1) / kUnit) < ((int64_t)1 << 30);
 }
 
 template <int BITS, int DP>
@@ -776,9 +783,7 @@ hipError_t launch_attn_decode(const void* q, int64_t ldq, int q_dtype, int64_t B
     a.out = out; a.dt = out_dtype; a.lse = lse;
     const bool shared = shared_work(B, H, c.heads, max_len, window);
     if (shared) {
-        // what fits: by the stages' LDS, and the registers at D above 128
-        const int bits = c.bits * (c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256);
-        const int64_t fit = c.D > 128 ? 256 : bits >= 1024 ? 512 : 768, HG = (int64_t)c.heads * a.gtiles;
+        const int64_t fit = 256 * blocks_on_cu(c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256), HG = (int64_t)c.heads * a.gtiles;
         a.share = (int32_t)(fit > HG ? fit / HG : 1);
         const int64_t slots = (a.share + B) * HG;
         a.part = static_cast<float*>(scratch);
