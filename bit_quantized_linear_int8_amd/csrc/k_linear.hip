@@ -3,9 +3,9 @@
 //
 //   out[m][n] = act(s_x[m] s_w[n] sum_k Xq[m][k] Wq[n][k] + bias[n]) + res[m][n]
 //
-// The product is exact (int32); the rest is fp32 and rounded once.  Two forms, of
-// the products that the adapters' linear has: weights streamed straight into MFMA
-// operands for few tokens, the tile product of qa_tile.hpp for many.
+// The product is exact (int32); the rest is fp32 and rounded once.  Three forms: for
+// few tokens the weights streamed, straight into MFMA operands in one round of blocks
+// or through LDS in many, and for many tokens the tile product of qa_tile.hpp.
 //
 // The activations need no table and no branch:
 //   silu x sigma(x), and gelu's tanh form 0.5 x (1 + tanh u) = x sigma(2 u), by the
@@ -33,7 +33,7 @@ struct LinearArgs {
     float c1, c3;              // sigma's argument c1 x + c3 x^3
     float least;               // linear: results below it become it (-inf, or relu's 0)
     int32_t dt;
-    bool vec, vecr;            // rows of out, of res allow 4-element vectors
+    bool vec, vecr, vecn;      // rows of out, of res, and s_w and bias allow 4-element vectors
 };
 
 enum Act { LINEAR = 0, SIGMA = 1, GELU = 2 };
@@ -57,6 +57,22 @@ __device__ __forceinline__ float activate(const LinearArgs& a, float x) {
         return (x < 0.0f ? 0.0f : x) - z * (0.5f * t * p * e);
     }
     return x < a.least ? a.least : x;                        // (a NaN stays)
+}
+
+// Sixteen bytes from each lane's offset to LDS, lane after lane.
+__device__ __forceinline__ void load_lds16(rsrc_t r, uint32_t off, void* lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (tile::lds_void*)lds, 16, off, 0, 0, 0);
+}
+
+// Four 16-bit values of type dt (1 fp16, 2 bf16).
+__device__ __forceinline__ v4f widen4(u32x2 w, int dt) {
+    v4f v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint16_t h = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        v[e] = dt == 1 ? h2f(h) : __builtin_bit_cast(float, (uint32_t)h << 16);
+    }
+    return v;
 }
 
 // Four residuals of type dt at p[at], of which the first n exist.
@@ -87,7 +103,12 @@ __device__ __forceinline__ v4f load4(const void* p, int64_t at, int dt, int n, b
 
 }  // namespace
 
-// Few tokens (16 MT): 16 output columns per block, K split over its 8 waves.
+// ---------------------------------------------------------------------------
+// Few tokens (at most 16 MT) and columns: 16 output columns per block, K split over
+// its 8 waves, which bring the weights' rows straight into MFMA operands with every
+// load in flight at once.  One round of blocks, bound by latency: 16 x 4096 x 4096 in
+// 6.8 us, 2.5 TB/s (the stream below, which has to go through LDS, 7.2; tiles 12.8).
+// ---------------------------------------------------------------------------
 template <int MT>
 __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int act) {
     __shared__ v4i part[8][MT][64];
@@ -161,8 +182,153 @@ __global__ __launch_bounds__(512) void k_linear_stream(LinearArgs a, int act) {
     store4(a.out, mo * a.ldo + no, a.dt, v, cols, a.vec);
 }
 
-// Many tokens: one tile of the product per block.
-template <class C, int ACT>
+// Four floats of a vector of n from column c on, as far as there are any.
+__device__ __forceinline__ v4f cols4(const float* p, int64_t c, int n, bool vec) {
+    if (vec && n >= 4) return *reinterpret_cast<const v4f*>(p + c);
+    v4f v = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < n) v[e] = p[c + e];
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// At most 16 tokens and many columns: the stream of the weights is the work.  A block
+// takes 16 output columns at a time (gridDim.x apart), its 8 waves a slice of 512
+// bytes each of every 4096 of K.  A wave's 16 rows of W come by direct loads of whole
+// lines into a stage of LDS of its own (the 16-byte chunk c of row r at c ^ (r & 7)),
+// one further stage in flight, so that no barrier drains the stream; its tokens' codes
+// are MFMA operands in registers, which stay there from column to column while K is at
+// most 4096 and are requested a stage ahead where it is more.  The waves' sums meet in
+// LDS, and one wave ends the tile.
+// By size (us, graphs of calls; this form, the one above, tiles of 64 x 64):
+//   K 4096   1 x 11008     12.0   10.9   13.3      16 x 11008    13.2   14.0   13.2
+//            1 x 32000     28.0   26.2   28.4      16 x 32000    29.4   40.8   29.2
+//            1 x 128000    95.8   89.3    128      16 x 128000    103    149    129
+//   K 11008  1 x 8192      18.3   21.0   33.1      16 x 8192     23.3   27.5   33.1
+//            1 x 16384     38.6   44.7   46.2      16 x 16384    48.3   59.6   46.8
+// (5.1 TB/s at 16 x 128000.)  32 tokens in two operands are no faster than tiles from
+// 8192 columns on (13.0 and 13.2), 64 slower (their codes' traffic passes the weights').
+// ---------------------------------------------------------------------------
+template <bool RES16>
+__global__ __launch_bounds__(512, 2) void k_linear_few(LinearArgs a, int act) {
+    constexpr int SL = 512, STEPS = SL / 64, INS = SL / 64, CH = SL / 16, NW = 8;
+    constexpr int STAGE = 16 * SL;
+    // one array: beside a second one the compiler takes every stage load for a writer of what is read
+    __shared__ __attribute__((aligned(16))) uint8_t smem[NW * 2 * STAGE + NW * 1024];
+    v4i* const part = reinterpret_cast<v4i*>(smem + NW * 2 * STAGE);
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int r16 = lane & 15, q16 = lane >> 4;
+    const uint32_t K = (uint32_t)a.K;
+    const int groups = (int)((a.N + 15) / 16), parts = (int)((K + NW * SL - 1) / (NW * SL));
+    const rsrc_t rx = make_rsrc(a.Xq, a.M * a.K);
+    const uint32_t ox = r16 < a.M ? (uint32_t)r16 * K : kOOB;
+    v4i x[STEPS];
+    auto load_x = [&](int p) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const uint32_t k = (uint32_t)(p * NW + wave) * SL + s * 64 + q16 * 16;
+            x[s] = __builtin_bit_cast(v4i, bload16(rx, k < K ? ox + k : kOOB));
+        }
+    };
+    // a lane's rows and chunks of the loads of a stage
+    uint32_t row[INS], chunk[INS];
+#pragma unroll
+    for (int n = 0; n < INS; ++n) {
+        const int P = n * 64 + lane;
+        row[n] = P / CH;
+        chunk[n] = (uint32_t)(((P % CH) ^ (row[n] & 7)) * 16);
+    }
+    uint8_t* const mine = smem + wave * 2 * STAGE;
+    auto fill = [&](int st, int grp, int p) __attribute__((always_inline)) {
+        const int64_t n0 = (int64_t)grp * 16;
+        const uint32_t rows = grp < groups ? (uint32_t)(a.N - n0 < 16 ? a.N - n0 : 16) : 0u;
+        const rsrc_t rw = make_rsrc(a.Wq + (grp < groups ? n0 : 0) * a.K, (int64_t)rows * K);
+        const uint32_t k0 = (uint32_t)(p * NW + wave) * SL;
+#pragma unroll
+        for (int n = 0; n < INS; ++n)
+            load_lds16(rw, row[n] < rows && k0 + chunk[n] < K ? row[n] * K + k0 + chunk[n] : kOOB, mine + st * STAGE + n * 1024);
+    };
+    const bool ends = wave == 0 && r16 < a.M;                // the lane's row is r16
+    const float sx = ends ? a.s_x[r16] : 0.0f;
+
+    // items: the parts of K of one group after the other
+    int grp = blockIdx.x, p = 0, ngrp = grp, np = 0, st = 0;
+    auto next = [&]() __attribute__((always_inline)) {
+        if (++np == parts) np = 0, ngrp += gridDim.x;
+    };
+    load_x(0);
+    fill(0, ngrp, np);
+    next();
+    fill(1, ngrp, np);
+    next();
+    v4i acc = v4i{0, 0, 0, 0};
+    while (grp < groups) {
+        __builtin_amdgcn_s_waitcnt(tile::vmcnt(INS));          // this stage and these codes are there, the next stage may not
+        asm volatile("" ::: "memory");
+        const uint8_t* from = mine + st * STAGE;
+        v4i w[STEPS];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            w[s] = *reinterpret_cast<const v4i*>(from + r16 * SL + (((4 * s + q16) ^ (r16 & 7)) << 4));
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s], x[s], acc, 0, 0, 0);
+        const bool last = p + 1 == parts;
+        const int64_t n = (int64_t)grp * 16 + 4 * q16;
+        const int cols = (int)(a.N - n < 4 ? a.N - n : 4);
+        // What the end reads is requested before the stream goes on, without a branch (one would wait for it).
+        const int64_t n0 = (int64_t)grp * 16;
+        const int64_t bytes = last && wave == 0 ? (a.N - n0 < 16 ? a.N - n0 : 16) * 4 : 0;
+        const rsrc_t rsw = make_rsrc(a.s_w + n0, bytes), rbi = make_rsrc(a.bias + n0, a.bias ? bytes : 0);
+        float sw[4], bi[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            sw[q] = __builtin_bit_cast(float, bload4(rsw, 16 * q16 + 4 * q));
+            bi[q] = __builtin_bit_cast(float, bload4(rbi, 16 * q16 + 4 * q));
+        }
+        u32x2 early;
+        if constexpr (RES16)
+            early = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.res) + (ends ? r16 : 0) * a.ldr + (cols > 0 ? n : 0));
+        if (parts > 1) load_x(last ? 0 : p + 1);
+        __builtin_amdgcn_s_waitcnt(0xC07F);                  // lgkmcnt(0): the stage is read
+        asm volatile("" ::: "memory");
+        fill(st, ngrp, np);
+        next();
+        st ^= 1;
+        if (!last) {
+            ++p;
+            continue;
+        }
+        p = 0;
+        lds_only_barrier();                                  // the sums before these have been taken
+        part[wave * 64 + lane] = acc;
+        acc = v4i{0, 0, 0, 0};
+        lds_only_barrier();
+        if (ends && cols > 0) {
+            v4i c = part[lane];
+#pragma unroll
+            for (int q = 1; q < NW; ++q) c += part[q * 64 + lane];
+            v4f res = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (RES16) res = widen4(early, a.dt);
+            else if (a.res) res = load4(a.res, r16 * a.ldr + n, a.dt, cols, a.vecr);
+            float v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float y = (float)c[q] * sx * sw[q] + bi[q];
+                v[q] = (act == SIGMA ? activate<SIGMA>(a, y) : act == GELU ? activate<GELU>(a, y) : activate<LINEAR>(a, y)) + res[q];
+            }
+            store4(a.out, r16 * a.ldo + n, a.dt, v, cols, a.vec);
+        }
+        grp += gridDim.x;
+    }
+    __builtin_amdgcn_s_waitcnt(tile::vmcnt(0));                // no load is left to land in another block's LDS
+}
+
+// Many tokens: one tile of the product per block.  RES16: a 16-bit residual whose
+// rows allow vectors is requested before the product and waits in registers (24 for
+// the largest tile), so that its bytes come during the product instead of after it:
+// 2048 x 11008 x 4096 takes 107 us so against 124.
+template <class C, int ACT, bool RES16>
 __global__ __launch_bounds__(C::THREADS, 4) void k_linear_tile(LinearArgs a, int32_t tiles_m, int32_t tiles_n) {
     extern __shared__ uint8_t smem[];
     int tm, tn;
@@ -172,55 +338,65 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_linear_tile(LinearArgs a, int
     const rsrc_t rw = make_rsrc(a.Wq + n0 * a.K, (a.N - n0) * a.K);
     const uint32_t K = (uint32_t)a.K;
     const int lane = threadIdx.x & 63, wave = wave_id();
+    const int64_t mw = m0 + (wave / C::WN) * C::TM + (lane & 15), nw = n0 + (wave % C::WN) * C::TN + 4 * (lane >> 4);
+    u32x2 early[RES16 ? C::FM : 1][RES16 ? C::FN : 1];
+    if constexpr (RES16) {
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) {
+                const int64_t m = mw + i * 16 < a.M ? mw + i * 16 : a.M - 1, n = nw + j * 16 < a.N ? nw + j * 16 : 0;
+                early[i][j] = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.res) + m * a.ldr + n);
+            }
+    }
     v4i acc[C::FM][C::FN];
     tile::product<C>(
         ra, rw, K, smem, [&](int r) -> uint32_t { return m0 + r < a.M ? (uint32_t)r * K : kOOB; },
         [&](int r) -> uint32_t { return n0 + r < a.N ? (uint32_t)r * K : kOOB; }, acc);
-    const int64_t mw = m0 + (wave / C::WN) * C::TM + (lane & 15), nw = n0 + (wave % C::WN) * C::TN + 4 * (lane >> 4);
     float sx[C::FM];
+    v4f sw[C::FN], bi[C::FN];
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) sx[i] = mw + i * 16 < a.M ? a.s_x[mw + i * 16] : 0.0f;
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
         const int64_t n = nw + j * 16;
-        if (n >= a.N) continue;
         const int cols = (int)(a.N - n < 4 ? a.N - n : 4);
-        float sw[4], bi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        sw[j] = cols4(a.s_w, n, cols, a.vecn);
+        bi[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        if (a.bias) bi[j] = cols4(a.bias, n, cols, a.vecn);
+    }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            sw[q] = a.s_w[n + min(q, cols - 1)];
-            if (a.bias) bi[q] = a.bias[n + min(q, cols - 1)];
-        }
-        v4f res[C::FM];
+    for (int i = 0; i < C::FM; ++i) {
+        const int64_t m = mw + i * 16;
+        if (m >= a.M) continue;
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-            res[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-            if (a.res && mw + i * 16 < a.M) res[i] = load4(a.res, (mw + i * 16) * a.ldr + n, a.dt, cols, a.vecr);
-        }
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-            if (mw + i * 16 >= a.M) continue;
+        for (int j = 0; j < C::FN; ++j) {
+            const int64_t n = nw + j * 16;
+            if (n >= a.N) continue;
+            const int cols = (int)(a.N - n < 4 ? a.N - n : 4);
+            v4f res = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (RES16) res = widen4(early[i][j], a.dt);
+            else if (a.res) res = load4(a.res, m * a.ldr + n, a.dt, cols, a.vecr);
             float v[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = activate<ACT>(a, (float)acc[i][j][q] * sx[i] * sw[q] + bi[q]) + res[i][q];
-            store4(a.out, (mw + i * 16) * a.ldo + n, a.dt, v, cols, a.vec);
+            for (int q = 0; q < 4; ++q) v[q] = activate<ACT>(a, (float)acc[i][j][q] * sx[i] * sw[j][q] + bi[j][q]) + res[q];
+            store4(a.out, m * a.ldo + n, a.dt, v, cols, a.vec);
         }
     }
 }
 
 namespace {
 
-// The streaming form while its blocks of 16 columns fit the CUs at once (the rule of
-// the adapters' linear, whose products these are).
-bool few_rows(int64_t M, int64_t N) {
-    const int64_t blocks = (N + 15) / 16;
-    return M <= 16 ? blocks <= 768 : M <= 32 ? blocks <= 512 : M <= 64 && blocks <= 256;
-}
+// Whether a 16-bit residual can be read four values at a time.
+bool res16(const LinearArgs& a) { return a.res && a.dt != 0 && a.vecr && a.N % 4 == 0; }
 
 template <class C, int ACT>
 hipError_t run_tile(const LinearArgs& a, hipStream_t st) {
     const int tm = (int)((a.M + C::BM - 1) / C::BM), tn = (int)((a.N + C::BN - 1) / C::BN);
-    hipLaunchKernelGGL((k_linear_tile<C, ACT>), dim3((unsigned)(tm * tn)), dim3(C::THREADS), C::LDS, st, a, tm, tn);
+    if (res16(a))
+        hipLaunchKernelGGL((k_linear_tile<C, ACT, true>), dim3((unsigned)(tm * tn)), dim3(C::THREADS), C::LDS, st, a, tm, tn);
+    else
+        hipLaunchKernelGGL((k_linear_tile<C, ACT, false>), dim3((unsigned)(tm * tn)), dim3(C::THREADS), C::LDS, st, a, tm, tn);
     return hipGetLastError();
 }
 
@@ -252,12 +428,19 @@ hipError_t launch_linear_i8_act(const int8_t* Xq, const float* s_x, int64_t M, i
     a.c3 = act == QA_ACT_GELU_TANH ? 0.0713548162726002527f : 0.0f;
     a.vec = vec4(out, ldo, dtype);
     a.vecr = res && vec4(res, ldr, dtype);
+    a.vecn = vec4(s_w, 0, 0) && vec4(bias, 0, 0);
     const int kind = act == QA_ACT_SILU || act == QA_ACT_GELU_TANH ? SIGMA : act == QA_ACT_GELU ? GELU : LINEAR;
-    if (few_rows(M, N)) {
-        const unsigned nb = (unsigned)((N + 15) / 16);
-        if (M <= 16) hipLaunchKernelGGL(k_linear_stream<1>, dim3(nb), dim3(512), 0, st, a, kind);
-        else if (M <= 32) hipLaunchKernelGGL(k_linear_stream<2>, dim3(nb), dim3(512), 0, st, a, kind);
-        else hipLaunchKernelGGL(k_linear_stream<4>, dim3(nb), dim3(512), 0, st, a, kind);
+    const int64_t groups = (N + 15) / 16;
+    if (M <= 64 && groups <= 256) {                          // one round of blocks
+        const dim3 g((unsigned)groups);
+        if (M <= 16) hipLaunchKernelGGL(k_linear_stream<1>, g, dim3(512), 0, st, a, kind);
+        else if (M <= 32) hipLaunchKernelGGL(k_linear_stream<2>, g, dim3(512), 0, st, a, kind);
+        else hipLaunchKernelGGL(k_linear_stream<4>, g, dim3(512), 0, st, a, kind);
+        return hipGetLastError();
+    }
+    if (M <= 16) {
+        if (res16(a)) hipLaunchKernelGGL(k_linear_few<true>, dim3(256), dim3(512), 0, st, a, kind);
+        else hipLaunchKernelGGL(k_linear_few<false>, dim3(256), dim3(512), 0, st, a, kind);
         return hipGetLastError();
     }
     return kind == SIGMA ? run_tiles<SIGMA>(a, st) : kind == GELU ? run_tiles<GELU>(a, st) : run_tiles<LINEAR>(a, st);
