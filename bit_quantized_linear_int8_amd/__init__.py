@@ -812,22 +812,54 @@ def qa_qlinear_int8_lora(Xq, s_x, X, Wq, s_w, A, B, alpha, seg, which, out_dtype
     return out
 
 
+def _one_device(t, *others):
+    """The operands' device, which has to be the same for all (None: not given)."""
+    d = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != d:
+            raise ValueError("all tensors must be on one device, got %s and %s" % (t.device, o.device))
+    return d
+
+
+class _Device:
+    """The operands' device made the current one for a call where it is not (the stream and the launch go by it)."""
+    __slots__ = ("want", "was")
+
+    def __init__(self, want):
+        self.want = want
+
+    def __enter__(self):
+        self.was = torch._C._cuda_getDevice()
+        if self.was != self.want:
+            torch._C._cuda_setDevice(self.want)
+
+    def __exit__(self, *exc):
+        if self.was != self.want:
+            torch._C._cuda_setDevice(self.was)
+
+
 def _cache(cache):
     """The four tensors of a cache -> (bits, pages, heads, page, D): see qa_kv_write."""
     kc, ks, vc, vs = cache
-    if kc.dtype not in (torch.int8, torch.int32):
-        raise TypeError("cache codes must be int8 (8 bits) or int32 (4 bits, packed), got %s" % kc.dtype)
-    _dev(kc, "k_codes", kc.dtype)
-    if kc.dim() != 4:
-        raise ValueError("k_codes must be [pages x heads x page x D (or D / 8 words)], got %s" % list(kc.shape))
-    _dev(ks, "k_scales", torch.float32)
-    _dev(vc, "v_codes", kc.dtype)
-    _dev(vs, "v_scales", torch.float32)
-    pages, heads, page, width = kc.shape
-    _shape(vc, "v_codes", kc.shape)
-    _shape(ks, "k_scales", kc.shape[:3])
-    _shape(vs, "v_scales", kc.shape[:3])
-    return (8, pages, heads, page, width) if kc.dtype == torch.int8 else (4, pages, heads, page, 8 * width)
+    shape, dt, f32 = kc.shape, kc.dtype, torch.float32
+    if not (len(shape) == 4 and kc.is_cuda and ks.is_cuda and vc.is_cuda and vs.is_cuda and vc.dtype == dt and
+            ks.dtype == f32 and vs.dtype == f32 and vc.shape == shape and ks.shape == shape[:3] and
+            vs.shape == shape[:3] and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and
+            vs.is_contiguous()):
+        _dev(kc, "k_codes", kc.dtype)
+        if kc.dim() != 4:
+            raise ValueError("k_codes must be [pages x heads x page x D (or D / 8 words)], got %s" % list(kc.shape))
+        _dev(ks, "k_scales", f32)
+        _dev(vc, "v_codes", kc.dtype)
+        _dev(vs, "v_scales", f32)
+        _shape(vc, "v_codes", kc.shape)
+        _shape(ks, "k_scales", kc.shape[:3])
+        _shape(vs, "v_scales", kc.shape[:3])
+    if dt == torch.int8:
+        return 8, shape[0], shape[1], shape[2], shape[3]
+    if dt != torch.int32:
+        raise TypeError("cache codes must be int8 (8 bits) or int32 (4 bits, packed), got %s" % dt)
+    return 4, shape[0], shape[1], shape[2], 8 * shape[3]
 
 
 def _tokens(t, name, heads, D):
@@ -836,11 +868,12 @@ def _tokens(t, name, heads, D):
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
     if t.dtype not in _DTYPE_CODE:
         raise TypeError("%s must be fp32, fp16 or bf16, got %s" % (name, t.dtype))
-    if t.dim() != 3 or t.shape[1:] != (heads, D):
-        raise ValueError("%s must be [tokens x %d x %d], got %s" % (name, heads, D, list(t.shape)))
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise ValueError("%s must be [tokens x %d x %d], got %s" % (name, heads, D, list(shape)))
+    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != D)):
         raise ValueError("%s must have contiguous heads of contiguous values" % name)
-    return t.stride(0) if t.shape[0] > 1 else heads * D
+    return stride[0] if shape[0] > 1 else heads * D
 
 
 def qa_kv_write(K, V, slots, cache, stream=None):
@@ -859,9 +892,11 @@ def qa_kv_write(K, V, slots, cache, stream=None):
     _dev(slots, "slots", torch.int64)
     _shape(slots, "slots", (T,))
     kc, ks, vc, vs = cache
-    _check("qa_kv_write",
-           lib().qa_kv_write(_a(K), ldk, _a(V), ldv, _DTYPE_CODE[K.dtype], T, _a(slots), bits, pages, heads, page, D,
-                             _a(kc), _a(ks), _a(vc), _a(vs), _s(stream)))
+    with _Device(_one_device(K, V, slots, kc, ks, vc, vs)):
+        _check("qa_kv_write",
+               lib().qa_kv_write(K.data_ptr(), ldk, V.data_ptr(), ldv, _DTYPE_CODE[K.dtype], T, slots.data_ptr(), bits,
+                                 pages, heads, page, D, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
+                                 _s(stream)))
 
 
 def qa_kv_read(slots, cache, out_dtype=torch.float16, stream=None):
@@ -873,13 +908,15 @@ def qa_kv_read(slots, cache, out_dtype=torch.float16, stream=None):
         raise ValueError("slots must be [T], got %s" % list(slots.shape))
     if out_dtype not in _DTYPE_CODE:
         raise TypeError("out_dtype must be fp32, fp16 or bf16, got %s" % out_dtype)
-    T = slots.numel()
+    T = slots.shape[0]
     K = _empty(stream, (T, heads, D), dtype=out_dtype, device=slots.device)
-    V = _empty(stream, (T, heads, D), dtype=out_dtype, device=slots.device)
+    V = torch.empty_like(K) if stream is None else _empty(stream, (T, heads, D), dtype=out_dtype, device=slots.device)
     kc, ks, vc, vs = cache
-    _check("qa_kv_read",
-           lib().qa_kv_read(_a(slots), T, bits, pages, heads, page, D, _a(kc), _a(ks), _a(vc), _a(vs), _a(K), _a(V),
-                            _DTYPE_CODE[out_dtype], _s(stream)))
+    with _Device(_one_device(slots, kc, ks, vc, vs)):
+        _check("qa_kv_read",
+               lib().qa_kv_read(slots.data_ptr(), T, bits, pages, heads, page, D, kc.data_ptr(), ks.data_ptr(),
+                                vc.data_ptr(), vs.data_ptr(), K.data_ptr(), V.data_ptr(), _DTYPE_CODE[out_dtype],
+                                _s(stream)))
     return K, V
 
 
@@ -899,7 +936,7 @@ def qa_attn_decode(q, cache, table, lengths, scale=None, window=0, max_len=None,
     bits, pages, heads, page, D = _cache(cache)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [B x H x D]")
-    B, H = q.shape[0], q.shape[1]
+    B, H, _ = q.shape
     ldq = _tokens(q, "q", H, D)
     ldt = _rows(table, "table", torch.int32)
     _dev(lengths, "lengths", torch.int32)
@@ -910,20 +947,27 @@ def qa_attn_decode(q, cache, table, lengths, scale=None, window=0, max_len=None,
         max_len = width * page
     if out is None:
         out = _empty(stream, (B, H, D), dtype=out_dtype or q.dtype, device=q.device)
-    _dev(out, "out")
-    _shape(out, "out", (B, H, D))
+    else:
+        _dev(out, "out")
+        _shape(out, "out", (B, H, D))
     if out.dtype not in _DTYPE_CODE or (out_dtype is not None and out.dtype != out_dtype):
         raise TypeError("out must be fp32, fp16 or bf16 (out_dtype), got %s" % out.dtype)
     lse = _empty(stream, (B, H), dtype=torch.float32, device=q.device) if want_lse else None
-    need = qa_attn_decode_workspace(B, H, heads, D, int(max_len), int(window))
-    if workspace is None and need:
-        workspace = _workspace(stream, need, q.device, None)
+    L = lib()
+    if workspace is None:
+        ws, need = None, L.qa_attn_decode_workspace(B, H, heads, D, int(max_len), int(window))
+        if need:
+            workspace = _empty(stream, need, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
+    else:
+        ws, need = workspace.data_ptr(), workspace.numel()
     kc, ks, vc, vs = cache
-    _check("qa_attn_decode",
-           lib().qa_attn_decode(_a(q), ldq, _DTYPE_CODE[q.dtype], B, H, bits, pages, heads, page, D, _a(kc), _a(ks),
-                                _a(vc), _a(vs), _a(table), ldt, width, _a(lengths), int(max_len), int(window),
-                                float(D ** -0.5 if scale is None else scale), _a(out), _DTYPE_CODE[out.dtype], _a(lse),
-                                _a(workspace), workspace.numel() if workspace is not None else 0, _s(stream)))
+    with _Device(_one_device(q, kc, ks, vc, vs, table, lengths, out, workspace)):
+        _check("qa_attn_decode",
+               L.qa_attn_decode(q.data_ptr(), ldq, _DTYPE_CODE[q.dtype], B, H, bits, pages, heads, page, D,
+                                kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), table.data_ptr(), ldt, width,
+                                lengths.data_ptr(), int(max_len), int(window), D ** -0.5 if scale is None else scale,
+                                out.data_ptr(), _DTYPE_CODE[out.dtype], _a(lse), ws, need, _s(stream)))
     return (out, lse) if want_lse else out
 
 
@@ -946,19 +990,22 @@ def qa_qlinear_int8_act(Xq, s_x, Wq, s_w, bias=None, act=QA_ACT_NONE, residual=N
     if bias is not None:
         _dev(bias, "bias", torch.float32)
         _shape(bias, "bias", (N,))
+    ldo = ldr = N
     if out is None:
         out = _empty(stream, (M, N), dtype=out_dtype if residual is None else residual.dtype, device=Xq.device)
+    else:
+        ldo = _rows(out, "out", out.dtype)
+        _shape(out, "out", (M, N))
     if out.dtype not in _DTYPE_CODE:
         raise TypeError("out must be fp32, fp16 or bf16, got %s" % out.dtype)
-    ldo = _rows(out, "out", out.dtype)
-    _shape(out, "out", (M, N))
-    ldr = N
     if residual is not None:
         ldr = _rows(residual, "residual", out.dtype)
         _shape(residual, "residual", (M, N))
-    _check("qa_qlinear_int8_act",
-           lib().qa_qlinear_int8_act(_a(Xq), _a(s_x), M, K, _a(Wq), _a(s_w), N, _a(bias), int(act), _a(residual), ldr,
-                                     _a(out), ldo, _DTYPE_CODE[out.dtype], _s(stream)))
+    with _Device(_one_device(Xq, s_x, Wq, s_w, bias, residual, out)):
+        _check("qa_qlinear_int8_act",
+               lib().qa_qlinear_int8_act(Xq.data_ptr(), s_x.data_ptr(), M, K, Wq.data_ptr(), s_w.data_ptr(), N, _a(bias),
+                                         int(act), _a(residual), ldr, out.data_ptr(), ldo, _DTYPE_CODE[out.dtype],
+                                         _s(stream)))
     return out
 
 
