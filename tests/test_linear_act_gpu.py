@@ -57,8 +57,10 @@ def check(got, Xq, s_x, Wq, s_w, bias, act, res):
     assert (err <= tol).all(), float((err / tol).max())
 
 
+# (the last ones: the weight stream's form, ragged columns, K in several parts and ending inside one)
 SHAPES = [(1, 16, 1), (1, 64, 16), (3, 80, 17), (16, 256, 100), (17, 128, 33), (32, 512, 48), (33, 144, 130),
-          (64, 1040, 64), (65, 96, 200), (130, 272, 131), (200, 512, 1000), (1, 4096, 13000)]
+          (64, 1040, 64), (65, 96, 200), (130, 272, 131), (200, 512, 1000), (1, 4096, 13000), (16, 4112, 4100),
+          (7, 9008, 4113), (16, 80, 8190)]
 
 
 @pytest.mark.parametrize("act", list(ACTS))
