@@ -243,7 +243,8 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs 
                 if (i == a.B - 1) a.before[a.B] = at;
             }
         if (part >= share) return;
-        const int u0 = (int)((int64_t)part * total / share), u1 = (int)((int64_t)(part + 1) * total / share);
+        const int each = total / share, more = total - each * share;    // the first `more` shares have one unit more
+        const int u0 = part * each + min(part, more), u1 = u0 + each + (part < more ? 1 : 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (pre <= u0 && u0 < pre + n[j]) plan[4] = 4 * threadIdx.x + j, plan[5] = u0 - pre;
@@ -683,9 +684,12 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
         if (tid == 0 && a.lse) a.lse[row] = -__builtin_inff();
         return;
     }
-    // share i has the units from i all / share on: the shares of the sequence's first and last unit
-    const int i0 = (int)(((int64_t)(u0 + 1) * share - 1) / all);
-    const int n = (int)(((int64_t)(u0 + n1) * share - 1) / all) - i0 + 1;
+    // the shares of the sequence's first and last unit (the first `more` shares have one unit more)
+    const int each = all / share, more = all - each * share;
+    auto share_of = [&](int u) __attribute__((always_inline)) {
+        return u < more * (each + 1) ? u / (each + 1) : more + (u - more * (each + 1)) / each;
+    };
+    const int i0 = share_of(u0), n = share_of(u0 + n1 - 1) - i0 + 1;
     if (n == 1) return;                                      // a single block has written it
     const int64_t slot = (int64_t)(b + i0) * HG + hg;        // of the first part; the next ones HG further on each
     const float* plse = a.plse + slot * 16 + (g & 15);
