@@ -812,68 +812,59 @@ def qa_qlinear_int8_lora(Xq, s_x, X, Wq, s_w, A, B, alpha, seg, which, out_dtype
     return out
 
 
-def _one_device(t, *others):
-    """The operands' device, which has to be the same for all (None: not given)."""
-    d = t.get_device()
-    for o in others:
-        if o is not None and o.get_device() != d:
-            raise ValueError("all tensors must be on one device, got %s and %s" % (t.device, o.device))
-    return d
-
-
-class _Device:
-    """The operands' device made the current one for a call where it is not (the stream and the launch go by it)."""
-    __slots__ = ("want", "was")
-
-    def __init__(self, want):
-        self.want = want
-
-    def __enter__(self):
-        self.was = torch._C._cuda_getDevice()
-        if self.was != self.want:
-            torch._C._cuda_setDevice(self.want)
-
-    def __exit__(self, *exc):
-        if self.was != self.want:
-            torch._C._cuda_setDevice(self.was)
+# The calls of a decoding step are host time: what follows looks at all operands in one expression, and where that
+# fails at each by itself, for the error that says which.
+def _on(t, name, d):
+    """An operand on another device than the first one."""
+    if t is not None and t.get_device() != d:
+        raise ValueError("%s must be on the same device as the other tensors, got %s" % (name, t.device))
 
 
 def _cache(cache):
-    """The four tensors of a cache -> (bits, pages, heads, page, D): see qa_kv_write."""
+    """The four tensors of a cache -> (bits, pages, heads, page, D, device index): see qa_kv_write."""
     kc, ks, vc, vs = cache
-    shape, dt, f32 = kc.shape, kc.dtype, torch.float32
-    if not (len(shape) == 4 and kc.is_cuda and ks.is_cuda and vc.is_cuda and vs.is_cuda and vc.dtype == dt and
-            ks.dtype == f32 and vs.dtype == f32 and vc.shape == shape and ks.shape == shape[:3] and
+    shape, dt, d, f32 = kc.shape, kc.dtype, kc.get_device(), torch.float32
+    if not (len(shape) == 4 and d >= 0 and ks.get_device() == d and vc.get_device() == d and vs.get_device() == d and
+            vc.dtype == dt and ks.dtype == f32 and vs.dtype == f32 and vc.shape == shape and ks.shape == shape[:3] and
             vs.shape == shape[:3] and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and
             vs.is_contiguous()):
-        _dev(kc, "k_codes", kc.dtype)
-        if kc.dim() != 4:
-            raise ValueError("k_codes must be [pages x heads x page x D (or D / 8 words)], got %s" % list(kc.shape))
+        _dev(kc, "k_codes", dt)
+        if len(shape) != 4:
+            raise ValueError("k_codes must be [pages x heads x page x D (or D / 8 words)], got %s" % list(shape))
         _dev(ks, "k_scales", f32)
-        _dev(vc, "v_codes", kc.dtype)
+        _dev(vc, "v_codes", dt)
         _dev(vs, "v_scales", f32)
-        _shape(vc, "v_codes", kc.shape)
-        _shape(ks, "k_scales", kc.shape[:3])
-        _shape(vs, "v_scales", kc.shape[:3])
+        _shape(vc, "v_codes", shape)
+        _shape(ks, "k_scales", shape[:3])
+        _shape(vs, "v_scales", shape[:3])
+        for t, name in ((ks, "k_scales"), (vc, "v_codes"), (vs, "v_scales")):
+            _on(t, name, d)
     if dt == torch.int8:
-        return 8, shape[0], shape[1], shape[2], shape[3]
+        return 8, shape[0], shape[1], shape[2], shape[3], d
     if dt != torch.int32:
         raise TypeError("cache codes must be int8 (8 bits) or int32 (4 bits, packed), got %s" % dt)
-    return 4, shape[0], shape[1], shape[2], 8 * shape[3]
+    return 4, shape[0], shape[1], shape[2], 8 * shape[3], d
 
 
-def _tokens(t, name, heads, D):
-    """A [tokens x heads x D] tensor whose tokens are contiguous -> its token stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
-    if t.dtype not in _DTYPE_CODE:
-        raise TypeError("%s must be fp32, fp16 or bf16, got %s" % (name, t.dtype))
+def _tokens(t, name, heads, D, d):
+    """A [tokens x heads x D] tensor whose tokens are contiguous, on device d -> its token stride."""
     shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
-        raise ValueError("%s must be [tokens x %d x %d], got %s" % (name, heads, D, list(shape)))
-    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != D)):
+    if not (len(shape) == 3 and shape[1] == heads and shape[2] == D and t.dtype in _DTYPE_CODE and
+            t.get_device() == d and (not shape[0] or (stride[2] == 1 and (heads == 1 or stride[1] == D)))):
+        if not t.is_cuda:
+            raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+        if t.dtype not in _DTYPE_CODE:
+            raise TypeError("%s must be fp32, fp16 or bf16, got %s" % (name, t.dtype))
+        if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+            raise ValueError("%s must be [tokens x %d x %d], got %s" % (name, heads, D, list(shape)))
+        _on(t, name, d)
         raise ValueError("%s must have contiguous heads of contiguous values" % name)
     return stride[0] if shape[0] > 1 else heads * D
+
+
+def _sd(stream, d):
+    """The given stream's handle, or that of device d's current stream."""
+    return torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
 
 
 def qa_kv_write(K, V, slots, cache, stream=None):
@@ -883,40 +874,49 @@ def qa_kv_write(K, V, slots, cache, stream=None):
     the tokens' places, page index * page + place in the page (-1: not written); cache = (k_codes, k_scales, v_codes,
     v_scales): codes int8 [pages x heads x page x D], or int32 [pages x heads x page x D / 8] for 4 bits, scales f32
     [pages x heads x page]."""
-    bits, pages, heads, page, D = _cache(cache)
-    ldk, ldv = _tokens(K, "K", heads, D), _tokens(V, "V", heads, D)
-    if V.dtype != K.dtype:
-        raise TypeError("V must be %s, got %s" % (K.dtype, V.dtype))
+    bits, pages, heads, page, D, d = _cache(cache)
+    if d != torch._C._cuda_getDevice():
+        with torch.cuda.device(d):
+            return qa_kv_write(K, V, slots, cache, stream)
+    ldk, ldv = _tokens(K, "K", heads, D, d), _tokens(V, "V", heads, D, d)
     T = K.shape[0]
-    _shape(V, "V", K.shape)
-    _dev(slots, "slots", torch.int64)
-    _shape(slots, "slots", (T,))
+    if not (V.dtype == K.dtype and V.shape[0] == T and slots.dtype == torch.int64 and slots.shape == (T,) and
+            slots.get_device() == d and slots.is_contiguous()):
+        if V.dtype != K.dtype:
+            raise TypeError("V must be %s, got %s" % (K.dtype, V.dtype))
+        _shape(V, "V", K.shape)
+        _dev(slots, "slots", torch.int64)
+        _shape(slots, "slots", (T,))
+        _on(slots, "slots", d)
     kc, ks, vc, vs = cache
-    with _Device(_one_device(K, V, slots, kc, ks, vc, vs)):
-        _check("qa_kv_write",
-               lib().qa_kv_write(K.data_ptr(), ldk, V.data_ptr(), ldv, _DTYPE_CODE[K.dtype], T, slots.data_ptr(), bits,
-                                 pages, heads, page, D, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
-                                 _s(stream)))
+    r = lib().qa_kv_write(K.data_ptr(), ldk, V.data_ptr(), ldv, _DTYPE_CODE[K.dtype], T, slots.data_ptr(), bits, pages,
+                          heads, page, D, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), _sd(stream, d))
+    if r:
+        _check("qa_kv_write", r)
 
 
 def qa_kv_read(slots, cache, out_dtype=torch.float16, stream=None):
     """The keys and values at places of a cache (see qa_kv_write) -> (K, V) [T x heads x D] of out_dtype; zeros for a
     slot outside it."""
-    bits, pages, heads, page, D = _cache(cache)
-    _dev(slots, "slots", torch.int64)
-    if slots.dim() != 1:
-        raise ValueError("slots must be [T], got %s" % list(slots.shape))
+    bits, pages, heads, page, D, d = _cache(cache)
+    if d != torch._C._cuda_getDevice():
+        with torch.cuda.device(d):
+            return qa_kv_read(slots, cache, out_dtype, stream)
+    if not (slots.dtype == torch.int64 and slots.dim() == 1 and slots.get_device() == d and slots.is_contiguous()):
+        _dev(slots, "slots", torch.int64)
+        if slots.dim() != 1:
+            raise ValueError("slots must be [T], got %s" % list(slots.shape))
+        _on(slots, "slots", d)
     if out_dtype not in _DTYPE_CODE:
         raise TypeError("out_dtype must be fp32, fp16 or bf16, got %s" % out_dtype)
     T = slots.shape[0]
     K = _empty(stream, (T, heads, D), dtype=out_dtype, device=slots.device)
     V = torch.empty_like(K) if stream is None else _empty(stream, (T, heads, D), dtype=out_dtype, device=slots.device)
     kc, ks, vc, vs = cache
-    with _Device(_one_device(slots, kc, ks, vc, vs)):
-        _check("qa_kv_read",
-               lib().qa_kv_read(slots.data_ptr(), T, bits, pages, heads, page, D, kc.data_ptr(), ks.data_ptr(),
-                                vc.data_ptr(), vs.data_ptr(), K.data_ptr(), V.data_ptr(), _DTYPE_CODE[out_dtype],
-                                _s(stream)))
+    r = lib().qa_kv_read(slots.data_ptr(), T, bits, pages, heads, page, D, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(),
+                         vs.data_ptr(), K.data_ptr(), V.data_ptr(), _DTYPE_CODE[out_dtype], _sd(stream, d))
+    if r:
+        _check("qa_kv_read", r)
     return K, V
 
 
@@ -933,41 +933,52 @@ def qa_attn_decode(q, cache, table, lengths, scale=None, window=0, max_len=None,
     the pages of each sequence (rows may be strided), lengths i32 [B] its tokens; scale: 1 / sqrt(D) if not given;
     window: the last tokens that are seen (0: all); max_len: an upper bound of the lengths (the table's places if not
     given), by which the work is split over the card -- lengths past it count as it; out_dtype: q's if not given."""
-    bits, pages, heads, page, D = _cache(cache)
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a tensor [B x H x D]")
+    bits, pages, heads, page, D, d = _cache(cache)
+    if d != torch._C._cuda_getDevice():
+        with torch.cuda.device(d):
+            return qa_attn_decode(q, cache, table, lengths, scale, window, max_len, out_dtype, want_lse, out, workspace,
+                                  stream)
+    if q.dim() != 3:
+        raise ValueError("q must be [B x H x D], got %s" % list(q.shape))
     B, H, _ = q.shape
-    ldq = _tokens(q, "q", H, D)
+    ldq = _tokens(q, "q", H, D, d)
     ldt = _rows(table, "table", torch.int32)
-    _dev(lengths, "lengths", torch.int32)
-    _shape(lengths, "lengths", (B,))
     width = table.shape[1]
-    _shape(table, "table", (B, width))
-    if max_len is None:
-        max_len = width * page
+    if not (lengths.dtype == torch.int32 and lengths.shape == (B,) and lengths.is_contiguous() and
+            lengths.get_device() == d and table.shape[0] == B and table.get_device() == d):
+        _dev(lengths, "lengths", torch.int32)
+        _shape(lengths, "lengths", (B,))
+        _shape(table, "table", (B, width))
+        _on(lengths, "lengths", d)
+        _on(table, "table", d)
+    max_len = width * page if max_len is None else int(max_len)
     if out is None:
-        out = _empty(stream, (B, H, D), dtype=out_dtype or q.dtype, device=q.device)
+        dt = out_dtype or q.dtype
+        out = torch.empty_like(q, dtype=dt) if stream is None and q.is_contiguous() else \
+            _empty(stream, (B, H, D), dtype=dt, device=q.device)
     else:
         _dev(out, "out")
         _shape(out, "out", (B, H, D))
+        _on(out, "out", d)
     if out.dtype not in _DTYPE_CODE or (out_dtype is not None and out.dtype != out_dtype):
         raise TypeError("out must be fp32, fp16 or bf16 (out_dtype), got %s" % out.dtype)
     lse = _empty(stream, (B, H), dtype=torch.float32, device=q.device) if want_lse else None
     L = lib()
     if workspace is None:
-        ws, need = None, L.qa_attn_decode_workspace(B, H, heads, D, int(max_len), int(window))
+        ws, need = None, L.qa_attn_decode_workspace(B, H, heads, D, max_len, window)
         if need:
             workspace = _empty(stream, need, dtype=torch.uint8, device=q.device)
             ws = workspace.data_ptr()
     else:
+        _on(workspace, "workspace", d)
         ws, need = workspace.data_ptr(), workspace.numel()
     kc, ks, vc, vs = cache
-    with _Device(_one_device(q, kc, ks, vc, vs, table, lengths, out, workspace)):
-        _check("qa_attn_decode",
-               L.qa_attn_decode(q.data_ptr(), ldq, _DTYPE_CODE[q.dtype], B, H, bits, pages, heads, page, D,
-                                kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), table.data_ptr(), ldt, width,
-                                lengths.data_ptr(), int(max_len), int(window), D ** -0.5 if scale is None else scale,
-                                out.data_ptr(), _DTYPE_CODE[out.dtype], _a(lse), ws, need, _s(stream)))
+    r = L.qa_attn_decode(q.data_ptr(), ldq, _DTYPE_CODE[q.dtype], B, H, bits, pages, heads, page, D, kc.data_ptr(),
+                         ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), table.data_ptr(), ldt, width, lengths.data_ptr(),
+                         max_len, window, D ** -0.5 if scale is None else scale, out.data_ptr(), _DTYPE_CODE[out.dtype],
+                         _a(lse), ws, need, _sd(stream, d))
+    if r:
+        _check("qa_attn_decode", r)
     return (out, lse) if want_lse else out
 
 
@@ -978,34 +989,49 @@ def qa_qlinear_int8_act(Xq, s_x, Wq, s_w, bias=None, act=QA_ACT_NONE, residual=N
     Xq i8 [M x K], s_x f32 [M]; Wq i8 [N x K], s_w f32 [N]; bias f32 [N]; act one of QA_ACT_*; residual [M x N] of the
     output's type (rows may be strided); out: the given tensor (rows may be strided, it may be the residual itself) or
     a new one of out_dtype (of the residual's type if there is one)."""
-    _dev(Xq, "Xq", torch.int8)
-    _dev(s_x, "s_x", torch.float32)
-    _dev(Wq, "Wq", torch.int8)
-    _dev(s_w, "s_w", torch.float32)
-    M, K = Xq.shape
-    N = Wq.shape[0]
-    _shape(s_x, "s_x", (M,))
-    _shape(Wq, "Wq", (N, K))
-    _shape(s_w, "s_w", (N,))
+    d = Xq.get_device()
+    if d >= 0 and d != torch._C._cuda_getDevice():
+        with torch.cuda.device(d):
+            return qa_qlinear_int8_act(Xq, s_x, Wq, s_w, bias, act, residual, out_dtype, out, stream)
+    i8, f32, shape, wshape = torch.int8, torch.float32, Xq.shape, Wq.shape
+    if not (d >= 0 and len(shape) == 2 and len(wshape) == 2 and Xq.dtype == i8 and Wq.dtype == i8 and s_x.dtype == f32 and
+            s_w.dtype == f32 and wshape[1] == shape[1] and s_x.shape == shape[:1] and s_w.shape == wshape[:1] and
+            s_x.get_device() == d and Wq.get_device() == d and s_w.get_device() == d and Xq.is_contiguous() and
+            Wq.is_contiguous() and s_x.is_contiguous() and s_w.is_contiguous()):
+        _dev(Xq, "Xq", i8)
+        _dev(s_x, "s_x", f32)
+        _dev(Wq, "Wq", i8)
+        _dev(s_w, "s_w", f32)
+        if len(shape) != 2:
+            raise ValueError("Xq must be [M x K], got %s" % list(shape))
+        _shape(s_x, "s_x", shape[:1])
+        _shape(Wq, "Wq", (wshape[0], shape[1]))
+        _shape(s_w, "s_w", wshape[:1])
+        for t, name in ((s_x, "s_x"), (Wq, "Wq"), (s_w, "s_w")):
+            _on(t, name, d)
+    M, K = shape
+    N = wshape[0]
     if bias is not None:
-        _dev(bias, "bias", torch.float32)
+        _dev(bias, "bias", f32)
         _shape(bias, "bias", (N,))
+        _on(bias, "bias", d)
     ldo = ldr = N
     if out is None:
         out = _empty(stream, (M, N), dtype=out_dtype if residual is None else residual.dtype, device=Xq.device)
     else:
         ldo = _rows(out, "out", out.dtype)
         _shape(out, "out", (M, N))
+        _on(out, "out", d)
     if out.dtype not in _DTYPE_CODE:
         raise TypeError("out must be fp32, fp16 or bf16, got %s" % out.dtype)
     if residual is not None:
         ldr = _rows(residual, "residual", out.dtype)
         _shape(residual, "residual", (M, N))
-    with _Device(_one_device(Xq, s_x, Wq, s_w, bias, residual, out)):
-        _check("qa_qlinear_int8_act",
-               lib().qa_qlinear_int8_act(Xq.data_ptr(), s_x.data_ptr(), M, K, Wq.data_ptr(), s_w.data_ptr(), N, _a(bias),
-                                         int(act), _a(residual), ldr, out.data_ptr(), ldo, _DTYPE_CODE[out.dtype],
-                                         _s(stream)))
+        _on(residual, "residual", d)
+    r = lib().qa_qlinear_int8_act(Xq.data_ptr(), s_x.data_ptr(), M, K, Wq.data_ptr(), s_w.data_ptr(), N, _a(bias), act,
+                                  _a(residual), ldr, out.data_ptr(), ldo, _DTYPE_CODE[out.dtype], _sd(stream, d))
+    if r:
+        _check("qa_qlinear_int8_act", r)
     return out
 
 
