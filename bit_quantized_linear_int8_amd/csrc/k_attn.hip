@@ -359,7 +359,8 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs 
                                     (int64_t)a.group * a.D * EL);
         // 16 values to an MFMA step: int8 piece s is step s; an int4 piece of 32 codes is two,
         // its even and its odd codes, one of 16 is its even and then its odd codes
-        float x[NS][CC], top = 0.0f;
+        float x[NS][CC];
+        uint32_t bits = 0;                                   // of magnitudes: they order like them, infinities and NaNs above all
         constexpr int V = 16 / EL;                           // values of a load
         u32x4 raw[NS][CC / V];
 #pragma unroll
@@ -383,12 +384,13 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs 
 #pragma unroll
         for (int s = 0; s < NS; ++s)
 #pragma unroll
-            for (int k = 0; k < CC; ++k) top = fmaxf(top, __builtin_fabsf(x[s][k]));
-        top = fmaxf(top, __shfl_xor(top, 16, QA_WAVE));
-        top = fmaxf(top, __shfl_xor(top, 32, QA_WAVE));
+            for (int k = 0; k < CC; ++k) bits = max(bits, __builtin_bit_cast(uint32_t, x[s][k]) & 0x7fffffffu);
+        bits = max(bits, (uint32_t)__shfl_xor((int)bits, 16, QA_WAVE));
+        bits = max(bits, (uint32_t)__shfl_xor((int)bits, 32, QA_WAVE));
         // times 2^e the head's largest is in [2^21, 2^22)
-        const int e = top > 0.0f && top < __builtin_inff() ? 22 - __builtin_amdgcn_frexp_expf(top) : 0;
-        qscale = __builtin_ldexpf(a.scale2, -e - (BITS == 8 ? 0 : 4));
+        const bool fine = bits < 0x7f800000u;
+        const int e = bits != 0 && fine ? 22 - __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, bits)) : 0;
+        qscale = fine ? __builtin_ldexpf(a.scale2, -e - (BITS == 8 ? 0 : 4)) : __builtin_nanf("");
         const float f1 = __builtin_ldexpf(1.0f, e / 2), f2 = __builtin_ldexpf(1.0f, e - e / 2);
 #pragma unroll
         for (int i = 0; i < NM; ++i)

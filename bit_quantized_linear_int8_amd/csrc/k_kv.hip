@@ -118,10 +118,11 @@ __global__ __launch_bounds__(256) void k_kv_write(KvArgs a) {
         if (fine) {
             if (s >= 0x1p-120f) {
                 c = codes8_dyn(x[w], s, 1.0f / s);
-            } else {                                         // the reciprocal overflows or loses digits
-#pragma unroll
+            } else {                                         // the reciprocal overflows or loses digits, and
+#pragma unroll                                               // a scale of few digits lets quotients pass q_max
                 for (int e = 0; e < 8; ++e)
-                    c[e >> 2] |= ((uint32_t)(int)__builtin_rintf(x[w][e] / s) & 0xffu) << (8 * (e & 3));
+                    c[e >> 2] |= ((uint32_t)(int)__builtin_amdgcn_fmed3f(__builtin_rintf(x[w][e] / s), -QM, QM) & 0xffu)
+                                 << (8 * (e & 3));
             }
         }
         if (live) {

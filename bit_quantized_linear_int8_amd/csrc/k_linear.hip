@@ -40,7 +40,10 @@ enum Act { LINEAR = 0, SIGMA = 1, GELU = 2 };
 
 template <int ACT>
 __device__ __forceinline__ float activate(const LinearArgs& a, float x) {
-    if constexpr (ACT == SIGMA) return x * sigmoid(x * __builtin_fmaf(a.c3 * x, x, a.c1));
+    if constexpr (ACT == SIGMA) {
+        const float y = __builtin_amdgcn_fmed3f(x, -256.0f, 256.0f);    // (sigma is 0 or 1 there, and c3 times an infinity may be NaN)
+        return x * sigmoid(y * __builtin_fmaf(a.c3 * y, y, a.c1));
+    }
     if constexpr (ACT == GELU) {
         const float z = __builtin_fabsf(x);
         const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(z, 0.353553390593273762f, 1.0f));
@@ -54,7 +57,7 @@ __device__ __forceinline__ float activate(const LinearArgs& a, float x) {
         p = __builtin_fmaf(p, t, 0.2823997f);
         p = __builtin_fmaf(p, t, 0.28208503f);
         const float e = __builtin_amdgcn_exp2f(x * x * -0.72134752044448170368f);
-        return (x < 0.0f ? 0.0f : x) - z * (0.5f * t * p * e);
+        return (x < 0.0f ? 0.0f : x) - __builtin_fminf(z, 32.0f) * (0.5f * t * p * e);    // (from 16 on e is 0: no infinity times it)
     }
     return x < a.least ? a.least : x;                        // (a NaN stays)
 }

@@ -999,7 +999,7 @@ qa_status qa_kv_write(const void* K, int64_t ldk, const void* V, int64_t ldv, qa
         return fail(QA_ERR_SHAPE, "qa_kv_write: need 0 <= T <= 2^23, 1 <= heads <= 65535, D %% 16 == 0 in 16..256, page "
                                   "a power of two in 16..1024, token strides >= heads D in whole 16 bytes");
     if (T == 0) return ok();
-    if (!K || !V || !slots || !k_codes || !k_scales || !v_codes || !v_scales)
+    if (!K || !V || !slots || (pages > 0 && (!k_codes || !k_scales || !v_codes || !v_scales)))
         return fail(QA_ERR_NULL, "qa_kv_write: NULL pointer");
     if (!aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 8) || !cache_aligned(k_codes, k_scales, v_codes, v_scales))
         return fail(QA_ERR_ALIGN, "qa_kv_write: K, V, codes, scales 16-byte, slots 8-byte aligned");
@@ -1018,7 +1018,7 @@ qa_status qa_kv_read(const int64_t* slots, int64_t T, int32_t bits, int64_t page
         return fail(QA_ERR_SHAPE, "qa_kv_read: need 0 <= T <= 2^23, 1 <= heads <= 65535, D %% 16 == 0 in 16..256, page "
                                   "a power of two in 16..1024");
     if (T == 0) return ok();
-    if (!K || !V || !slots || !k_codes || !k_scales || !v_codes || !v_scales)
+    if (!K || !V || !slots || (pages > 0 && (!k_codes || !k_scales || !v_codes || !v_scales)))
         return fail(QA_ERR_NULL, "qa_kv_read: NULL pointer");
     if (!aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 8) || !cache_aligned(k_codes, k_scales, v_codes, v_scales))
         return fail(QA_ERR_ALIGN, "qa_kv_read: K, V, codes, scales 16-byte, slots 8-byte aligned");
@@ -1056,8 +1056,8 @@ qa_status qa_attn_decode(const void* q, int64_t ldq, qa_dtype q_dtype, int64_t B
                                   "<= 2^30, ldt >= width, ldq >= H D in whole 16 bytes, window >= 0");
     if (B == 0) return ok();
     const size_t need = qa_attn_decode_workspace(B, H, heads, D, max_len, window);
-    if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !lengths || !out || (width > 0 && !table) ||
-        (need > 0 && !workspace))
+    if (!q || (pages > 0 && (!k_codes || !k_scales || !v_codes || !v_scales)) || !lengths || !out ||
+        (width > 0 && !table) || (need > 0 && !workspace))
         return fail(QA_ERR_NULL, "qa_attn_decode: NULL pointer");
     if (!aligned(q, 16) || !cache_aligned(k_codes, k_scales, v_codes, v_scales) || !aligned(table, 4) ||
         !aligned(lengths, 4) || !aligned(out, 16) || !aligned(lse_or_null, 4) || (need > 0 && !aligned(workspace, kAlign)))

@@ -754,7 +754,8 @@ qa_status qa_qlinear_int8_lora(const int8_t* Xq, const float* s_x, const void* X
  * multiple of 16 in 16..256, page not a power of two in 16..1024, pages < 0 or
  * pages > 2^31 - 1, a token stride below heads D or not a multiple of 16
  * bytes; (QA_ERR_VALUE) bad dtype, bits not 8 or 4; NULL pointers; K, V, codes
- * and scales not 16-byte, slots not 8-byte aligned.  T == 0 is a no-op.
+ * and scales not 16-byte, slots not 8-byte aligned.  T == 0 is a no-op; a cache
+ * of no pages may have NULL pointers (and is one that no slot lies in).
  * ------------------------------------------------------------------------- */
 qa_status qa_kv_write(const void* K, int64_t ldk, const void* V, int64_t ldv, qa_dtype dtype, int64_t T,
                       const int64_t* slots, int32_t bits, int64_t pages, int32_t heads, int32_t page, int32_t D,
@@ -775,9 +776,10 @@ qa_status qa_kv_read(const int64_t* slots, int64_t T, int32_t bits, int64_t page
  * A sequence without a token to see (length 0, every page masked) gets a row of
  * zeros and lse = -infinity.  Scales and sums are fp32; scores and weights keep
  * about 2^-21 of their head's largest, and the output is rounded once.  A NaN
- * scale among the tokens that are seen makes the head's outputs NaN.
+ * scale among the tokens that are seen, or an infinity or NaN in the query, makes
+ * the head's outputs NaN.
  *   q        [B x H x D] of q_dtype (fp32, fp16 or bf16), token stride ldq
- *            elements, finite
+ *            elements
  *   table    i32 [B x width], row stride ldt: the pages of each sequence.  Entries
  *            past the last token's may hold anything
  *   lengths  i32 [B]: tokens in the cache, the new one's included

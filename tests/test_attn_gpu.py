@@ -235,6 +235,29 @@ def test_queries_of_extreme_magnitude():
         check(q, cache, values, table, lengths, 16, scale=0.125 / f)
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_queries_without_a_finite_value_reach_their_row_alone(dt, bits):
+    q, cache, values, table, lengths = make(3, [300, 0, 40], 4, 2, 64, 16, bits, dt, seed=21)
+    clean, clean_lse = qa.qa_attn_decode(q, cache, table, lengths, want_lse=True)
+    q = q.clone()
+    q[0, 1, 63] = math.inf
+    q[1, 2, 0] = math.nan                                    # (of a sequence without tokens: zeros as before)
+    q[2, 3, 17] = math.nan
+    q[2, 0, 5] = -math.inf
+    got, lse = qa.qa_attn_decode(q, cache, table, lengths, want_lse=True)
+    bad = torch.zeros(3, 4, dtype=torch.bool, device=DEV)
+    bad[0, 1] = bad[2, 3] = bad[2, 0] = True
+    assert torch.isnan(got[bad]).all() and torch.isnan(lse[bad]).all()
+    assert torch.equal(got[~bad], clean[~bad]) and torch.equal(lse[~bad], clean_lse[~bad])
+
+
+def test_a_cache_without_pages():
+    q, cache, values, table, lengths = make(2, [300, 40], 4, 2, 64, 16, 8, seed=22)
+    o, lse = qa.qa_attn_decode(q, tuple(t[:0] for t in cache), table, lengths, want_lse=True)
+    assert (o == 0).all() and (lse == -math.inf).all()
+
+
 def test_strided_tables_and_outputs():
     q, cache, values, table, lengths = make(3, [100, 250, 9], 4, 2, 128, 16, 8, seed=14)
     wide = torch.full((3, 64), -3, dtype=torch.int32, device=DEV)

@@ -161,6 +161,32 @@ def test_one_place_read_many_times():
     assert (k == k[0]).all() and (v == v[0]).all()
 
 
+@pytest.mark.parametrize("bits", [8, 4])
+def test_scales_of_few_digits(bits):
+    """Rows of fp32's smallest numbers: the scale is a few of its last steps, so quotients pass q_max and are clipped."""
+    heads, D, page = 2, 64, 16
+    top = torch.arange(1, 400, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    k = torch.randint(-10 ** 6, 10 ** 6, (top.numel(), heads, D), device=DEV, generator=g) % (top + 1)[:, None, None]
+    k[:, :, 9] = -top[:, None]
+    k = k.to(torch.int32)
+    k = torch.where(k < 0, -k + torch.iinfo(torch.int32).min, k).view(torch.float32)    # so many steps of 2^-149
+    cache = new_cache(25, heads, page, D, bits)
+    slots = torch.arange(top.numel(), device=DEV)
+    qa.qa_kv_write(k, -k, slots, cache)
+    check(cache, k, -k, slots, page, bits)
+
+
+def test_a_cache_without_pages():
+    for bits in (8, 4):
+        cache = new_cache(0, 2, 16, 64, bits)
+        k, v = inputs(5, 2, 64, "f16", 1)
+        slots = torch.arange(5, device=DEV)
+        qa.qa_kv_write(k, v, slots, cache)
+        kr, vr = qa.qa_kv_read(slots, cache)
+        assert (kr == 0).all() and (vr == 0).all()
+
+
 def test_no_tokens():
     cache = new_cache(2, 2, 16, 64, 8)
     before = [t.clone() for t in cache]

@@ -146,6 +146,19 @@ def test_rows_without_a_finite_scale(M, act):
     assert torch.equal(got[rest], clean[rest])
 
 
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("M,N", [(1, 100), (3, 5000), (100, 70)])
+def test_results_past_the_largest_number(M, N, act):
+    """Scales whose products pass fp32's largest number: +infinity stays one through every activation."""
+    x = make(M, 64, N, seed=6)
+    x[0].abs_()
+    x[2].abs_()
+    x[1].fill_(3e38)
+    x[3][::3] = 3e38
+    got = qa.qa_qlinear_int8_act(*x[:4], act=ACTS[act], out_dtype=torch.float32)
+    assert (got[:, ::3] == math.inf).all() and not torch.isnan(got).any()
+
+
 def test_the_integer_sum_is_exact():
     """K at the boundary's largest with codes of 127: sums of 2^31 and no rounding before the scales."""
     K, N = 131072, 40
