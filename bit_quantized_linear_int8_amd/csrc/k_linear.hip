@@ -327,10 +327,115 @@ __global__ __launch_bounds__(512, 2) void k_linear_few(LinearArgs a, int act) {
     __builtin_amdgcn_s_waitcnt(tile::vmcnt(0));                // no load is left to land in another block's LDS
 }
 
-// Many tokens: one tile of the product per block.  RES16: a 16-bit residual whose
-// rows allow vectors is requested before the product and waits in registers (24 for
-// the largest tile), so that its bytes come during the product instead of after it:
-// 2048 x 11008 x 4096 takes 107 us so against 124.
+// ---------------------------------------------------------------------------
+// Many tokens: one tile of the product per block.
+//
+// A stage's fragment reads are what a tile of few blocks per CU waits for most: with
+// Split the waves are two groups that take half of each stage's K each, so that a
+// wave's tile is twice as large and its reads per product half in one direction; the
+// groups exchange halves of their sums through LDS at the end.  (us, tiles as below
+// without and with it, graphs of calls with gelu and residual)
+//   K 4096   128 x 4096  14.1  12.2      512 x 4096   20.7  18.4      200 x 16000  28.9  26.8
+//            256 x 4096  15.1  12.9      777 x 4096   28.5  26.5      1024 x 4096  32.1  28.5
+//   K 11008  128 x 4096  29.0  24.3      777 x 4096   57.7  52.2
+// (4, 5 stages or half of the waves with larger tiles are no faster: 26 to 27 at 777 x
+// 4096; of its 26 about 4 are the epilogue's vector instructions, 40 a result with gelu.)
+// Tiles that have two blocks on each CU anyway are slower with it (2048 x 4096: 47.2
+// and 50.9), and at 128 x 192 their sums pass the registers.
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int WM, int WN, int STAGES>
+struct Whole : tile::Cfg<BM, BN, WM, WN, STAGES> {
+    static constexpr int KS = 1;
+};
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
+struct Split {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KS = 2, NW = WM * WN, NWA = KS * NW;
+    static constexpr int BK = 128, STAGES = STAGES_, THREADS = 64 * NWA;
+    static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+    static constexpr int INS = (BM + BN) / 8 / NWA;          // load instructions of a wave per stage
+    static constexpr int STAGE = (BM + BN) * BK, LDS = STAGES * STAGE;
+    static_assert(FM % 2 == 0 && TN % 16 == 0, "the groups halve a wave tile's fragments");
+    static_assert((BM + BN) % (8 * NWA) == 0 && BM % 8 == 0, "a stage's rows split evenly over the waves");
+    static_assert(BM * BN * 4 <= LDS && STAGES >= 3, "both groups' halves fit the stages");
+};
+
+// tile::product with each stage's K halved between two groups of waves: on return sum
+// holds the first (group 0) or second half of the wave tile's rows of fragments.
+template <class C, class RA, class RB>
+__device__ __forceinline__ void split_product(rsrc_t rsa, rsrc_t rsb, uint32_t K, uint8_t* smem, RA&& row_a, RB&& row_b,
+                                              v4i (&sum)[C::FM / 2][C::FN]) {
+    const int lane = threadIdx.x & 63, all = wave_id(), grp = all / C::NW, wave = all % C::NW;
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    uint32_t off[C::INS], ck[C::INS];
+#pragma unroll
+    for (int q = 0; q < C::INS; ++q) {
+        const int P = (q * C::NWA + all) * 64 + lane;        // 16-byte chunk of the stage
+        const int r = P >> 3, c = (P & 7) ^ (r & 7);
+        const uint32_t base = r < C::BM ? row_a(r) : row_b(r - C::BM);
+        off[q] = base == kOOB ? kOOB : base + c * 16;
+        ck[q] = c * 16;
+    }
+    const int nk = (int)((K + C::BK - 1) / C::BK);
+    auto issue = [&](int kt, int st) __attribute__((always_inline)) {    // (zeros past K: always as many loads)
+        const uint32_t k0 = (uint32_t)kt * C::BK;
+#pragma unroll
+        for (int q = 0; q < C::INS; ++q) {
+            const bool a = (q * C::NWA + all) * 8 < C::BM;
+            load_lds16(a ? rsa : rsb, k0 + ck[q] < K ? off[q] + k0 : kOOB, smem + st * C::STAGE + (q * C::NWA + all) * 1024);
+        }
+    };
+    v4i acc[C::FM][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < C::STAGES - 1; ++q) issue(q, q);
+    const int c = (lane >> 4) + 4 * grp;
+    int st = 0;
+    for (int kt = 0; kt < nk; ++kt) {
+        // this stage is there, and what this wave read of the one before has arrived: its buffer is filled anew
+        __builtin_amdgcn_s_waitcnt(tile::vmcnt(C::INS * (C::STAGES - 2)) & 0xf0ff);
+        tile::block_barrier();
+        issue(kt + C::STAGES - 1, st == 0 ? C::STAGES - 1 : st - 1);
+        const uint8_t* sa = smem + st * C::STAGE;
+        const uint8_t* sb = sa + C::BM * C::BK;
+        v4i fa[C::FM], fb[C::FN];
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+            fa[i] = *reinterpret_cast<const v4i*>(sa + tile::swz(wm * C::TM + i * 16 + (lane & 15), c));
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+            fb[j] = *reinterpret_cast<const v4i*>(sb + tile::swz(wn * C::TN + j * 16 + (lane & 15), c));
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        st = st + 1 == C::STAGES ? 0 : st + 1;
+    }
+    __builtin_amdgcn_s_waitcnt(tile::vmcnt(0));
+    __syncthreads();                                         // the stages are free
+    constexpr int H = C::FM / 2;
+    v4i* const mine = reinterpret_cast<v4i*>(smem) + all * (H * C::FN * 64) + lane;
+    const v4i* const theirs = reinterpret_cast<const v4i*>(smem) + ((1 - grp) * C::NW + wave) * (H * C::FN * 64) + lane;
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+            mine[(i * C::FN + j) * 64] = grp ? acc[i][j] : acc[H + i][j];
+            sum[i][j] = grp ? acc[H + i][j] : acc[i][j];
+        }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) sum[i][j] += theirs[(i * C::FN + j) * 64];
+}
+
+// RES16: a 16-bit residual whose rows allow vectors is requested before the product
+// and waits in registers (24 for the largest tile), so that its bytes come during
+// the product instead of after it: 2048 x 11008 x 4096 takes 103 us so against 119.
 template <class C, int ACT, bool RES16>
 __global__ __launch_bounds__(C::THREADS, 4) void k_linear_tile(LinearArgs a, int32_t tiles_m, int32_t tiles_n) {
     extern __shared__ uint8_t smem[];
@@ -340,26 +445,29 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_linear_tile(LinearArgs a, int
     const rsrc_t ra = make_rsrc(a.Xq + m0 * a.K, (a.M - m0) * a.K);
     const rsrc_t rw = make_rsrc(a.Wq + n0 * a.K, (a.N - n0) * a.K);
     const uint32_t K = (uint32_t)a.K;
-    const int lane = threadIdx.x & 63, wave = wave_id();
-    const int64_t mw = m0 + (wave / C::WN) * C::TM + (lane & 15), nw = n0 + (wave % C::WN) * C::TN + 4 * (lane >> 4);
-    u32x2 early[RES16 ? C::FM : 1][RES16 ? C::FN : 1];
+    constexpr int FM = C::FM / C::KS;                        // rows of fragments that the wave ends
+    const int lane = threadIdx.x & 63, wave = wave_id() % (C::WM * C::WN), grp = wave_id() / (C::WM * C::WN);
+    const int64_t mw = m0 + (wave / C::WN) * C::TM + grp * 16 * FM + (lane & 15);
+    const int64_t nw = n0 + (wave % C::WN) * C::TN + 4 * (lane >> 4);
+    u32x2 early[RES16 ? FM : 1][RES16 ? C::FN : 1];
     if constexpr (RES16) {
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i)
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < C::FN; ++j) {
                 const int64_t m = mw + i * 16 < a.M ? mw + i * 16 : a.M - 1, n = nw + j * 16 < a.N ? nw + j * 16 : 0;
                 early[i][j] = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.res) + m * a.ldr + n);
             }
     }
-    v4i acc[C::FM][C::FN];
-    tile::product<C>(
-        ra, rw, K, smem, [&](int r) -> uint32_t { return m0 + r < a.M ? (uint32_t)r * K : kOOB; },
-        [&](int r) -> uint32_t { return n0 + r < a.N ? (uint32_t)r * K : kOOB; }, acc);
-    float sx[C::FM];
+    v4i acc[FM][C::FN];
+    const auto row_a = [&](int r) -> uint32_t { return m0 + r < a.M ? (uint32_t)r * K : kOOB; };
+    const auto row_b = [&](int r) -> uint32_t { return n0 + r < a.N ? (uint32_t)r * K : kOOB; };
+    if constexpr (C::KS == 1) tile::product<C>(ra, rw, K, smem, row_a, row_b, acc);
+    else split_product<C>(ra, rw, K, smem, row_a, row_b, acc);
+    float sx[FM];
     v4f sw[C::FN], bi[C::FN];
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i) sx[i] = mw + i * 16 < a.M ? a.s_x[mw + i * 16] : 0.0f;
+    for (int i = 0; i < FM; ++i) sx[i] = mw + i * 16 < a.M ? a.s_x[mw + i * 16] : 0.0f;
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
         const int64_t n = nw + j * 16;
@@ -369,7 +477,7 @@ __global__ __launch_bounds__(C::THREADS, 4) void k_linear_tile(LinearArgs a, int
         if (a.bias) bi[j] = cols4(a.bias, n, cols, a.vecn);
     }
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i) {
+    for (int i = 0; i < FM; ++i) {
         const int64_t m = mw + i * 16;
         if (m >= a.M) continue;
 #pragma unroll
@@ -403,14 +511,14 @@ hipError_t run_tile(const LinearArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Tiles by how many of them there are, as in the adapters' linear.
+// Tiles by how many of them there are.
 template <int ACT>
 hipError_t run_tiles(const LinearArgs& a, hipStream_t st) {
     const int64_t small = ((a.M + 63) / 64) * ((a.N + 63) / 64), tiles = ((a.M + 127) / 128) * ((a.N + 127) / 128);
-    if (small <= 512) return run_tile<tile::Cfg<64, 64, 2, 4, 3>, ACT>(a, st);
-    if (tiles <= 256) return run_tile<tile::Cfg<64, 128, 2, 4, 3>, ACT>(a, st);
-    if (tiles <= 512) return run_tile<tile::Cfg<128, 128, 2, 4, 2>, ACT>(a, st);
-    return run_tile<tile::Cfg<128, 192, 2, 4, 2>, ACT>(a, st);
+    if (small <= 512) return run_tile<Split<64, 64, 2, 2, 3>, ACT>(a, st);
+    if (tiles <= 256) return run_tile<Split<128, 128, 2, 4, 3>, ACT>(a, st);
+    if (tiles <= 512) return run_tile<Whole<128, 128, 2, 4, 2>, ACT>(a, st);
+    return run_tile<Whole<128, 192, 2, 4, 2>, ACT>(a, st);
 }
 
 bool vec4(const void* p, int64_t ld, int dt) {
