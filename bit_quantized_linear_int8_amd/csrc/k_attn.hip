@@ -171,12 +171,14 @@ constexpr int vmcnt_only(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >
 
 // Stages of LDS for a wave and blocks on a CU, by D rounded up: at 64 four blocks hide
 // each other's waits better than stages do (33 sequences of 1000 tokens, 32 heads:
-// 26.2 us against 27.7 with two stages and 30.7 with three of three blocks); from 128
-// on two stages (4 sequences of up to 131072 in int4: 95 us of the call against
-// 96 with one stage and three blocks, 102 with three of each); at 256 the registers
-// leave one block.
-constexpr int stages(int DP) { return DP == 64 ? 1 : 2; }
-constexpr int blocks_on_cu(int DP) { return DP == 64 ? 4 : DP == 128 ? 2 : 1; }
+// 26.2 us against 27.7 with two stages and 30.7 with three of three blocks); at 128
+// two stages (4 sequences of up to 131072 in int4: 95 us of the call against
+// 96 with one stage and three blocks, 102 with three of each); at 256 two blocks of
+// one stage, against one block of two: short sequences wait (78 of 21 tokens, 19
+// heads: 30.6 us against 48.3), and long ones in int4 too (64 of up to 4000, 8 heads:
+// 79.9 against 103; in int8 121 and 126).
+constexpr int stages(int DP) { return DP == 128 ? 2 : 1; }
+constexpr int blocks_on_cu(int DP) { return DP == 64 ? 4 : 2; }
 
 __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
 
