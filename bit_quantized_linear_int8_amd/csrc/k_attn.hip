@@ -38,7 +38,7 @@
 // far inside fp32's range.
 //
 // The four waves of a block take tiles in turn and are joined through LDS.  Where
-// there are few sequences and heads, the work of all of them, in units of 128 tokens
+// there are few sequences and heads for their length, the work of all of them, in units of 128 tokens
 // of a head, is one line that the blocks that fit the card share evenly, whatever the
 // lengths are (a block finds its place by a sum over them); a head that reaches over
 // several blocks is joined by k_attn_join.  (Equal chunks of each sequence leave
@@ -746,14 +746,24 @@ namespace {
 
 constexpr int64_t kMaxShare = 1024;        // blocks that share the work: at most four on each CU
 
-// Whether the blocks share the work: where a block to each sequence and tile of heads
-// would not fill the card (768: with 1056 of 1000 tokens, 40 us shared and 31 not; and
-// sequences are longer than a unit), as far as the sums
-// over sequences fit a block and 31 bits.
+// Whether the blocks share the work, as far as the sums over sequences fit a block and
+// 31 bits.  Shares balance the card, but a block that takes up several sequences
+// begins and ends each, and the join is a launch.  By sequences of 8 key heads and
+// their longest length (us; a block to each sequence and head, and shared; lengths
+// evenly spread below it; heads of 128, 32 queries, 8 bits):
+//       1000          2000          4000          8000
+//    1  13.4  11.4    21.1  11.9    36.8  13.4    66.2  16.8
+//    8  14.6  14.4    22.5  17.7    37.4  24.3    66.9  31.8
+//   32  15.5  21.9    23.7  28.2    39.8  41.2    71.0  63.7
+//   64  20.8  35.0    33.5  49.9    59.0  70.9     109   111
+//   90  28.8  46.8    42.8  60.3    74.7  90.3     139   145
+// The lengths are not known here, and where one is much longer than the others only the
+// first column grows with it, by 7.5 us for 1000 tokens: the border lies below the
+// point where evenly spread ones are equal.
 bool shared_work(int64_t B, int32_t H, int32_t heads, int64_t max_len, int32_t window) {
     const int64_t group = H / heads, pairs = B * heads * ((group + 15) / 16);
     const int64_t span = window > 0 && (int64_t)window + 31 < max_len ? (int64_t)window + 31 : max_len;
-    return span > kUnit && B <= 1024 && pairs < 768 && pairs * ((span + kUnit - 1) / kUnit) < ((int64_t)1 << 30);
+    return B <= 1024 && pairs < 768 && span > 512 + 7 * pairs && pairs * ((span + kUnit - 1) / kUnit) < ((int64_t)1 << 30);
 }
 
 template <int BITS, int DP>

@@ -147,6 +147,47 @@ def test_splits(B, n, bits):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("D", [64, 128, 160])
+@pytest.mark.parametrize("B,H,heads", [(1, 4, 2), (7, 20, 1), (60, 6, 3), (700, 1, 1), (1024, 2, 1)])
+def test_work_shared_over_short_sequences(B, H, heads, D, bits):
+    """Tables far wider than the sequences: shares that hold many of them, of all lengths from 0 on, and one that is long."""
+    lengths = [(i * 131 + 77) % 260 if i % 5 else 0 for i in range(B)]
+    lengths[B // 3] = 1900
+    x = make(B, lengths, H, heads, D, 32, bits, "f16", seed=23, width=300)
+    a = check(*x, 32)
+    b = check(*x, 32)                                        # the same bits again
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    x[3][B // 2:, :3] = -1                                   # sequences whose first pages, or all, are gone
+    check(*x, 32)
+    x[4].zero_()
+    got, lse = qa.qa_attn_decode(x[0], x[1], x[3], x[4], want_lse=True)
+    assert (got == 0).all() and (lse == -math.inf).all()
+
+
+def test_graphs_on_one_workspace():
+    """Two captured calls of shared work on one workspace, replayed in turn with the lengths going on between."""
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+    calls, graphs, outs = [], [], []
+    for i, (B, H, heads) in enumerate([(3, 8, 2), (40, 4, 4)]):
+        q, cache, values, table, lengths = make(B, [1500] * B, H, heads, 64, 16, 8, seed=24 + i, width=600)
+        lengths -= torch.arange(B, dtype=torch.int32, device=DEV) * 30
+        calls.append((q, cache, table, lengths))
+        assert qa.qa_attn_decode_workspace(B, H, heads, 64, 9600) > 0
+        qa.qa_attn_decode(*calls[i], workspace=ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            outs.append(qa.qa_attn_decode(*calls[i], workspace=ws, want_lse=True))
+    for turn in range(4):
+        for i in (0, 1):
+            calls[i][3].sub_(17 * turn)
+            ws.fill_(0xff)                                   # (NaNs: nothing in it lasts from call to call)
+            graphs[i].replay()
+            want = qa.qa_attn_decode(*calls[i], want_lse=True)
+            assert torch.equal(outs[i][0], want[0]) and torch.equal(outs[i][1], want[1])
+
+
 @pytest.mark.parametrize("window", [1, 2, 16, 31, 32, 33, 100, 128, 1000, 4096])
 def test_windows(window):
     lengths = [4000, 100, 33, 32, 1, 0, 129, 2047]
