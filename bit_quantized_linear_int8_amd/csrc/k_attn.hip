@@ -7,8 +7,9 @@
 // over the tokens t of a sequence (inside its window, on a page that the cache
 // has).  The heads that share a key head are the 16 columns of one MFMA tile.
 //
-// A wave takes 32 tokens at a time through stages of LDS of its own (no barrier in
-// the loop), filled by direct global -> LDS loads of whole lines, NST tiles ahead:
+// A wave takes 32 tokens at a time through a stage of LDS of its own (no barrier in
+// the loop), filled by direct global -> LDS loads of whole lines while the tile before
+// is worked on in registers:
 //   - keys are the rows of A of an int8 product: lane (m, c) takes 16-byte pieces
 //     c, c + 4, ... of token m (and 16 + m), as they are (int4: the nibbles in the
 //     upper halves of bytes, 16 times the codes);
@@ -169,16 +170,13 @@ __device__ __forceinline__ void load_lds4(const void* p, void* lds) {
 // s_waitcnt immediate waiting for vmcnt <= n only (gfx9 encoding)
 constexpr int vmcnt_only(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 
-// Stages of LDS for a wave and blocks on a CU, by D rounded up: at 64 four blocks hide
-// each other's waits better than stages do (33 sequences of 1000 tokens, 32 heads:
-// 26.2 us against 27.7 with two stages and 30.7 with three of three blocks); at 128
-// two stages (4 sequences of up to 131072 in int4: 95 us of the call against
-// 96 with one stage and three blocks, 102 with three of each); at 256 two blocks of
-// one stage, against one block of two: short sequences wait (78 of 21 tokens, 19
-// heads: 30.6 us against 48.3), and long ones in int4 too (64 of up to 4000, 8 heads:
-// 79.9 against 103; in int8 121 and 126).
-constexpr int stages(int DP) { return DP == 128 ? 2 : 1; }
-constexpr int blocks_on_cu(int DP) { return DP == 64 ? 4 : 2; }
+// Blocks on a CU, by D rounded up: as many as the registers hold, but for 128 in int8,
+// where two bring long sequences in faster than three (64 ragged ones up to 8192:
+// 105.6 us of the call against 113; 200 of up to 200 tokens 27.3 against 23.6; 4 of up to
+// 131072 in int4: 89.6 with three, 93.3 with two).  A second stage of LDS for each wave
+// was no faster with any of them (107.4 and 94.2): a stage is read into registers at
+// once and filled again, so that two tiles of each wave are under way as it is.
+constexpr int blocks_on_cu(int DP, int BITS) { return DP == 64 ? 4 : DP == 128 && BITS == 4 ? 3 : 2; }
 
 __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
 
@@ -187,7 +185,7 @@ __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), f
 // DP: D rounded up to 64, 128 or 256 (what lies behind D meets queries of 0, or is
 // not stored).  F32: fp32 queries.
 template <int BITS, int DP, bool F32>
-__global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs a) {
+__global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(AttnArgs a) {
     constexpr int CC = BITS == 8 || DP == 64 ? 16 : 32;      // codes of a lane's piece of a key
     constexpr int NS = DP / (4 * CC);                        // pieces of a lane
     constexpr int PB = CC * BITS / 8;                        // bytes of a piece
@@ -198,9 +196,9 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs 
     constexpr int DPB = DP * BITS / 8, NCH = DPB / 16;       // a row in LDS, its chunks
     constexpr int INS = 16 * DPB < 1024 ? 1 : 16 * DPB / 1024;    // loads of 16 rows
     constexpr int HALF = INS * 1024;
-    constexpr int SB = 4 * HALF + 256, NST = stages(DP);
+    constexpr int SB = 4 * HALF + 256;                       // a stage
     constexpr int RED = 4 * 16 * (DP / 4 + 1) * 16;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[4 * NST * SB > RED ? 4 * NST * SB : RED];
+    __shared__ __attribute__((aligned(16))) uint8_t smem[4 * SB > RED ? 4 * SB : RED];
     auto swz = [](int r) { return (NCH <= 8 ? r / (8 / (NCH <= 8 ? NCH : 8)) : r) & (NCH - 1); };
     __shared__ float st_m[4][16], st_l[4][16], st_e[4][16], inv_l[16];
     __shared__ int plan[6];
@@ -315,9 +313,9 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs 
                                                  p < 0 ? 0 : (int)(((uint32_t)page - at) * RB), 0x00020000);
     };
 
-    // A stage: keys and values of two times 16 tokens, rows of DPB bytes whose 16-byte chunk c is at c ^ swz(row), so
+    // The stage: keys and values of two times 16 tokens, rows of DPB bytes whose 16-byte chunk c is at c ^ swz(row), so
     // that reads of 16 rows meet all banks; behind them 32 scales of keys and 32 of values.
-    uint8_t* const mine = smem + wave * NST * SB;
+    uint8_t* const mine = smem + wave * SB;
     uint32_t src[INS];                                       // a lane's part of a load of 16 rows
 #pragma unroll
     for (int n = 0; n < INS; ++n) {
@@ -325,34 +323,27 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs 
         src[n] = rr < 16 && (uint32_t)(16 * c) < RB ? (uint32_t)rr * RB + 16 * c : kOOB;
     }
     const float* const scales_at = (lane < 32 ? a.ks : a.vs) + (((int64_t)h << a.shift) + m16);
-    auto fill = [&](int st, int t, int q0, int q1) __attribute__((always_inline)) {
-        uint8_t* const to = mine + st * SB;
+    auto fill = [&](int t, int q0, int q1) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const rsrc_t rk = rows_of(a.kc, t + 16 * u, u ? q1 : q0), rv = rows_of(a.vc, t + 16 * u, u ? q1 : q0);
 #pragma unroll
             for (int n = 0; n < INS; ++n) {
-                load_lds16(rk, src[n], to + u * HALF + n * 1024);
-                load_lds16(rv, src[n], to + (2 + u) * HALF + n * 1024);
+                load_lds16(rk, src[n], mine + u * HALF + n * 1024);
+                load_lds16(rv, src[n], mine + (2 + u) * HALF + n * 1024);
             }
         }
         // scales: 16 tokens of u to 16 lanes, keys' and then values' (of page 0 where there is none: not looked at)
         const int64_t r0 = (((int64_t)(q0 < 0 ? 0 : q0) * a.heads) << a.shift) + ((uint32_t)t & (uint32_t)(page - 1));
         const int64_t r1 = (((int64_t)(q1 < 0 ? 0 : q1) * a.heads) << a.shift) + ((uint32_t)(t + 16) & (uint32_t)(page - 1));
-        load_lds4(scales_at + (lane & 16 ? r1 : r0), to + 4 * HALF);
+        load_lds4(scales_at + (lane & 16 ? r1 : r0), mine + 4 * HALF);
     };
-    constexpr int PER = 4 * INS + 1;                         // loads of a stage, always as many
 
-    // the wave's first tiles, and the queries while they come
+    // the wave's first tile, and the queries while it comes
     int t0 = lo + 32 * wave, it = 0;
     int ent = entries(t0), ent2 = entries(t0 + 32 * 128);
-    int p0[NST], p1[NST];
-#pragma unroll
-    for (int s = 0; s < NST; ++s) {
-        p0[s] = page_of(t0 + 128 * s, __builtin_amdgcn_readlane(ent, 2 * s));
-        p1[s] = page_of(t0 + 128 * s + 16, __builtin_amdgcn_readlane(ent, 2 * s + 1));
-        fill(s, t0 + 128 * s, p0[s], p1[s]);
-    }
+    int p0 = page_of(t0, __builtin_amdgcn_readlane(ent, 0)), p1 = page_of(t0 + 16, __builtin_amdgcn_readlane(ent, 1));
+    fill(t0, p0, p1);
     v4i qd[3][NM];                                           // digits of 1, 256, 65536
     float qscale;
     {
@@ -436,12 +427,10 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs 
         const int rr = 4 * c4 + j, byte = m16 * VB;
         av[j] = 2 * HALF + rr * DPB + (((byte >> 4) ^ swz(rr)) << 4) + (byte & 15);
     }
-    int st = 0;
     while (t0 < hi) {
-        // this tile's stage into registers
-        __builtin_amdgcn_s_waitcnt(vmcnt_only(PER * (NST - 1)));
+        // the stage into registers
+        __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
         asm volatile("" ::: "memory");
-        const uint8_t* const from_ = mine + st * SB;
         u32x4 kq[2][NS];
         uint32_t vq[8][VW];
         v4f ks[2], vs[2];
@@ -449,18 +438,18 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs 
         for (int u = 0; u < 2; ++u) {
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
-                const uint8_t* q = from_ + u * HALF + ak[i];
+                const uint8_t* q = mine + u * HALF + ak[i];
                 if constexpr (PB == 16) kq[u][i] = *reinterpret_cast<const u32x4*>(q);
                 else {
                     const u32x2 w = *reinterpret_cast<const u32x2*>(q);
                     kq[u][i] = u32x4{w[0], w[1], 0u, 0u};
                 }
             }
-            ks[u] = *reinterpret_cast<const v4f*>(from_ + 4 * HALF + 64 * u + 16 * c4);
-            vs[u] = *reinterpret_cast<const v4f*>(from_ + 4 * HALF + 128 + 64 * u + 16 * c4);
+            ks[u] = *reinterpret_cast<const v4f*>(mine + 4 * HALF + 64 * u + 16 * c4);
+            vs[u] = *reinterpret_cast<const v4f*>(mine + 4 * HALF + 128 + 64 * u + 16 * c4);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint8_t* q = from_ + u * HALF + av[j];
+                const uint8_t* q = mine + u * HALF + av[j];
                 uint32_t* o = vq[4 * u + j];
                 if constexpr (VB == 2) o[0] = *reinterpret_cast<const uint16_t*>(q);
                 else if constexpr (VB == 4) o[0] = *reinterpret_cast<const uint32_t*>(q);
@@ -473,21 +462,19 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs 
                 }
             }
         }
-        // and the stage, once it is read, for the tile NST further on
+        // and the next tile into it, once it is read
         __builtin_amdgcn_s_waitcnt(0xC07F);                  // lgkmcnt(0)
         asm volatile("" ::: "memory");
-        const int q0 = p0[0], q1 = p1[0];                    // this tile's pages
+        const int q0 = p0, q1 = p1;                          // this tile's pages
         {
-            const int at = it + NST, tn = t0 + 128 * NST;
+            const int at = it + 1, tn = t0 + 128;
             if ((at & 31) == 0) {                            // the next 32 tiles' entries
                 ent = ent2;
                 ent2 = entries(tn + 32 * 128);
             }
-#pragma unroll
-            for (int s = 0; s + 1 < NST; ++s) p0[s] = p0[s + 1], p1[s] = p1[s + 1];
-            p0[NST - 1] = page_of(tn, __builtin_amdgcn_readlane(ent, 2 * (at & 31)));
-            p1[NST - 1] = page_of(tn + 16, __builtin_amdgcn_readlane(ent, 2 * (at & 31) + 1));
-            fill(st, tn, p0[NST - 1], p1[NST - 1]);
+            p0 = page_of(tn, __builtin_amdgcn_readlane(ent, 2 * (at & 31)));
+            p1 = page_of(tn + 16, __builtin_amdgcn_readlane(ent, 2 * (at & 31) + 1));
+            fill(tn, p0, p1);
         }
 
         // scores as exact integers / 2^k, with their factors
@@ -619,7 +606,6 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs 
         }
         t0 += 128;
         ++it;
-        st = st + 1 == NST ? 0 : st + 1;
     }
     __builtin_amdgcn_s_waitcnt(vmcnt_only(0));               // no load may land in what the waves share below
     __syncthreads();
@@ -671,7 +657,7 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP)) void k_attn_decode(AttnArgs 
     left -= k1 - k0;
     k0 = 0;
     ++b;
-    if (left > 0) __syncthreads();                           // the stages' LDS is free again
+    if (left > 0) __syncthreads();                           // the stages are free again
     }
 }
 
@@ -805,7 +791,7 @@ hipError_t launch_attn_decode(const void* q, int64_t ldq, int q_dtype, int64_t B
     a.out = out; a.dt = out_dtype; a.lse = lse;
     const bool shared = shared_work(B, H, c.heads, max_len, window);
     if (shared) {
-        const int64_t fit = 256 * blocks_on_cu(c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256), HG = (int64_t)c.heads * a.gtiles;
+        const int64_t fit = 256 * blocks_on_cu(c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256, c.bits), HG = (int64_t)c.heads * a.gtiles;
         a.share = (int32_t)(fit > HG ? fit / HG : 1);
         const int64_t slots = (a.share + B) * HG;
         a.part = static_cast<float*>(scratch);
