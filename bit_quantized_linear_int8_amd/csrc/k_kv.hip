@@ -9,7 +9,7 @@
 // codes are packed eight to a word like every int4 row of this library.
 //
 // A row of D values is eight values to a lane and 8, 16 or 32 lanes; the maximum
-// over them is the only exchange (DPP).  The lanes of a token do its key and its
+// over them is the only exchange (moves between lanes).  The lanes of a token do its key and its
 // value, so a place is looked up once and two rows are in flight.  Consecutive
 // rows of a block are consecutive tokens of one head: prompts then write whole
 // pieces of a page, codes and scales.
@@ -33,21 +33,64 @@ struct KvArgs {
 
 __device__ __forceinline__ float bf2f(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
 
+// Eight values of a row as they stand in memory.
 template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float* x) {
-    if constexpr (DT == 0) {
-        const v4f* q = reinterpret_cast<const v4f*>(static_cast<const float*>(p) + at);
-        const v4f a = q[0], b = q[1];
+struct Raw {
+    u32x4 w[DT == 0 ? 2 : 1];
+};
+template <int DT>
+__device__ __forceinline__ Raw<DT> load8(const void* p, int64_t at) {
+    Raw<DT> r;
+    const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(p) + at * (DT == 0 ? 4 : 2));
+    r.w[0] = q[0];
+    if constexpr (DT == 0) r.w[1] = q[1];
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ void widen8(const Raw<DT>& r, float* x) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
-    } else {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint16_t u = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (DT == 0) {
+            const uint32_t u = r.w[j >> 2][j & 3];
+            x[j] = __builtin_bit_cast(float, u);
+        } else {
+            const uint16_t u = (uint16_t)(r.w[0][j >> 1] >> (16 * (j & 1)));
             x[j] = DT == 1 ? h2f(u) : bf2f(u);
         }
     }
+}
+// The bits of the largest magnitude of the eight, as a number of the type: patterns order like the values,
+// infinities and NaNs above all.
+template <int DT>
+__device__ __forceinline__ uint32_t largest8(const Raw<DT>& r) {
+    uint32_t m = 0;
+    if constexpr (DT == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, r.w[j >> 2][j & 3] & 0x7fffffffu);
+        return m;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = pk_max_u16(m, r.w[0][j] & 0x7fff7fffu);
+    return max(m & 0xffffu, m >> 16);
+}
+// The largest over N = 8, 16 or 32 lanes side by side: moves within rows of 16 lanes, and between two of them.
+template <int N>
+__device__ __forceinline__ uint32_t largest_of(uint32_t m) {
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));     // lane ^ 1
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));     // lane ^ 2
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, false));    // the other four of eight
+    if constexpr (N >= 16) m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xF, 0xF, false));
+    if constexpr (N == 32) m = max(m, (uint32_t)__builtin_amdgcn_ds_swizzle((int)m, 0x401F));    // lane ^ 16
+    return m;
+}
+// m / Q for a whole number Q, rounded to nearest, for m of at least 2^-107: the product with the rounded reciprocal is
+// within one step of the quotient, and its exact remainder times the reciprocal rounds it (all 2^23 significands
+// of m agree with the division for 127 and for 7).
+template <int Q>
+__device__ __forceinline__ float divide_by(float m) {
+    constexpr float r = 1.0f / Q;
+    const float q = m * r;
+    return __builtin_fmaf(__builtin_fmaf(-q, (float)Q, m), r, q);
 }
 
 template <bool NT, class T>
@@ -84,7 +127,10 @@ __device__ __forceinline__ int64_t row_of(const KvArgs& a, int64_t slot, int h) 
     return (((slot >> a.shift) * a.heads + h) << a.shift) + (slot & ((1 << a.shift) - 1));
 }
 
-// LPR lanes to a row, 256 / LPR tokens of head blockIdx.y to a block.
+// LPR lanes to a row, 256 / LPR tokens of head blockIdx.y to a block.  16411 tokens of 8
+// heads of 128, bf16 to 8 bits: 23.4 us, 4.4 TB/s (a large copy reaches 4.9); 8192 of 32
+// heads of 64, fp16 to 4 bits: 22.4.  With divisions for the scale and its reciprocal, maxima
+// exchanged through LDS and codes packed byte by byte instructions bound it: 26.1 and 24.9.
 template <int DT, int BITS, int LPR>
 __global__ __launch_bounds__(256) void k_kv_write(KvArgs a) {
     const int j = threadIdx.x % LPR;
@@ -93,46 +139,47 @@ __global__ __launch_bounds__(256) void k_kv_write(KvArgs a) {
     const int64_t slot = t < a.T ? a.slots[t] : -1;
     const bool row = slot >= 0 && slot < a.places;           // the same for a row's lanes
     const bool live = row && j * 8 < a.D;
-    float x[2][8];
+    Raw<DT> raw[2] = {};
+    if (live)
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[w][e] = 0.0f;
-        if (live) load8<DT>(a.x[w], t * a.ld[w] + (int64_t)h * a.D + j * 8, x[w]);
-    }
+        for (int w = 0; w < 2; ++w) raw[w] = load8<DT>(a.x[w], t * a.ld[w] + (int64_t)h * a.D + j * 8);
     const int64_t at = row ? row_of(a, slot, h) : 0;
-    constexpr float QM = BITS == 8 ? 127.0f : 7.0f;
+    constexpr int QM = BITS == 8 ? 127 : 7;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-        // magnitudes as bit patterns: they order like the values, infinities and NaNs above all
-        uint32_t m = 0;
+        const uint32_t bits = largest_of<LPR>(largest8<DT>(raw[w]));
+        const float m = DT == 0 ? __builtin_bit_cast(float, bits) : DT == 1 ? h2f((uint16_t)bits) : bf2f((uint16_t)bits);
+        float x[8];
+        widen8<DT>(raw[w], x);
+        float y[8];                                          // 4 bits: even values, then odd ones
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = max(m, __builtin_bit_cast(uint32_t, x[w][e]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = LPR / 2; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, QA_WAVE));
-        const bool fine = m < 0x7f800000u;
-        float s = __builtin_bit_cast(float, m) / QM;
-        if (s == 0.0f) s = 1.0f;
-        if (!fine) s = __builtin_nanf("");
+        for (int e = 0; e < 8; ++e) y[e] = x[BITS == 8 ? e : 2 * (e & 3) + (e >> 2)];
+        float s = divide_by<QM>(m);
         u32x2 c = u32x2{0u, 0u};
-        if (fine) {
-            if (s >= 0x1p-120f) {
-                c = codes8_dyn(x[w], s, 1.0f / s);
-            } else {                                         // the reciprocal overflows or loses digits, and
-#pragma unroll                                               // a scale of few digits lets quotients pass q_max
-                for (int e = 0; e < 8; ++e)
-                    c[e >> 2] |= ((uint32_t)(int)__builtin_amdgcn_fmed3f(__builtin_rintf(x[w][e] / s), -QM, QM) & 0xffu)
-                                 << (8 * (e & 3));
-            }
+        if (m >= 0x1p-107f && m < __builtin_inff()) {
+            // (the reciprocal's own step more than codes8_dyn counts with is 2^-17 of the sum, far inside its margin)
+            c = codes8_dyn(y, s, __builtin_amdgcn_rcpf(s));
+        } else if (m < 0x1p-107f) {                          // the reciprocal overflows or loses digits, and
+            s = m / (float)QM;                               // a scale of few digits lets quotients pass q_max
+            if (s == 0.0f) s = 1.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                c[e >> 2] |= ((uint32_t)(int)__builtin_amdgcn_fmed3f(__builtin_rintf(y[e] / s), -(float)QM, (float)QM) & 0xffu)
+                             << (8 * (e & 3));
+        } else {
+            s = __builtin_nanf("");
         }
         if (live) {
             if constexpr (BITS == 8) *reinterpret_cast<u32x2*>(a.codes[w] + at * a.D + j * 8) = c;
-            else *reinterpret_cast<uint32_t*>(a.codes[w] + at * (a.D / 2) + j * 4) = pack_nibbles(c);
+            else *reinterpret_cast<uint32_t*>(a.codes[w] + at * (a.D / 2) + j * 4) =
+                (c[0] & 0x0f0f0f0fu) | ((c[1] & 0x0f0f0f0fu) << 4);
         }
         if (row && j == 0) a.scales[w][at] = s;
     }
 }
 
+// 16411 tokens of 8 heads of 128 out of 8 bits, which the write before left in the cache:
+// 17 us, 6 TB/s; 24 contexts of up to 8192 out of 4 bits: 132 us, 4.9 TB/s.
 // NT: codes and outputs with the non-temporal hint, for outputs that pass the 256 MB
 // cache (8 heads of 128, 8 bits, fp16: 65536 tokens and a kernel that reads them 137
 // us against 142; 16384 tokens, whose outputs that kernel finds in the cache, 39
