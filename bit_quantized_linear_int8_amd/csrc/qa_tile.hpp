@@ -1,5 +1,5 @@
-// qa_tile.hpp -- the int8 tile product shared by the grouped and the adapter
-// linears: acc[FM][FN] = A rows x B rows^T with rows picked by the caller.
+// qa_tile.hpp -- the int8 tile product shared by the grouped, the adapter and the
+// epilogue linears: acc[FM][FN] = A rows x B rows^T with rows picked by the caller.
 //
 // Both operands are K-contiguous int8 rows.  A stage holds BK = 128 bytes of K
 // of the tile's BM rows of A followed by its BN rows of B; it is filled by
