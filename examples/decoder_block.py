@@ -3,8 +3,8 @@
 
     python examples/decoder_block.py            # on a GPU; prints both steps' times and their distance from fp32
 
-The projection stands where attention's input and output projections would; attention itself is not part of this
-library.
+The projection stands where attention's input and output projections would; attention itself, on a quantized cache, is
+in attention_step.py.
 """
 import os
 import sys
