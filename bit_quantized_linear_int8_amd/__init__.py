@@ -970,8 +970,9 @@ def qa_attn_decode(q, cache, table, lengths, scale=None, window=0, max_len=None,
             workspace = _empty(stream, need, dtype=torch.uint8, device=q.device)
             ws = workspace.data_ptr()
     else:
+        _dev(workspace, "workspace")
         _on(workspace, "workspace", d)
-        ws, need = workspace.data_ptr(), workspace.numel()
+        ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     kc, ks, vc, vs = cache
     r = L.qa_attn_decode(q.data_ptr(), ldq, _DTYPE_CODE[q.dtype], B, H, bits, pages, heads, page, D, kc.data_ptr(),
                          ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), table.data_ptr(), ldt, width, lengths.data_ptr(),

@@ -378,3 +378,20 @@ def test_refusals():
     with pytest.raises(qa.QAError):                          # a workspace that is too small
         x = make(1, [5000], 4, 2, 64, 16, 8)
         qa.qa_attn_decode(x[0], x[1], x[3], x[4], workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+
+
+def test_refused_workspaces():
+    q, cache, values, table, lengths = make(2, [900, 700], 4, 2, 64, 16, 8, seed=26, width=100)
+    need = qa.qa_attn_decode_workspace(2, 4, 2, 64, 1600)
+    assert need > 0
+    with pytest.raises(ValueError):                          # as many elements, not as many bytes
+        qa.qa_attn_decode(q, cache, table, lengths, workspace=torch.empty(1, dtype=torch.uint8, device=DEV).expand(need))
+    with pytest.raises(TypeError):
+        qa.qa_attn_decode(q, cache, table, lengths, workspace=torch.empty(need, dtype=torch.uint8))
+    with pytest.raises(qa.QAError):
+        qa.qa_attn_decode(q, cache, table, lengths, workspace=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
+    with pytest.raises(qa.QAError):                          # aligned to 256 bytes
+        qa.qa_attn_decode(q, cache, table, lengths, workspace=torch.empty(need + 64, dtype=torch.uint8, device=DEV)[16:])
+    want = qa.qa_attn_decode(q, cache, table, lengths)
+    words = torch.empty(need // 4, dtype=torch.float32, device=DEV)
+    assert torch.equal(qa.qa_attn_decode(q, cache, table, lengths, workspace=words), want)
