@@ -46,7 +46,7 @@
 // blocks of unequal size: half the card's waves were idle with ragged lengths.)
 //
 // What bounds it: 64 ragged sequences of up to 8192 (8 key heads of 128, 4 queries each,
-// 8 bits, 580 MB) take 102 us, 5.7 TB/s, and 6.6 the join: the memory (the loads alone take
+// 8 bits, 580 MB) take 97 to 103 us, 5.6 to 6.0 TB/s, and 7 the join: the memory (the loads alone take
 // no less).  4 of up to 131072 in 4 bits with 8 queries each take 82 to 91, 5.0 to 5.5 TB/s:
 // the loads alone and the arithmetic alone (vector instructions busy for 61% of
 // the time, most of them values' codes made fp16) are 85 each.  A single sequence of 4096 is
@@ -182,9 +182,10 @@ constexpr int vmcnt_only(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >
 // Blocks on a CU, by D rounded up: as many as the registers hold, but for 128 in int8,
 // where two bring long sequences in faster than three (64 ragged ones up to 8192:
 // 105.6 us of the call against 113; 200 of up to 200 tokens 27.3 against 23.6; 4 of up to
-// 131072 in int4: 89.6 with three, 93.3 with two).  A second stage of LDS for each wave
-// was no faster with any of them (107.4 and 94.2): a stage is read into registers at
-// once and filled again, so that two tiles of each wave are under way as it is.
+// 131072 in int4: 89.6 with three, 93.3 with two).  At 256 one block of two stages took 48.3
+// us for 78 sequences of 21 tokens and 19 heads, two of one stage 30.6.  A second stage of
+// LDS for each wave was no faster in the others either (107.4 and 94.2): a stage is read into
+// registers at once and filled again, so that two tiles of each wave are under way as it is.
 constexpr int blocks_on_cu(int DP, int BITS) { return DP == 64 ? 4 : DP == 128 && BITS == 4 ? 3 : 2; }
 
 __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
@@ -750,11 +751,11 @@ constexpr int64_t kMaxShare = 1024;        // blocks that share the work: at mos
 // their longest length (us; a block to each sequence and head, and shared; lengths
 // evenly spread below it; heads of 128, 32 queries, 8 bits):
 //       1000          2000          4000          8000
-//    1  13.4  11.4    21.1  11.9    36.8  13.4    66.2  16.8
-//    8  14.6  14.4    22.5  17.7    37.4  24.3    66.9  31.8
-//   32  15.5  21.9    23.7  28.2    39.8  41.2    71.0  63.7
-//   64  20.8  35.0    33.5  49.9    59.0  70.9     109   111
-//   90  28.8  46.8    42.8  60.3    74.7  90.3     139   145
+//    1  13.1  11.1    20.5  11.6    35.9  12.9    65.1  16.0
+//    8  13.9  14.3    21.6  17.0    36.2  22.9    65.6  30.3
+//   32  14.5  20.9    22.7  27.8    38.8  39.5    69.8  60.5
+//   64  19.5  32.7    32.7  47.3    57.9  66.9     108   108
+//   90  27.2  44.2    41.4  56.4    72.7  85.6     138   140
 // The lengths are not known here, and where one is much longer than the others only the
 // first column grows with it, by 7.5 us for 1000 tokens: the border lies below the
 // point where evenly spread ones are equal.
