@@ -211,6 +211,7 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
     __shared__ __attribute__((aligned(16))) uint8_t smem[4 * SB > RED ? 4 * SB : RED];
     auto swz = [](int r) { return (NCH <= 8 ? r / (8 / (NCH <= 8 ? NCH : 8)) : r) & (NCH - 1); };
     __shared__ float st_m[4][16], st_l[4][16], st_e[4][16], inv_l[16];
+    __shared__ int power[16];
     __shared__ int plan[6];
 
     const int lane = threadIdx.x & 63, wave = wave_id();
@@ -637,15 +638,21 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
             red[(wave * 16 + m16) * (DP / 4 + 1) + VN / 4 * (4 * c4 + e) + i] = v4f{acc[4 * i][e], acc[4 * i + 1][e], acc[4 * i + 2][e], acc[4 * i + 3][e]};
     __syncthreads();
     if (threadIdx.x < 16) {
-        float mg = kLow, lg = 0.0f;
+        float mg = kLow, lg = 0.0f, f[4];
+        int top = -1000;
 #pragma unroll
         for (int w = 0; w < 4; ++w) mg = fmaxf(mg, st_m[w][threadIdx.x]);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const float f = __builtin_amdgcn_exp2f(st_m[w][threadIdx.x] - mg);
-            lg += st_l[w][threadIdx.x] * f;
-            st_e[w][threadIdx.x] = __builtin_ldexpf(f, (int)st_e[w][threadIdx.x] + 10);    // (values' codes came times 2^-10)
+            f[w] = __builtin_amdgcn_exp2f(st_m[w][threadIdx.x] - mg);
+            lg += st_l[w][threadIdx.x] * f[w];
+            if (f[w] > 0.0f) top = max(top, (int)st_e[w][threadIdx.x] + __builtin_amdgcn_frexp_expf(f[w]));
         }
+        // Factors next to the waves' largest, whose power of two comes last: together they may pass fp32 although the
+        // sums, weighted and divided, do not.
+#pragma unroll
+        for (int w = 0; w < 4; ++w) st_e[w][threadIdx.x] = __builtin_ldexpf(f[w], (int)st_e[w][threadIdx.x] - top);
+        power[threadIdx.x] = top + 10;                       // (values' codes came times 2^-10)
         inv_l[threadIdx.x] = lg == 0.0f ? 0.0f : 1.0f / lg;
         if ((int)threadIdx.x < heads_here) {
             const float lse = lg == 0.0f ? -__builtin_inff() : mg + __builtin_log2f(lg);
@@ -661,6 +668,8 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
 #pragma unroll
         for (int w = 1; w < 4; ++w) o += red[(w * 16 + r) * (DP / 4 + 1) + d] * st_e[w][r];
         o *= inv_l[r];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = __builtin_ldexpf(o[j], power[r]);
         if (!whole) *reinterpret_cast<v4f*>(a.part + (slot * 16 + r) * a.D + 4 * d) = o;
         else store_quad(a.out, (row0 + r) * a.D + 4 * d, a.dt, o);
     }
