@@ -734,19 +734,20 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     if (lane == 0) red[4 + wave] = total;
     __syncthreads();
     total = red[4] + red[5] + red[6] + red[7];
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     if (mine) {
+        // Divided weights, at most 1 together: a sum that is divided afterwards may pass fp32 although the parts do not.
         // (a part without a token holds zeros; four requests at a time: 512 parts of one head of 128 in 11 us less, and
         // eight at a time, or four times the threads, no faster or slower where rows are many)
-        s *= wt[grp];
+        s *= wt[grp] * inv;
 #pragma unroll 4
-        for (int i = grp + groups; i < n; i += groups) s += wt[i] * part_at(i);
+        for (int i = grp + groups; i < n; i += groups) s += wt[i] * inv * part_at(i);
     }
     sum[tid] = s;
     __syncthreads();
     if (tid >= L) return;
     for (int i = 1; i < groups; ++i) s += sum[i * L + tid];
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    store_quad(a.out, row * a.D + 4 * tid, a.dt, s * inv);
+    store_quad(a.out, row * a.D + 4 * tid, a.dt, s);
     if (tid == 0 && a.lse) a.lse[row] = total == 0.0f ? -__builtin_inff() : (top + __builtin_log2f(total)) * kLn2;
 }
 

@@ -124,3 +124,13 @@ def test_values_near_the_largest_numbers(bits, dt):
     q = torch.randn(3, 4, 64, device=DEV, generator=g).to(dt)
     got, _ = check(Cached(seqs, bits), q, 0.125, dt)
     assert (got[:, :, 2::4] == 0).all()
+
+
+@pytest.mark.parametrize("n", [1500, 20000])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_values_near_the_largest_numbers_in_parts(bits, n):
+    seqs, g = written([n], 2, 64, bits, torch.float32, seed=1)
+    q = torch.randn(1, 4, 64, device=DEV, generator=g)
+    assert qa.qa_attn_decode_workspace(1, 4, 2, 64, n) > 0
+    got, _ = check(Cached(seqs, bits), q, 0.125)
+    assert (got[:, :, 2::4] == 0).all()
