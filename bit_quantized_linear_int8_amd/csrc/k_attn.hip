@@ -558,7 +558,9 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
             wm = fmaxf(wm, __shfl_xor(wm, 16, QA_WAVE));
             wm = fmaxf(wm, __shfl_xor(wm, 32, QA_WAVE));
             const float down = m - mn;
-            const float en = fmaxf(-120.0f, fmaxf(__builtin_ceilf(ex + down), (float)__builtin_amdgcn_frexp_expf(wm)));
+            // (a tile without weight, whose frexp exponent is 0, raises nothing)
+            const float ew = wm > 0.0f ? (float)__builtin_amdgcn_frexp_expf(wm) : -120.0f;
+            const float en = fmaxf(-120.0f, fmaxf(__builtin_ceilf(ex + down), ew));
             l *= __builtin_amdgcn_exp2f(down);
             const float z = __builtin_ldexpf(__builtin_amdgcn_exp2f(down), (int)fmaxf(ex - en, -300.0f));
 #pragma unroll

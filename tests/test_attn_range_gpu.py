@@ -134,3 +134,31 @@ def test_values_near_the_largest_numbers_in_parts(bits, n):
     assert qa.qa_attn_decode_workspace(1, 4, 2, 64, n) > 0
     got, _ = check(Cached(seqs, bits), q, 0.125)
     assert (got[:, :, 2::4] == 0).all()
+
+
+def two_heads(x0, x1, vs, bits=8, seed=2, D=16):
+    """One key head under two queries that read a channel each: scores x0 and x1 (whole numbers), value scales vs."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    n = len(vs)
+    kc = torch.zeros(n, 1, D, dtype=torch.int64, device=DEV)
+    kc[:, 0, 0], kc[:, 0, 1] = torch.tensor(x0, device=DEV), torch.tensor(x1, device=DEV)
+    q = torch.zeros(1, 2, D, device=DEV)
+    q[0, 0, 0] = q[0, 1, 1] = 1.0
+    return (kc, torch.ones(n, 1, device=DEV), codes(g, n, 1, D, bits=bits), torch.tensor(vs, device=DEV)[:, None]), q
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.float16])
+@pytest.mark.parametrize("order", [24, 27, 60])
+def test_a_tile_far_below_while_another_head_grows(order, dt):
+    """Head 0 sees tokens near its largest, then a tile of each wave without weight, then such tokens again; head 1's
+    largest moves in the tile without weight."""
+    x0 = [0] * 128 + [-120] * 128 + [-(t % 3) for t in range(128)]
+    x1 = [0] * 128 + [40] * 128 + [0] * 128
+    s, q = two_heads(x0, x1, [2.0 ** -order] * 384)
+    check(Cached([s]), q.to(dt), 1.0, exact_queries=True)
+
+
+@pytest.mark.parametrize("order", [10, 27, 60])
+def test_value_scales_of_zero_before_small_ones(order):
+    s, q = two_heads([0] * 256, [1] * 256, [0.0] * 128 + [2.0 ** -order] * 128)
+    check(Cached([s]), q, 1.0, exact_queries=True)
