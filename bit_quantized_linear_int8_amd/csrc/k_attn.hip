@@ -210,7 +210,7 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
     constexpr int RED = 4 * 16 * (DP / 4 + 1) * 16;
     __shared__ __attribute__((aligned(16))) uint8_t smem[4 * SB > RED ? 4 * SB : RED];
     auto swz = [](int r) { return (NCH <= 8 ? r / (8 / (NCH <= 8 ? NCH : 8)) : r) & (NCH - 1); };
-    __shared__ float st_m[4][16], st_l[4][16], st_e[4][16], inv_l[16];
+    __shared__ float st_m[4][16], st_l[4][16], st_e[4][16];
     __shared__ int power[16];
     __shared__ int plan[6];
 
@@ -541,7 +541,8 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
         };
         weigh();
         if (__any(fmaxf(max4(p[0]), max4(p[1])) > 65536.0f || fmaxf(max4(w[0]), max4(w[1])) > 16384.0f)) {
-            // new references from this tile's maxima and the old ones
+            // New references from this tile's maxima and the old ones, whole: the factors are powers of two, and the
+            // exponent of the weights falls by as much as m grows.
             float tm = -__builtin_inff(), wm = 0.0f;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -549,7 +550,7 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
                 for (int e = 0; e < 4; ++e) tm = fmaxf(tm, f[u][e] * fs[u][e]);
             tm = fmaxf(tm, __shfl_xor(tm, 16, QA_WAVE));
             tm = fmaxf(tm, __shfl_xor(tm, 32, QA_WAVE));
-            const float mn = fmaxf(m, tm);
+            const float mn = fmaxf(m, __builtin_ceilf(tm));
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -560,7 +561,7 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
             const float down = m - mn;
             // (a tile without weight, whose frexp exponent is 0, raises nothing)
             const float ew = wm > 0.0f ? (float)__builtin_amdgcn_frexp_expf(wm) : -120.0f;
-            const float en = fmaxf(-120.0f, fmaxf(__builtin_ceilf(ex + down), ew));
+            const float en = fmaxf(-120.0f, fmaxf(ex + down, ew));
             l *= __builtin_amdgcn_exp2f(down);
             const float z = __builtin_ldexpf(__builtin_amdgcn_exp2f(down), (int)fmaxf(ex - en, -300.0f));
 #pragma unroll
@@ -640,22 +641,22 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
             red[(wave * 16 + m16) * (DP / 4 + 1) + VN / 4 * (4 * c4 + e) + i] = v4f{acc[4 * i][e], acc[4 * i + 1][e], acc[4 * i + 2][e], acc[4 * i + 3][e]};
     __syncthreads();
     if (threadIdx.x < 16) {
-        float mg = kLow, lg = 0.0f, f[4];
-        int top = -1000;
+        float mg = kLow, lg = 0.0f, e[4], top = -1000.0f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) mg = fmaxf(mg, st_m[w][threadIdx.x]);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            f[w] = __builtin_amdgcn_exp2f(st_m[w][threadIdx.x] - mg);
-            lg += st_l[w][threadIdx.x] * f[w];
-            if (f[w] > 0.0f) top = max(top, (int)st_e[w][threadIdx.x] + __builtin_amdgcn_frexp_expf(f[w]));
+            const float down = st_m[w][threadIdx.x] - mg;
+            lg += st_l[w][threadIdx.x] * __builtin_amdgcn_exp2f(down);
+            e[w] = st_e[w][threadIdx.x] + down;              // of the wave's sums, 2^e
+            top = fmaxf(top, e[w]);
         }
-        // Factors next to the waves' largest, whose power of two comes last: together they may pass fp32 although the
-        // sums, weighted and divided, do not.
+        // Factors next to the largest, divided; its power of two comes last: together they, or sums that are divided
+        // afterwards, may pass fp32 although the output does not.
+        const float inv = lg == 0.0f ? 0.0f : 1.0f / lg;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) st_e[w][threadIdx.x] = __builtin_ldexpf(f[w], (int)st_e[w][threadIdx.x] - top);
-        power[threadIdx.x] = top + 10;                       // (values' codes came times 2^-10)
-        inv_l[threadIdx.x] = lg == 0.0f ? 0.0f : 1.0f / lg;
+        for (int w = 0; w < 4; ++w) st_e[w][threadIdx.x] = __builtin_amdgcn_exp2f(e[w] - top) * inv;
+        power[threadIdx.x] = (int)top + 10;                  // (values' codes came times 2^-10)
         if ((int)threadIdx.x < heads_here) {
             const float lse = lg == 0.0f ? -__builtin_inff() : mg + __builtin_log2f(lg);
             if (!whole) a.plse[slot * 16 + threadIdx.x] = lse;
@@ -669,7 +670,6 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
         v4f o = red[r * (DP / 4 + 1) + d] * st_e[0][r];
 #pragma unroll
         for (int w = 1; w < 4; ++w) o += red[(w * 16 + r) * (DP / 4 + 1) + d] * st_e[w][r];
-        o *= inv_l[r];
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] = __builtin_ldexpf(o[j], power[r]);
         if (!whole) *reinterpret_cast<v4f*>(a.part + (slot * 16 + r) * a.D + 4 * d) = o;

@@ -162,3 +162,23 @@ def test_a_tile_far_below_while_another_head_grows(order, dt):
 def test_value_scales_of_zero_before_small_ones(order):
     s, q = two_heads([0] * 256, [1] * 256, [0.0] * 128 + [2.0 ** -order] * 128)
     check(Cached([s]), q, 1.0, exact_queries=True)
+
+
+@pytest.mark.parametrize("step", [0.9, 0.3, 1.7])
+def test_references_that_move_by_parts_of_a_binary_order(step):
+    """Head 1's scores move its reference in every tile of a wave and head 0's with it, by `step` binary orders;
+    the values' scales make up for it, so that head 0's first tokens and its last ones weigh the same."""
+    tiles = 60
+    i = torch.arange(128 * tiles, device=DEV) // 128
+    n = 128 * tiles
+    g = torch.Generator(device=DEV).manual_seed(4)
+    kc = torch.zeros(n, 1, 16, dtype=torch.int64, device=DEV)
+    kc[:, 0, 0] = i
+    vs = torch.where(i == 0, 1.0, torch.exp2(-step * (tiles - 1) * torch.ones_like(i, dtype=torch.float32)))
+    s = (kc, torch.ones(n, 1, device=DEV), codes(g, n, 1, 16), vs[:, None])
+    q = torch.zeros(768, 2, 16, device=DEV)
+    q[:, 0, 0], q[:, 1, 0] = 1.0, 64.0
+    c = Cached([s] + [tuple(x[:1] for x in s)] * 767)
+    c.lengths[1:] = 0
+    c.seqs = c.seqs[:1]
+    check(c, q, step * math.log(2.0), exact_queries=True)
