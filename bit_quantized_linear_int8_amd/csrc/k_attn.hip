@@ -29,14 +29,14 @@
 // codes become fp16 (times 2^-10) exactly: the byte or nibble with its sign bit
 // flipped is an fp16 number below the normal ones, and a fused multiply-add
 // scales it and takes the flip away.  p s_v enters as two fp16 numbers with a power
-// of two per head, 2^-22 of the value, so that neither the scales' range nor a
-// softmax over long contexts costs digits: one fp16 number would add an error as
-// large as the rounding of an fp16 output.  Sums are fp32.
+// of two per head: 2^-22 of the value, and 2^-37 of the wave's largest, below which
+// fp16 has no numbers; one fp16 number would add an error as large as the rounding
+// of an fp16 output.  Sums are fp32.
 //
 // The reference m of the exponentials and the power of two of p s_v follow their
-// running maxima lazily: only when a tile passes one by 2^16 (or 2^14) are
-// they taken anew, with the lanes' exchange that this needs; 2^16 leaves the sums
-// far inside fp32's range.
+// running maxima lazily: only when a tile passes one by 2^16 (or fp16's largest
+// number) are they taken anew, with the lanes' exchange that this needs; 2^16 leaves
+// the sums far inside fp32's range.
 //
 // The four waves of a block take tiles in turn and are joined through LDS.  Where
 // there are few sequences and heads for their length, the work of all of them, in units of 128 tokens
@@ -87,6 +87,15 @@ struct AttnArgs {
 
 constexpr float kLow = -3.0e38f;           // the reference before any token
 constexpr float kLn2 = 0.693147180559945309f;
+
+// Weights p s_v times 2^-ex: taken anew, the largest lies in [2^12, 2^13); up to kMostWeight, fp16's largest number,
+// they may grow before that.  Half a step of fp16's smallest numbers is then at most 2^-37 of the largest weight.  (With
+// a largest below 1 the weights of 32768 tokens 17.5 nats below one were lost, 2^-24 being the smallest number.  A
+// largest of 2^13 or more has to be taken anew more often: 64 ragged sequences of up to 8192 in 8 bits take 106.4 us
+// against 105.3, 4 of up to 131072 in 4 bits with fp32 queries 96.3 against 95.0; of 2^11 or more, 105.4 and 94.9.)
+constexpr int kWeightBits = 13;
+constexpr float kMostWeight = 65504.0f;
+constexpr float kLeastExp = -126.0f;       // of 2^-ex in fp32
 
 __device__ __forceinline__ v2h pk(uint32_t u) { return __builtin_bit_cast(v2h, u); }
 __device__ __forceinline__ uint32_t up(v2h h) { return __builtin_bit_cast(uint32_t, h); }
@@ -424,7 +433,7 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
     v4f acc[VN];
 #pragma unroll
     for (int i = 0; i < VN; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = kLow, l = 0.0f, ex = -120.0f, r = 0.0f;        // r = 2^-ex, the factor of p s_v
+    float m = kLow, l = 0.0f, ex = kLeastExp, r = 0.0f;       // r = 2^-ex, the factor of p s_v
 
     // a lane's places in a stage
     uint32_t ak[NS], av[4];
@@ -540,7 +549,7 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
                 }
         };
         weigh();
-        if (__any(fmaxf(max4(p[0]), max4(p[1])) > 65536.0f || fmaxf(max4(w[0]), max4(w[1])) > 16384.0f)) {
+        if (__any(fmaxf(max4(p[0]), max4(p[1])) > 65536.0f || fmaxf(max4(w[0]), max4(w[1])) > kMostWeight)) {
             // New references from this tile's maxima and the old ones, whole: the factors are powers of two, and the
             // exponent of the weights falls by as much as m grows.
             float tm = -__builtin_inff(), wm = 0.0f;
@@ -560,8 +569,8 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
             wm = fmaxf(wm, __shfl_xor(wm, 32, QA_WAVE));
             const float down = m - mn;
             // (a tile without weight, whose frexp exponent is 0, raises nothing)
-            const float ew = wm > 0.0f ? (float)__builtin_amdgcn_frexp_expf(wm) : -120.0f;
-            const float en = fmaxf(-120.0f, fmaxf(ex + down, ew));
+            const float ew = wm > 0.0f ? (float)(__builtin_amdgcn_frexp_expf(wm) - kWeightBits) : kLeastExp;
+            const float en = fmaxf(kLeastExp, fmaxf(ex + down, ew));
             l *= __builtin_amdgcn_exp2f(down);
             const float z = __builtin_ldexpf(__builtin_amdgcn_exp2f(down), (int)fmaxf(ex - en, -300.0f));
 #pragma unroll

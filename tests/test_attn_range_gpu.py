@@ -4,8 +4,8 @@ against softmax attention in 64 bits on the values that the codes stand for.
 Tolerance of an output, before any run: with u = 2^-24, X the largest score's magnitude and n the tokens,
   scores: exact sums of the codes and the queries' whole numbers, 2^-30 (fp32 queries) or 2^-22 of the head's largest
   query times sum |k|; the factors, the sums' two halves and the difference from the reference are 10 roundings of X;
-  weights: exp2, p s_v and its two fp16 numbers, 2^-21 of each, and 2^-38 of the largest weight (half a step of the
-  smallest fp16 numbers, 2^-25, beside a largest of 2^13 or more) times the codes;
+  weights: exp2, p s_v and its two fp16 numbers, 2^-21 of each, and 2^-37 of the largest weight (half a step of the
+  smallest fp16 numbers, 2^-25, beside a largest of 2^12 or more) times the codes;
   sums: n / 32 + 64 additions in a row at most, u each, of A = sum_t p_t |v_t|, in the numerator and the denominator;
   and half a step of the output's type."""
 import math
@@ -75,7 +75,7 @@ def check(c, q, scale, dt=torch.float32, exact_queries=False, **kw):
             want, A = p @ v, p @ v.abs()
             X = float(x.abs().max())
             off = part * float(Q.abs().max()) * float(k.abs().sum(1).max()) * abs(scale) + 10 * U * X
-            least = 2.0 ** -38 * float((p * vs[:, g].abs()).max()) * vc[:, g].abs().sum(0)
+            least = 2.0 ** -37 * float((p * vs[:, g].abs()).max()) * vc[:, g].abs().sum(0)
             tol = (2 * off + 2 * (n / 32 + 64) * U + 2.0 ** -21) * A + least + torch.finfo(dt).eps / 2 * want.abs()
             err = (got[b, h].double() - want).abs()
             assert (err <= tol).all(), (b, h, float((err / tol.clamp(min=1e-300)).max()))
@@ -161,6 +161,40 @@ def test_a_tile_far_below_while_another_head_grows(order, dt):
 @pytest.mark.parametrize("order", [10, 27, 60])
 def test_value_scales_of_zero_before_small_ones(order):
     s, q = two_heads([0] * 256, [1] * 256, [0.0] * 128 + [2.0 ** -order] * 128)
+    check(Cached([s]), q, 1.0, exact_queries=True)
+
+
+def first_far_above(n, nats, bits=8, D=16, seed=3):
+    """A first token whose score is `nats` above the equal ones of n - 1 others; its values leave every other channel."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    kc = torch.zeros(n, 1, D, dtype=torch.int64, device=DEV)
+    kc[0, 0, 0] = 7
+    ks = torch.full((n, 1), nats / 7.0, device=DEV)
+    vc = codes(g, n, 1, D, bits=bits).abs()
+    vc[0, 0, ::2] = 0
+    q = torch.zeros(1, 1, D, device=DEV)
+    q[0, 0, 0] = 1.0
+    return (kc, ks, vc, torch.rand(n, 1, device=DEV, generator=g) + 0.5), q
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("nats", [10.0, 14.0, 17.5, 20.0])
+def test_many_small_weights_beside_one(nats, bits):
+    """One block takes the whole sequence, as with many sequences: where the first token's values are 0, the sum of the
+    others is the output."""
+    s, q = first_far_above(32768, nats, bits)
+    short = tuple(x[:1] for x in s)
+    c = Cached([s] + [short] * 767, bits)
+    c.lengths[1:] = 0
+    c.seqs = c.seqs[:1]
+    assert qa.qa_attn_decode_workspace(768, 1, 1, 16, 32768) == 0
+    q = q.expand(768, 1, 16).contiguous()
+    check(c, q, 1.0, exact_queries=True)
+
+
+@pytest.mark.parametrize("nats", [10.0, 17.5])
+def test_many_small_weights_beside_one_in_parts(nats):
+    s, q = first_far_above(32768, nats)
     check(Cached([s]), q, 1.0, exact_queries=True)
 
 
