@@ -198,6 +198,10 @@ constexpr int vmcnt_only(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >
 constexpr int blocks_on_cu(int DP, int BITS) { return DP == 64 ? 4 : DP == 128 && BITS == 4 ? 3 : 2; }
 
 __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
+// Of magnitudes: weights have the sign of their value scale.
+__device__ __forceinline__ float most4(v4f v) {
+    return fmaxf(fmaxf(__builtin_fabsf(v[0]), __builtin_fabsf(v[1])), fmaxf(__builtin_fabsf(v[2]), __builtin_fabsf(v[3])));
+}
 
 }  // namespace
 
@@ -549,7 +553,7 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
                 }
         };
         weigh();
-        if (__any(fmaxf(max4(p[0]), max4(p[1])) > 65536.0f || fmaxf(max4(w[0]), max4(w[1])) > kMostWeight)) {
+        if (__any(fmaxf(max4(p[0]), max4(p[1])) > 65536.0f || fmaxf(most4(w[0]), most4(w[1])) > kMostWeight)) {
             // New references from this tile's maxima and the old ones, whole: the factors are powers of two, and the
             // exponent of the weights falls by as much as m grows.
             float tm = -__builtin_inff(), wm = 0.0f;
@@ -564,7 +568,7 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    wm = fmaxf(wm, __builtin_amdgcn_exp2f(__builtin_fmaf(f[u][e], fs[u][e], -mn)) * sv[u][e]);
+                    wm = fmaxf(wm, __builtin_fabsf(__builtin_amdgcn_exp2f(__builtin_fmaf(f[u][e], fs[u][e], -mn)) * sv[u][e]));
             wm = fmaxf(wm, __shfl_xor(wm, 16, QA_WAVE));
             wm = fmaxf(wm, __shfl_xor(wm, 32, QA_WAVE));
             const float down = m - mn;

@@ -216,3 +216,15 @@ def test_references_that_move_by_parts_of_a_binary_order(step):
     c.lengths[1:] = 0
     c.seqs = c.seqs[:1]
     check(c, q, step * math.log(2.0), exact_queries=True)
+
+
+@pytest.mark.parametrize("n", [400, 5000])
+def test_value_scales_below_zero(n):
+    """A filled cache may hold them: weights of either sign, larger and larger."""
+    g = torch.Generator(device=DEV).manual_seed(6)
+    sign = torch.randint(0, 2, (n, 2), device=DEV, generator=g) * 2.0 - 1.0
+    for s in (sign, -torch.ones_like(sign)):
+        vs = s * torch.exp2(torch.arange(n, device=DEV)[:, None] * (60.0 / n) - 20.0)
+        x = (codes(g, n, 2, 64), torch.rand(n, 2, device=DEV, generator=g) / 100, codes(g, n, 2, 64), vs)
+        q = torch.randn(1, 4, 64, device=DEV, generator=g)
+        check(Cached([x]), q, 0.125)
