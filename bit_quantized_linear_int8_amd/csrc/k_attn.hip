@@ -22,10 +22,15 @@
 // registers have every lane of a load in a line of its own: 460 accesses of the L1
 // for a tile's 68 lines, which bounded the kernel at 4.4 TB/s.)
 //
-// Queries enter as whole numbers of 22 bits and a sign next to the head's largest
-// (what fp16 and bf16 hold of values down to 2^-11 and 2^-14 of it), in three
-// balanced digits of base 256, so that the scores of integers are exact: three
-// int8 products cost less than to convert every key's codes to fp16.  Values'
+// Queries enter as whole numbers next to the head's largest, in balanced digits of
+// base 256, so that the scores of integers are exact: an int8 product for each digit
+// costs less than to convert every key's codes to fp16.  fp32 queries have 30 bits and a
+// sign, four digits: what is left out, 2^-30 of the largest times sum |k|, is below the
+// roundings of fp32 sums of their products.  fp16 and bf16 ones have 22 and a sign, three
+// digits: values down to 2^-11 and 2^-14 of the largest are as they were, smaller
+// ones within 2^-22 of it, 2^10 times less than the half step that the largest itself
+// came with.  (A fourth digit for them: 64 ragged sequences of up to 8192 105.1 -> 106.5 us,
+// with heads of 256 114 -> 124, windows of 1000 over 32 heads of 64 25.5 -> 28.2.)  Values'
 // codes become fp16 (times 2^-10) exactly: the byte or nibble with its sign bit
 // flipped is an fp16 number below the normal ones, and a fused multiply-add
 // scales it and takes the flip away.  p s_v enters as two fp16 numbers with a power
@@ -188,14 +193,16 @@ __device__ __forceinline__ void load_lds4(const void* p, void* lds) {
 // s_waitcnt immediate waiting for vmcnt <= n only (gfx9 encoding)
 constexpr int vmcnt_only(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 
-// Blocks on a CU, by D rounded up: as many as the registers hold, but for 128 in int8,
+// Blocks on a CU, by D rounded up: as many as the registers hold in the loop over tiles (what they do not hold beside it,
+// for heads of 256 in int8 and with fp32 queries, and of 128 in int4 with them, is put aside before
+// the loop and taken up after it; heads of 64 with fp32 queries would spill into it with four), but for 128 in int8,
 // where two bring long sequences in faster than three (64 ragged ones up to 8192:
 // 105.6 us of the call against 113; 200 of up to 200 tokens 27.3 against 23.6; 4 of up to
 // 131072 in int4: 89.6 with three, 93.3 with two).  At 256 one block of two stages took 48.3
 // us for 78 sequences of 21 tokens and 19 heads, two of one stage 30.6.  A second stage of
 // LDS for each wave was no faster in the others either (107.4 and 94.2): a stage is read into
 // registers at once and filled again, so that two tiles of each wave are under way as it is.
-constexpr int blocks_on_cu(int DP, int BITS) { return DP == 64 ? 4 : DP == 128 && BITS == 4 ? 3 : 2; }
+constexpr int blocks_on_cu(int DP, int BITS, bool F32) { return DP == 64 ? (F32 ? 3 : 4) : DP == 128 && BITS == 4 ? 3 : 2; }
 
 __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
 // Of magnitudes: weights have the sign of their value scale.
@@ -208,11 +215,12 @@ __device__ __forceinline__ float most4(v4f v) {
 // DP: D rounded up to 64, 128 or 256 (what lies behind D meets queries of 0, or is
 // not stored).  F32: fp32 queries.
 template <int BITS, int DP, bool F32>
-__global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(AttnArgs a) {
+__global__ __launch_bounds__(256, blocks_on_cu(DP, BITS, F32)) void k_attn_decode(AttnArgs a) {
     constexpr int CC = BITS == 8 || DP == 64 ? 16 : 32;      // codes of a lane's piece of a key
     constexpr int NS = DP / (4 * CC);                        // pieces of a lane
     constexpr int PB = CC * BITS / 8;                        // bytes of a piece
     constexpr int NM = DP / 64;                              // MFMA steps of a key
+    constexpr int ND = F32 ? 4 : 3, QB = F32 ? 30 : 22;      // a query's digits, and its bits
     constexpr int VN = DP / 16;                              // values of a lane per token
     constexpr int VB = VN * BITS / 8;                        // their bytes
     constexpr int VW = VB < 4 ? 1 : VB / 4;                  // their words
@@ -368,7 +376,7 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
     int ent = entries(t0), ent2 = entries(t0 + 32 * 128);
     int p0 = page_of(t0, __builtin_amdgcn_readlane(ent, 0)), p1 = page_of(t0 + 16, __builtin_amdgcn_readlane(ent, 1));
     fill(t0, p0, p1);
-    v4i qd[3][NM];                                           // digits of 1, 256, 65536
+    v4i qd[ND][NM];                                          // digits of 1, 256, 65536, 2^24
     float qscale;
     {
         constexpr uint32_t EL = F32 ? 4 : 2;                 // bytes of a query value
@@ -404,18 +412,20 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
             for (int k = 0; k < CC; ++k) bits = max(bits, __builtin_bit_cast(uint32_t, x[s][k]) & 0x7fffffffu);
         bits = max(bits, (uint32_t)__shfl_xor((int)bits, 16, QA_WAVE));
         bits = max(bits, (uint32_t)__shfl_xor((int)bits, 32, QA_WAVE));
-        // times 2^e the head's largest is in [2^21, 2^22)
+        // times 2^e the head's largest is in [2^(QB - 1), 2^QB)
         const bool fine = bits < 0x7f800000u;
-        const int e = bits != 0 && fine ? 22 - __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, bits)) : 0;
+        const int e = bits != 0 && fine ? QB - __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, bits)) : 0;
+        // (of queries below 2^-89 in all qscale is subnormal and loses digits; scores show them beside key scales above 2^60)
         qscale = fine ? __builtin_ldexpf(a.scale2, -e - (BITS == 8 ? 0 : 4)) : __builtin_nanf("");
         const float f1 = __builtin_ldexpf(1.0f, e / 2), f2 = __builtin_ldexpf(1.0f, e - e / 2);
 #pragma unroll
         for (int i = 0; i < NM; ++i)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                // Beside 3 2^22 the whole number is in the low bits of the sum; a digit is a byte of it, or of
-                // it with what carries into the next digit: n, n + 128, n + 128 + 2^15.
-                uint32_t n[4], n1[4], n2[4];
+                // A digit is a byte of the whole number, or of it with what carries into the next digit: n,
+                // n + 128, n + 128 + 2^15, n + 128 + 2^15 + 2^23.  (22 bits: beside 3 2^22 the number is in the
+                // low bits of the sum.)
+                uint32_t n[4], n1[4], n2[4], n3[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     // value at byte k of step i
@@ -424,13 +434,16 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
                     if constexpr (BITS == 8) y = x[i][k];
                     else if constexpr (CC == 32) y = x[i / 2][2 * k + (i & 1)];
                     else y = x[i][k < 8 ? 2 * k : 2 * (k - 8) + 1];
-                    n[j] = __builtin_bit_cast(uint32_t, __builtin_fmaf(y * f1, f2, 12582912.0f));
-                    n1[j] = n[j] + (128u - 0x4b400000u);
+                    if constexpr (ND == 4) n[j] = (uint32_t)(int)__builtin_rintf(y * f1 * f2);
+                    else n[j] = __builtin_bit_cast(uint32_t, __builtin_fmaf(y * f1, f2, 12582912.0f));
+                    n1[j] = n[j] + (ND == 4 ? 128u : 128u - 0x4b400000u);
                     n2[j] = n1[j] + 0x8000u;
+                    n3[j] = n2[j] + 0x800000u;
                 }
                 qd[0][i][w] = (int)bytes4<0>(n);
                 qd[1][i][w] = (int)bytes4<1>(n1);
                 qd[2][i][w] = (int)bytes4<2>(n2);
+                if constexpr (ND == 4) qd[3][i][w] = (int)bytes4<3>(n3);
             }
     }
 
@@ -505,26 +518,34 @@ __global__ __launch_bounds__(256, blocks_on_cu(DP, BITS)) void k_attn_decode(Att
         v4f f[2], fs[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            v4i s0 = v4i{0, 0, 0, 0}, s1 = s0, s2 = s0;
+            v4i kf[NM];
 #pragma unroll
             for (int i = 0; i < NM; ++i) {
-                v4i kf;
-                if constexpr (BITS == 8) kf = __builtin_bit_cast(v4i, kq[u][i]);
+                if constexpr (BITS == 8) kf[i] = __builtin_bit_cast(v4i, kq[u][i]);
                 else if constexpr (CC == 32) {
                     const u32x4 w = kq[u][i / 2];
-                    kf = __builtin_bit_cast(v4i, (i & 1 ? w : w << 4) & 0xf0f0f0f0u);
+                    kf[i] = __builtin_bit_cast(v4i, (i & 1 ? w : w << 4) & 0xf0f0f0f0u);
                 } else {
                     const u32x4 w = kq[u][i];
-                    kf = __builtin_bit_cast(v4i, u32x4{w[0] << 4, w[1] << 4, w[0], w[1]} & 0xf0f0f0f0u);
+                    kf[i] = __builtin_bit_cast(v4i, u32x4{w[0] << 4, w[1] << 4, w[0], w[1]} & 0xf0f0f0f0u);
                 }
-                s0 = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf, qd[0][i], s0, 0, 0, 0);
-                s1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf, qd[1][i], s1, 0, 0, 0);
-                s2 = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf, qd[2][i], s2, 0, 0, 0);
             }
+            // Two digits to a sum, the upper one's products times 256 under the lower one's: |s| <= 256 * 128 * 128 of a
+            // digit, and the uppermost is at most 65: both sums fit.  (Sums of their own for each digit take
+            // registers: heads of 64 with fp32 queries, windows of 1000, 33.0 us against 29.3.)
+            v4i low = v4i{0, 0, 0, 0}, high = low;
+            auto add = [&](int d, v4i s) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < NM; ++i) s = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[i], qd[d][i], s, 0, 0, 0);
+                return s;
+            };
+            low = add(1, low);
+            high = add(ND - 1, high);
+            low = add(0, low << 8);
+            if constexpr (ND == 4) high = add(2, high << 8);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                // |s1| <= 256 * 128 * 127: 256 s1 + s0 fits
-                f[u][e] = __builtin_fmaf((float)s2[e], 65536.0f, (float)(s1[e] * 256 + s0[e]));
+                f[u][e] = __builtin_fmaf((float)high[e], 65536.0f, (float)low[e]);
                 fs[u][e] = ks[u][e] * qscale;
             }
         }
@@ -829,7 +850,7 @@ hipError_t launch_attn_decode(const void* q, int64_t ldq, int q_dtype, int64_t B
     a.out = out; a.dt = out_dtype; a.lse = lse;
     const bool shared = shared_work(B, H, c.heads, max_len, window);
     if (shared) {
-        const int64_t fit = 256 * blocks_on_cu(c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256, c.bits), HG = (int64_t)c.heads * a.gtiles;
+        const int64_t fit = 256 * blocks_on_cu(c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256, c.bits, q_dtype == 0), HG = (int64_t)c.heads * a.gtiles;
         a.share = (int32_t)(fit > HG ? fit / HG : 1);
         const int64_t slots = (a.share + B) * HG;
         a.part = static_cast<float*>(scratch);

@@ -774,10 +774,13 @@ qa_status qa_kv_read(const int64_t* slots, int64_t T, int32_t bits, int64_t page
  *   out[b][h][d] = sum_t exp(x_t) v_t[d] / sum_t exp(x_t)
  *   lse[b][h] = log sum_t exp(x_t)
  * A sequence without a token to see (length 0, every page masked) gets a row of
- * zeros and lse = -infinity.  Scales and sums are fp32; scores and weights keep
- * about 2^-21 of their head's largest, and the output is rounded once.  A NaN
+ * zeros and lse = -infinity.  Scores are off by a few roundings of fp32 and by
+ * what the queries are rounded to, 2^-30 (fp32) or 2^-22 (fp16, bf16) of the
+ * head's largest; weights by 2^-21 of themselves and 2^-37 of the largest; sums
+ * are fp32, and the output is rounded once.  Scales may have either sign.  A NaN
  * scale among the tokens that are seen, or an infinity or NaN in the query, makes
- * the head's outputs NaN.
+ * the head's outputs NaN; infinite scales and scores past fp32 give infinities or
+ * NaNs.
  *   q        [B x H x D] of q_dtype (fp32, fp16 or bf16), token stride ldq
  *            elements
  *   table    i32 [B x width], row stride ldt: the pages of each sequence.  Entries
