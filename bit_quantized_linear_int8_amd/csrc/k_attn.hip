@@ -51,11 +51,11 @@
 // blocks of unequal size: half the card's waves were idle with ragged lengths.)
 //
 // What bounds it: 64 ragged sequences of up to 8192 (8 key heads of 128, 4 queries each,
-// 8 bits, 580 MB) take 97 to 103 us, 5.6 to 6.0 TB/s, and 7 the join: the memory (the loads alone take
-// no less).  4 of up to 131072 in 4 bits with 8 queries each take 82 to 91, 5.0 to 5.5 TB/s:
-// the loads alone and the arithmetic alone (vector instructions busy for 61% of
-// the time, most of them values' codes made fp16) are 85 each.  A single sequence of 4096 is
-// latency: 8.0 and 3.9 for the join.  Many short ones, where no block shares, are their
+// 8 bits, 580 MB) take 98 to 103 us, 5.6 to 5.9 TB/s, and 7 the join: the memory (the loads alone take
+// no less).  4 of up to 131072 in 4 bits with 8 queries each take 86 to 92, 4.9 to 5.3 TB/s:
+// the loads alone and the arithmetic alone (vector instructions busy for 62% of
+// the time, most of them values' codes made fp16) are about 85 each.  A single sequence of 4096 is
+// latency: 8.2 to 9.2 and 4.3 to 4.8 for the join.  Many short ones, where no block shares, are their
 // bytes and 7 us of dependent loads (length, table, codes) at the beginning and the joint of
 // the waves at the end.
 #include "qa_device.hpp"
@@ -804,7 +804,11 @@ constexpr int64_t kMaxShare = 1024;        // blocks that share the work: at mos
 //   90  27.2  44.2    41.4  56.4    72.7  85.6     138   140
 // The lengths are not known here, and where one is much longer than the others only the
 // first column grows with it, by 7.5 us for 1000 tokens: the border lies below the
-// point where evenly spread ones are equal.
+// point where evenly spread ones are equal.  From 768 pairs of a sequence and a key head on
+// nothing is shared.  Evenly long sequences take the same there either way (96 of 8000 tokens
+// 263 us and 263), but one of 100000 tokens beside 95 of 1000 takes 742 us by itself, 74 if
+// the blocks shared it (beside 94, where they do, 76).  The table is for heads of 128 in
+// 8 bits; head size, bits and blocks on a CU do not enter the rule.
 bool shared_work(int64_t B, int32_t H, int32_t heads, int64_t max_len, int32_t window) {
     const int64_t group = H / heads, pairs = B * heads * ((group + 15) / 16);
     const int64_t span = window > 0 && (int64_t)window + 31 < max_len ? (int64_t)window + 31 : max_len;

@@ -210,7 +210,9 @@ __device__ __forceinline__ v4f cols4(const float* p, int64_t c, int n, bool vec)
 //            1 x 128000    95.8   89.3    128      16 x 128000    103    149    129
 //   K 11008  1 x 8192      18.3   21.0   33.1      16 x 8192     23.3   27.5   33.1
 //            1 x 16384     38.6   44.7   46.2      16 x 16384    48.3   59.6   46.8
-// (5.1 TB/s at 16 x 128000.)  32 tokens in two operands are no faster than tiles from
+// (5.1 TB/s at 16 x 128000.)  The border to the form above goes by columns alone: a
+// single token whose K is one part would be 7 to 10% faster there, 16 tokens, and one with
+// K of several parts, are slower.  32 tokens in two operands are no faster than tiles from
 // 8192 columns on (13.0 and 13.2), 64 slower (their codes' traffic passes the weights').
 // ---------------------------------------------------------------------------
 template <bool RES16>
