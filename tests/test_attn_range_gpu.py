@@ -148,7 +148,7 @@ def two_heads(x0, x1, vs, bits=8, seed=2, D=16):
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.float16])
-@pytest.mark.parametrize("order", [24, 27, 60])
+@pytest.mark.parametrize("order", [24, 27, 60, 110])
 def test_a_tile_far_below_while_another_head_grows(order, dt):
     """Head 0 sees tokens near its largest, then a tile of each wave without weight, then such tokens again; head 1's
     largest moves in the tile without weight."""
@@ -158,7 +158,7 @@ def test_a_tile_far_below_while_another_head_grows(order, dt):
     check(Cached([s]), q.to(dt), 1.0, exact_queries=True)
 
 
-@pytest.mark.parametrize("order", [10, 27, 60])
+@pytest.mark.parametrize("order", [10, 27, 60, 110])
 def test_value_scales_of_zero_before_small_ones(order):
     s, q = two_heads([0] * 256, [1] * 256, [0.0] * 128 + [2.0 ** -order] * 128)
     check(Cached([s]), q, 1.0, exact_queries=True)
