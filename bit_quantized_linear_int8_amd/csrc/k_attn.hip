@@ -195,9 +195,9 @@ constexpr int vmcnt_only(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >
 
 // Blocks on a CU, by D rounded up: as many as the registers hold in the loop over tiles (what they do not hold beside it,
 // for heads of 256 in int8 and with fp32 queries, and of 128 in int4 with them, is put aside before
-// the loop and taken up after it; heads of 64 with fp32 queries would spill into it with four), but for 128 in int8,
-// where two bring long sequences in faster than three (64 ragged ones up to 8192:
-// 105.6 us of the call against 113; 200 of up to 200 tokens 27.3 against 23.6; 4 of up to
+// the loop and taken up after it), but for 64 with fp32 queries (33 windows of 1000 over 32 heads: 29.3 us of the call
+// with three, 29.8 with four) and for 128 in int8, where two bring long sequences in faster than three (64
+// ragged ones up to 8192: 105.6 us against 113; 200 of up to 200 tokens 27.3 against 23.6; 4 of up to
 // 131072 in int4: 89.6 with three, 93.3 with two).  At 256 one block of two stages took 48.3
 // us for 78 sequences of 21 tokens and 19 heads, two of one stage 30.6.  A second stage of
 // LDS for each wave was no faster in the others either (107.4 and 94.2): a stage is read into

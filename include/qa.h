@@ -776,11 +776,11 @@ qa_status qa_kv_read(const int64_t* slots, int64_t T, int32_t bits, int64_t page
  * A sequence without a token to see (length 0, every page masked) gets a row of
  * zeros and lse = -infinity.  Scores are off by a few roundings of fp32 and by
  * what the queries are rounded to, 2^-30 (fp32) or 2^-22 (fp16, bf16) of the
- * head's largest; weights by 2^-21 of themselves and 2^-37 of the largest; sums
- * are fp32, and the output is rounded once.  Scales may have either sign.  A NaN
- * scale among the tokens that are seen, or an infinity or NaN in the query, makes
- * the head's outputs NaN; infinite scales and scores past fp32 give infinities or
- * NaNs.
+ * head's largest; weights by 2^-21 of themselves and 2^-37 of the largest, and
+ * exp(x_t) below 2^-126 of the largest may count as 0; sums are fp32, and the
+ * output is rounded once.  Scales may have either sign.  A NaN scale among the
+ * tokens that are seen, or an infinity or NaN in the query, makes the head's
+ * outputs NaN; infinite scales and scores past fp32 give infinities or NaNs.
  *   q        [B x H x D] of q_dtype (fp32, fp16 or bf16), token stride ldq
  *            elements
  *   table    i32 [B x width], row stride ldt: the pages of each sequence.  Entries
